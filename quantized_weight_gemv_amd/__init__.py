@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -74,6 +75,22 @@ def lib() -> ctypes.CDLL:
         "qgemm_q4_0_prefill": (c_int, [vp, vp, vp, i64, i64, i64, vp]),
         "qdequant_q4_0": (c_int, [vp, i64, i64, c_int, vp, vp]),
         "qdequant_q8_0": (c_int, [vp, i64, i64, c_int, vp, vp]),
+        "qpacked_bytes_f8": (sz, [i64, i64]),
+        "qact_bytes_f8": (sz, [i64, i64]),
+        "qquantize_f8": (c_int, [vp, i64, i64, vp, sz]),
+        "qdequant_f8": (c_int, [vp, i64, i64, c_int, vp, vp]),
+        "qtranspose_f8": (c_int, [vp, i64, i64, vp, vp]),
+        "qact_quantize_f8": (c_int, [vp, c_int, i64, i64, i64, vp, vp]),
+        "qact_dequant_f8": (c_int, [vp, i64, i64, c_int, vp, vp]),
+        "qgemv_f8": (c_int, [vp, vp, c_int, vp, c_int, i64, i64, vp]),
+        "qgemm_f8": (c_int, [vp, vp, vp, c_int, i64, i64, i64, vp]),
+        "qgemm_f8_wgrad_workspace": (sz, [i64, i64, i64]),
+        "qgemm_f8_wgrad": (c_int, [vp, vp, vp, c_int, i64, i64, i64, vp, vp]),
+        "qmoe_route_workspace": (sz, [i64, i64]),
+        "qmoe_route": (c_int, [vp, c_int, i64, vp, i64, i64, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "qmoe_route_backward": (c_int, [vp, c_int, i64, vp, i64, i64, c_int, c_int, vp, vp, vp, vp, vp, vp, vp]),
+        "qmoe_gemm_f8": (c_int, [vp, i64, vp, i64, c_int, vp, vp, vp, c_int, i64, i64, vp]),
+        "qmoe_gemm_f8_wgrad": (c_int, [vp, vp, i64, c_int, vp, vp, i64, vp, c_int, i64, i64, vp]),
         "qg_time_next_launch": (None, [vp, vp]),
         "qg_device_cus": (c_int, [c_int, ctypes.POINTER(c_int)]),
         "qg_set_gemv_shape": (None, [c_int, c_int, c_int, c_int, i64, c_int, c_int, c_int]),
@@ -94,6 +111,9 @@ def exported_symbols() -> list[str]:
             "qmoe_gemv_q4_0",
             "qgemm_q4_0_prefill", "qdequant_q4_0",
             "qdequant_q8_0", "qpacked_bytes_q2w", "qquantize_q2w", "qgemv_q2w", "qgemv_q2w_q8act", "qgemv_q2w_lut", "qdequant_q2w",
+            "qpacked_bytes_f8", "qact_bytes_f8", "qquantize_f8", "qdequant_f8", "qtranspose_f8", "qact_quantize_f8",
+            "qact_dequant_f8", "qgemv_f8", "qgemm_f8", "qgemm_f8_wgrad_workspace", "qgemm_f8_wgrad",
+            "qmoe_route_workspace", "qmoe_route", "qmoe_route_backward", "qmoe_gemm_f8", "qmoe_gemm_f8_wgrad",
             "qg_time_next_launch", "qg_device_cus", "qg_set_gemv_shape", "qg_read_probe", "qg_set_prefill_shape"]
 
 
@@ -338,6 +358,293 @@ def qdequant_q8_0(Wp, N: int, K: int, fp16: bool = False, out=None):
 
 def qdequant_q2w(Wp, N: int, K: int, fp16: bool = False, out=None):
     return _dequant("qdequant_q2w", Q2W, Wp, N, K, fp16, out)
+
+
+# ------------------------------------------------------------------------- f8
+def qpacked_bytes_f8(N: int, K: int) -> int:
+    """Bytes of one packed N x K f8 matrix (0 where the sizes are out of range)."""
+    return int(lib().qpacked_bytes_f8(N, K))
+
+
+def qact_bytes_f8(M: int, K: int) -> int:
+    """Bytes of M x K packed f8 activations (0 where the sizes are out of range)."""
+    return int(lib().qact_bytes_f8(M, K))
+
+
+def qquantize_f8(w: np.ndarray, out: np.ndarray | None = None) -> np.ndarray:
+    """Quantize + pack fp32 [N][K] host weights into the f8 layout (host bytes)."""
+    w = np.ascontiguousarray(w, dtype=np.float32)
+    if w.ndim != 2:
+        raise ValueError("weights must be [N][K]")
+    N, K = w.shape
+    nb = qpacked_bytes_f8(N, K)
+    if nb == 0:
+        raise QGError("qquantize_f8", 2)
+    if out is None:
+        out = np.empty(nb, np.uint8)
+    if out.dtype != np.uint8 or not out.flags["C_CONTIGUOUS"] or out.size < nb:
+        raise ValueError("out must be a contiguous uint8 array of at least the packed size")
+    _check("qquantize_f8", lib().qquantize_f8(w.ctypes.data, N, K, out.ctypes.data, out.size))
+    return out
+
+
+def _type(dtype) -> int:
+    """QG_F32 / QG_F16 / QG_BF16 of a torch dtype."""
+    torch = _torch()
+    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    return code
+
+
+class _Call:
+    """One call's device: every tensor has to be on it, and the call is made
+    with it as the current device, on its current stream."""
+
+    def __init__(self, first, name: str):
+        torch = _torch()
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise TypeError(f"{name} must be a device tensor")
+        self.device = first.device
+
+    def ptr(self, t, dtype, name: str, numel: int, optional: bool = False):
+        torch = _torch()
+        if t is None and optional:
+            return None
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a device tensor")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {self.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.numel() < numel:
+            raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
+        return t.data_ptr()
+
+    def new(self, shape, dtype):
+        return _torch().empty(shape, dtype=dtype, device=self.device)
+
+    def out(self, t, shape, dtype, name: str):
+        """The caller's output of this shape, or a new one."""
+        if t is None:
+            return self.new(shape, dtype)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        return t
+
+    def __call__(self, fn: str, *args):
+        torch = _torch()
+        f = getattr(lib(), fn)
+        if self.device.index == torch.cuda.current_device():
+            st = f(*args, torch.cuda.current_stream().cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = f(*args, torch.cuda.current_stream().cuda_stream)
+        if st:
+            raise QGError(fn, st)
+
+
+def _sizes(fn: str, *nbytes: int):
+    if 0 in nbytes:
+        raise QGError(fn, 2)
+
+
+def qdequant_f8(Wp, N: int, K: int, fp16: bool = False, out=None):
+    """The values of a packed f8 matrix, [N][K] in fp32 or fp16."""
+    torch = _torch()
+    c, nb = _Call(Wp, "Wp"), qpacked_bytes_f8(N, K)
+    _sizes("qdequant_f8", nb)
+    dt = torch.float16 if fp16 else torch.float32
+    out = c.out(out, (N, K), dt, "out")
+    c("qdequant_f8", c.ptr(Wp, torch.uint8, "Wp", nb), N, K, int(fp16), c.ptr(out, dt, "out", N * K))
+    return out
+
+
+def qtranspose_f8(Wp, N: int, K: int, out=None):
+    """The packed N x K matrix as the packed K x N matrix (exact), the operand of dx = f8(dy) W."""
+    torch = _torch()
+    c, nb, nt = _Call(Wp, "Wp"), qpacked_bytes_f8(N, K), qpacked_bytes_f8(K, N)
+    _sizes("qtranspose_f8", nb, nt)
+    if out is None:
+        out = c.new((nt,), torch.uint8)
+    c("qtranspose_f8", c.ptr(Wp, torch.uint8, "Wp", nb), N, K, c.ptr(out, torch.uint8, "out", nt))
+    return out
+
+
+def qact_quantize_f8(x, out=None):
+    """x[M][K] (fp32, fp16 or bf16; rows may be strided) -> packed f8 activations (uint8)."""
+    torch = _torch()
+    c = _Call(x, "x")
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [M][K] with contiguous rows")
+    M, K = x.shape
+    ld = x.stride(0) if M > 1 else K
+    nb = qact_bytes_f8(M, K)
+    _sizes("qact_quantize_f8", nb)
+    if out is None:
+        out = c.new((nb,), torch.uint8)
+    c("qact_quantize_f8", x.data_ptr(), _type(x.dtype), ld, M, K, c.ptr(out, torch.uint8, "out", nb))
+    return out
+
+
+def qact_dequant_f8(xq, M: int, K: int, dtype=None, out=None):
+    """The values of packed f8 activations, [M][K] (fp32 by default)."""
+    torch = _torch()
+    c, nb = _Call(xq, "xq"), qact_bytes_f8(M, K)
+    _sizes("qact_dequant_f8", nb)
+    dtype = dtype or (torch.float32 if out is None else out.dtype)
+    code = _type(dtype)
+    out = c.out(out, (M, K), dtype, "out")
+    c("qact_dequant_f8", c.ptr(xq, torch.uint8, "xq", nb), M, K, code, c.ptr(out, dtype, "out", M * K))
+    return out
+
+
+def qgemv_f8(Wp, x, N: int, K: int, y=None):
+    """y[M][N] (fp32) = f8(x)[M][K] @ W^T, 1 <= M <= 8: x (fp32, fp16 or bf16) is quantized inside the launch."""
+    torch = _torch()
+    c, nb = _Call(Wp, "Wp"), qpacked_bytes_f8(N, K)
+    _sizes("qgemv_f8", nb)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [M][{K}]")
+    M = x.shape[0]
+    y = c.out(y, (M, N), torch.float32, "y")
+    c("qgemv_f8", c.ptr(Wp, torch.uint8, "Wp", nb), c.ptr(x, x.dtype, "x", M * K), _type(x.dtype),
+      c.ptr(y, torch.float32, "y", M * N), M, N, K)
+    return y
+
+
+def qgemm_f8(Wp, xq, M: int, N: int, K: int, dtype=None, Y=None):
+    """Y[M][N] = X @ W^T on packed f8 activations (fp32 by default, or fp16 / bf16)."""
+    torch = _torch()
+    c, nb, na = _Call(Wp, "Wp"), qpacked_bytes_f8(N, K), qact_bytes_f8(M, K)
+    _sizes("qgemm_f8", nb, na)
+    dtype = dtype or (torch.float32 if Y is None else Y.dtype)
+    code = _type(dtype)
+    Y = c.out(Y, (M, N), dtype, "Y")
+    c("qgemm_f8", c.ptr(Wp, torch.uint8, "Wp", nb), c.ptr(xq, torch.uint8, "xq", na), c.ptr(Y, dtype, "Y", M * N),
+      code, M, N, K)
+    return Y
+
+
+def qgemm_f8_wgrad(dY, xq, M: int, N: int, K: int, dW=None, accumulate: bool = False):
+    """dW[N][K] (fp32) = dY[M][N]^T @ X from bf16 dY and the packed f8 activations X (added to dW with accumulate)."""
+    torch = _torch()
+    c, na = _Call(dY, "dY"), qact_bytes_f8(M, K)
+    _sizes("qgemm_f8_wgrad", na, N)
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs dW")
+    dW = c.out(dW, (N, K), torch.float32, "dW")
+    ws = int(lib().qgemm_f8_wgrad_workspace(M, N, K))
+    w = c.new((ws,), torch.uint8) if ws else None
+    c("qgemm_f8_wgrad", c.ptr(dY, torch.bfloat16, "dY", M * N), c.ptr(xq, torch.uint8, "xq", na),
+      c.ptr(dW, torch.float32, "dW", N * K), int(accumulate), M, N, K, w.data_ptr() if ws else None)
+    return dW
+
+
+class MoeRoute(NamedTuple):
+    """What qmoe_route returns; qmoe_route_backward and qmoe_gemm_f8 take it up."""
+    idx: object       # int32 [T][k], -1: no expert
+    weight: object    # fp32 [T][k]
+    counts: object    # int32 [E], slots of each expert
+    tokens: object    # int32 [1], tokens that were routed
+    offsets: object   # int32 [E + 1]
+    order: object     # int32 [T k], the slots sorted by expert
+    loss: object      # fp32 [1], the balance loss
+
+
+def _logits(logits, mask):
+    torch = _torch()
+    c = _Call(logits, "logits")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [T][E] with contiguous rows")
+    T, E = logits.shape
+    if mask is not None and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    if mask is not None and mask.shape != (T,):
+        raise ValueError(f"mask must be [{T}]")
+    return c, T, E, logits.stride(0) if T > 1 else E, c.ptr(mask, torch.uint8, "mask", T, optional=True)
+
+
+def qmoe_route(logits, k: int, mask=None, renormalize: bool = True) -> MoeRoute:
+    """Top-k softmax routing of logits[T][E] (fp32, fp16 or bf16; rows may be
+    strided) with per-expert counts, the slots sorted by expert and the balance
+    loss; mask (bool or uint8 [T]): 0 for tokens that are not routed."""
+    torch = _torch()
+    c, T, E, ld, mp = _logits(logits, mask)
+    code = _type(logits.dtype)
+    if not (1 <= k <= min(E, 16) and 1 <= T <= 1 << 24 and E <= 512):
+        raise QGError("qmoe_route", 2)
+    i32 = c.new((T * k * 2 + 2 * (E + 1),), torch.int32)
+    f32 = c.new((T * k + 1,), torch.float32)
+    idx, order, counts, offsets = i32.split([T * k, T * k, E + 1, E + 1])
+    weight, loss = f32.split([T * k, 1])
+    ws = int(lib().qmoe_route_workspace(T, E))
+    w = c.new((ws,), torch.uint8) if ws else None
+    c("qmoe_route", logits.data_ptr(), code, ld, mp, T, E, k, int(renormalize), idx.data_ptr(), weight.data_ptr(),
+      counts.data_ptr(), offsets.data_ptr(), order.data_ptr(), loss.data_ptr(), w.data_ptr() if ws else None)
+    return MoeRoute(idx.view(T, k), weight.view(T, k), counts[:E], counts[E:], offsets, order, loss)
+
+
+def qmoe_route_backward(logits, route: MoeRoute, grad_weight=None, grad_loss=None, mask=None,
+                        renormalize: bool = True, out=None):
+    """The gradient of route.weight and route.loss with respect to the logits (their type)."""
+    torch = _torch()
+    c, T, E, ld, mp = _logits(logits, mask)
+    k = route.idx.shape[1]
+    if route.idx.shape != (T, k) or route.weight.shape != (T, k) or route.counts.shape != (E,) or \
+            route.tokens.data_ptr() != route.counts.data_ptr() + 4 * E:
+        raise ValueError("route is not of these logits")
+    for name, t, n in (("grad_weight", grad_weight, (T, k)), ("grad_loss", grad_loss, None)):
+        if t is not None and (t.numel() != 1 if n is None else tuple(t.shape) != n):
+            raise ValueError(f"{name} has shape {list(t.shape)}")
+    dl = c.out(out, (T, E), logits.dtype, "out")
+    f32, i32 = torch.float32, torch.int32
+    c("qmoe_route_backward", logits.data_ptr(), _type(logits.dtype), ld, mp, T, E, k, int(renormalize),
+      c.ptr(route.idx, i32, "route.idx", T * k), c.ptr(route.weight, f32, "route.weight", T * k),
+      c.ptr(route.counts, i32, "route.counts", E), c.ptr(grad_weight, f32, "grad_weight", T * k, optional=True),
+      c.ptr(grad_loss, f32, "grad_loss", 1, optional=True), c.ptr(dl, logits.dtype, "out", T * E))
+    return dl
+
+
+def _slots(T: int, order):
+    S = order.numel()
+    if T < 1 or S < 1 or S % T:
+        raise ValueError(f"order has {S} slots, not a multiple of {T} tokens")
+    return S, S // T
+
+
+def qmoe_gemm_f8(pool, P: int, xq, T: int, order, offsets, N: int, K: int, dtype=None, Y=None):
+    """Y[slot][N] = expert's matrix times X[slot // k] for the slots of
+    qmoe_route's order / offsets (k = order.numel() // T; T rows of X); slots
+    without an expert get zeros."""
+    torch = _torch()
+    c, nb, na = _Call(pool, "pool"), qpacked_bytes_f8(N, K), qact_bytes_f8(T, K)
+    _sizes("qmoe_gemm_f8", nb, na)
+    S, k = _slots(T, order)
+    dtype = dtype or (torch.float32 if Y is None else Y.dtype)
+    code = _type(dtype)
+    Y = c.out(Y, (S, N), dtype, "Y")
+    c("qmoe_gemm_f8", c.ptr(pool, torch.uint8, "pool", P * nb), P, c.ptr(xq, torch.uint8, "xq", na), T, k,
+      c.ptr(order, torch.int32, "order", S), c.ptr(offsets, torch.int32, "offsets", P + 1),
+      c.ptr(Y, dtype, "Y", S * N), code, N, K)
+    return Y
+
+
+def qmoe_gemm_f8_wgrad(dY, xq, T: int, order, offsets, P: int, N: int, K: int, dW=None, accumulate: bool = False):
+    """dW[P][N][K] (fp32): for each expert, dY^T @ X over its slots (dY bf16 [slots][N], X packed with T rows)."""
+    torch = _torch()
+    c, na = _Call(dY, "dY"), qact_bytes_f8(T, K)
+    _sizes("qmoe_gemm_f8_wgrad", na, N)
+    S, k = _slots(T, order)
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs dW")
+    dW = c.out(dW, (P, N, K), torch.float32, "dW")
+    c("qmoe_gemm_f8_wgrad", c.ptr(dY, torch.bfloat16, "dY", S * N), c.ptr(xq, torch.uint8, "xq", na), T, k,
+      c.ptr(order, torch.int32, "order", S), c.ptr(offsets, torch.int32, "offsets", P + 1), P,
+      c.ptr(dW, torch.float32, "dW", P * N * K), int(accumulate), N, K)
+    return dW
 
 
 # --------------------------------------------------------------- measurement

@@ -38,6 +38,8 @@ constexpr int kMaxDevices = 64;
 int g_cus[kMaxDevices] = {0};
 std::mutex g_mu;
 
+}  // namespace
+
 int device_cus()
 {
     int dev = 0;
@@ -52,6 +54,8 @@ int device_cus()
     }
     return g_cus[dev];
 }
+
+namespace {
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

@@ -1,0 +1,297 @@
+// Shared by the f8 translation units: packed layouts, element types, the
+// quantizer's rule and the operands' conversions (qgemv_f8.h states the
+// formats).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "qgemv_f8.h"
+#include "qgemv_internal.h"
+
+namespace qg {
+
+constexpr int64_t kF8MaxK = 1 << 20;
+constexpr int64_t kF8MaxRows = INT32_MAX;
+constexpr int64_t kF8MaxGemvK = 16384;        // 128 KiB of codes in LDS
+constexpr int64_t kRouteMaxTokens = 1 << 24;
+constexpr int kMaxExperts = 512;
+constexpr int kMaxTopK = 16;
+
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Packed weights of an N x K matrix.
+struct F8Weights {
+    int cb;             // column blocks of 128
+    int rt;             // row tiles of 16
+    int ls;             // bytes of a row of scales
+    int64_t scales;     // byte offset of the scale region
+    int64_t bytes;
+};
+
+inline F8Weights f8_weights(int64_t N, int64_t K)
+{
+    F8Weights w;
+    w.cb = (int)ceil_div(K, 128);
+    w.rt = (int)ceil_div(N, 16);
+    w.ls = (w.cb + 3) / 4 * 4;
+    w.scales = (int64_t)w.rt * w.cb * 2048;
+    w.bytes = ceil_div(w.scales + ceil_div(N, 128) * w.ls, 256) * 256;
+    return w;
+}
+
+// Packed activations of M x K.
+struct F8Acts {
+    int cb, ls;
+    int64_t scales, bytes;
+};
+
+inline F8Acts f8_acts(int64_t M, int64_t K)
+{
+    F8Acts a;
+    a.cb = (int)ceil_div(K, 128);
+    a.ls = (a.cb + 3) / 4 * 4;
+    a.scales = ceil_div(M * a.cb * 128, 256) * 256;
+    a.bytes = ceil_div(a.scales + M * a.ls, 256) * 256;
+    return a;
+}
+
+inline int type_bytes(int t) { return t == QG_F32 ? 4 : 2; }
+inline bool type_ok(int t) { return t == QG_F32 || t == QG_F16 || t == QG_BF16; }
+
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
+typedef float f16v_t __attribute__((ext_vector_type(16)));
+typedef int i8_t __attribute__((ext_vector_type(8)));
+
+// Element types as C++ types, for templates.
+struct Bf16 {
+    uint16_t u;
+};
+struct Fp16 {
+    uint16_t u;
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(Fp16 v) { return (float)__builtin_bit_cast(_Float16, v.u); }
+__device__ __forceinline__ float to_f32(Bf16 v) { return __uint_as_float((uint32_t)v.u << 16); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ Fp16 from_f32<Fp16>(float v) { return Fp16{__builtin_bit_cast(uint16_t, (_Float16)v)}; }
+template <>
+__device__ __forceinline__ Bf16 from_f32<Bf16>(float v) { return Bf16{__builtin_bit_cast(uint16_t, (__bf16)v)}; }
+
+// 16 bytes at any element's alignment (the hardware takes unaligned
+// addresses; rows of an odd stride start anywhere).
+struct __attribute__((packed, aligned(2))) Raw16 {
+    uint32_t w[4];
+};
+
+// N consecutive elements as fp32; elements from `left` on are zero.
+template <typename T, int N>
+__device__ __forceinline__ void load_row(const T *p, int left, float (&v)[N])
+{
+    if (left >= N) {
+        constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < N / kPer; ++i) {
+            const Raw16 r = *reinterpret_cast<const Raw16 *>(p + i * kPer);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if constexpr (sizeof(T) == 4)
+                    v[i * kPer + j] = __uint_as_float(r.w[j]);
+                else
+                    v[i * kPer + j] = to_f32(T{(uint16_t)(r.w[j / 2] >> (16 * (j & 1)))});
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = i < left ? to_f32(p[i]) : 0.0f;
+    }
+}
+
+// Scale byte of a block whose largest finite magnitude has the fp32 bits
+// `amax`: the smallest e >= -127 with amax <= 448 * 2^e, 448 = 1.75 * 2^8, as
+// e + 127; 127 for an empty or zero block.  From the bits alone, so it is
+// exact: with amax = 1.f * 2^x, e = x - 8, one more where 1.f > 1.75.
+// Subnormal amax needs e < -127 at any rate.
+__host__ __device__ __forceinline__ uint32_t f8_scale_byte(uint32_t amax)
+{
+    if (amax == 0)
+        return 127;
+    const int e = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);   // biased by 127
+    return e < 0 ? 0u : (uint32_t)e;
+}
+
+// 2^(byte - 127) and its reciprocal; byte 0 is the subnormal 2^-127, and the
+// reciprocal of the largest scales the quantizer writes (2^120) is normal.
+__device__ __forceinline__ float f8_scale(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
+
+// v * 2^-(byte - 127) without an intermediate that leaves fp32's range: 2^127
+// is the largest power, all that byte 0 needs.
+__device__ __forceinline__ float f8_inverse(uint32_t byte) { return byte >= 254 ? 0x1p-127f : __uint_as_float((254u - byte) << 23); }
+
+// |v| of a finite v, 0 of the others, as bits (ordered like the magnitudes).
+__device__ __forceinline__ uint32_t finite_mag(float v)
+{
+    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+}
+
+// Four values, scaled, as e4m3 codes in one word.  The conversion rounds to
+// nearest even and saturates nothing here (the scale keeps |v| <= 448); an
+// infinity becomes NaN (v * 0 is added where the value is not finite, because
+// the conversion would clamp it).
+__device__ __forceinline__ float f8_prepare(float v, float inv)
+{
+    const float s = v * inv;
+    return finite_mag(v) == (__float_as_uint(v) & 0x7FFFFFFFu) ? s : __uint_as_float(0x7FC00000u);
+}
+
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
+{
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    return (uint32_t)w;
+}
+
+// Eight codes (two words) times a power of two as a bf16 operand: exact (four
+// significant bits, bf16's exponent range).
+__device__ __forceinline__ bf8_t f8_widen(uint32_t lo, uint32_t hi, float scale)
+{
+    const bf2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    bf8_t r;
+    r[0] = a[0], r[1] = a[1], r[2] = b[0], r[3] = b[1], r[4] = c[0], r[5] = c[1], r[6] = d[0], r[7] = d[1];
+    return r;
+}
+
+// Where a group's rows are: rows r0 .. r1 - 1 of `order` (or of Y and X, dense),
+// at most `tile` of them, of expert e; e = P: slots without an expert.
+struct F8Unit {
+    int e;
+    int64_t r0, r1;
+};
+
+// The unit-th tile of `tile` rows, counting expert by expert, each expert
+// beginning a tile of its own; r0 = r1 past the last one.  Every wave finds it
+// by itself: a lane counts the tiles of its share of the experts, a prefix sum
+// over the lanes and one ballot find the share that holds the unit.  Offsets
+// are device data: they are held to 0 .. rows and to their order, so a tile
+// never leaves `order`.
+__device__ __forceinline__ F8Unit f8_unit(const int32_t *offsets, int P, int64_t rows, int tile, int64_t unit)
+{
+    const int lane = threadIdx.x & 63;
+    const int per = (P + 1 + 63) / 64;
+    const int n = (int)rows;
+    auto span = [&](int e, int &a, int &b) {
+        a = min(max(offsets[e], 0), n);
+        b = e < P ? max(a, min(max(offsets[e + 1], 0), n)) : n;
+    };
+    int mine = 0;
+    for (int j = 0; j < per; ++j) {
+        const int e = lane * per + j;
+        int a = 0, b = 0;
+        if (e <= P)
+            span(e, a, b);
+        mine += (b - a + tile - 1) / tile;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(incl, d);
+        incl += lane >= d ? o : 0;
+    }
+    const unsigned long long holds = __ballot((int64_t)incl > unit);
+    if (holds == 0)
+        return F8Unit{P, 0, 0};
+    const int src = __ffsll(holds) - 1;
+    int left = (int)unit - __builtin_amdgcn_readlane(incl - mine, src);
+    for (int j = 0; j < per; ++j) {
+        const int e = src * per + j;
+        if (e > P)
+            break;
+        int a, b;
+        span(e, a, b);
+        const int tiles = (b - a + tile - 1) / tile;
+        if (left < tiles)
+            return F8Unit{e, a + (int64_t)left * tile, min((int64_t)b, a + (int64_t)(left + 1) * tile)};
+        left -= tiles;
+    }
+    return F8Unit{P, 0, 0};
+}
+
+// An upper bound of the tiles that f8_unit counts.
+inline int64_t f8_units(int64_t rows, int P, int tile) { return rows / tile + (rows < P + 1 ? rows : P + 1); }
+
+// Launchers (arguments validated by the callers in qgemv_f8_capi.hip).
+hipError_t launch_act_quantize(const void *x, int type, int64_t ldx, int64_t M, int64_t K, uint8_t *xq,
+                               hipStream_t stream);
+hipError_t launch_act_dequant(const uint8_t *xq, int64_t M, int64_t K, int type, void *out, hipStream_t stream);
+hipError_t launch_f8_dequant(const uint8_t *W, int64_t N, int64_t K, bool fp16, void *out, hipStream_t stream);
+hipError_t launch_f8_transpose(const uint8_t *W, int64_t N, int64_t K, uint8_t *WT, hipStream_t stream);
+
+// Rows of a product: all M of them, or the slots of one expert after the
+// other (order, offsets), with row s of X being slot / k_slots.
+struct F8Rows {
+    int64_t rows;             // rows of Y
+    int64_t x_rows;           // rows of X
+    const int32_t *order;     // nullptr: dense
+    const int32_t *offsets;   // [P + 1]
+    int P;
+    int k_slots;
+    int64_t stride;           // bytes between pool matrices
+};
+
+// x (type QG_*) to be quantized in the launch, or nullptr and xq.
+hipError_t launch_f8_skinny(const uint8_t *W, const uint8_t *xq, const void *x, int x_type, void *Y, int y_type,
+                            const F8Rows &r, int64_t N, int64_t K, int cus, hipStream_t stream);
+hipError_t launch_f8_gemm(const uint8_t *W, const uint8_t *xq, void *Y, int y_type, const F8Rows &r, int64_t N,
+                          int64_t K, int cus, hipStream_t stream);
+
+size_t f8_wgrad_workspace(int64_t M, int64_t N, int64_t K);
+hipError_t launch_f8_wgrad(const uint16_t *dY, const uint8_t *xq, float *dW, bool accumulate, const F8Rows &r,
+                           int64_t N, int64_t K, float *workspace, int cus, hipStream_t stream);
+
+struct RouteArgs {
+    const void *logits;
+    int type;
+    int64_t ldl;
+    const uint8_t *mask;
+    int64_t T;
+    int E, k;
+    bool renormalize;
+    int32_t *idx;
+    float *weight;
+    int32_t *counts, *offsets, *order;
+    float *loss;
+    void *workspace;
+};
+struct RouteGradArgs {
+    const void *logits;
+    int type;
+    int64_t ldl;
+    const uint8_t *mask;
+    int64_t T;
+    int E, k;
+    bool renormalize;
+    const int32_t *idx;
+    const float *weight;
+    const int32_t *counts;
+    const float *grad_weight, *grad_loss;
+    void *dlogits;
+};
+size_t route_workspace(int64_t T, int64_t E);
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+hipError_t launch_route_backward(const RouteGradArgs &a, int cus, hipStream_t stream);
+
+}  // namespace qg

@@ -50,6 +50,9 @@ __device__ __forceinline__ uint16_t stream_load2(__amdgpu_buffer_rsrc_t r, uint3
     return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, kNtAux);
 }
 
+// Compute units of the current device (cached per device; 0 if the query fails).
+int device_cus();
+
 // Arguments of the GEMV / MoE kernel (passed by value).
 struct GemvParams {
     const uint8_t *W;          // packed matrix, or the expert pool for MoE
