@@ -401,17 +401,16 @@ class _Call:
     """One call's device: every tensor has to be on it, and the call is made
     with it as the current device, on its current stream."""
 
+    __slots__ = ("device", "torch")
+
     def __init__(self, first, name: str):
-        torch = _torch()
+        self.torch = torch = _torch()
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError(f"{name} must be a device tensor")
         self.device = first.device
 
-    def ptr(self, t, dtype, name: str, numel: int, optional: bool = False):
-        torch = _torch()
-        if t is None and optional:
-            return None
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    def ptr(self, t, dtype, name: str, numel: int):
+        if not isinstance(t, self.torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a device tensor")
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the call's other tensors on {self.device}")
@@ -423,25 +422,32 @@ class _Call:
             raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
         return t.data_ptr()
 
-    def new(self, shape, dtype):
-        return _torch().empty(shape, dtype=dtype, device=self.device)
+    def opt(self, t, dtype, name: str, numel: int):
+        return None if t is None else self.ptr(t, dtype, name, numel)
 
-    def out(self, t, shape, dtype, name: str):
-        """The caller's output of this shape, or a new one."""
+    def new(self, shape, dtype):
+        return self.torch.empty(shape, dtype=dtype, device=self.device)
+
+    def result(self, t, shape, dtype, name: str, numel: int):
+        """The caller's output of this shape, or a new one, and its address."""
         if t is None:
-            return self.new(shape, dtype)
-        if tuple(t.shape) != tuple(shape):
+            t = self.torch.empty(shape, dtype=dtype, device=self.device)
+            return t, t.data_ptr()
+        if tuple(t.shape) != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        return t
+        return t, self.ptr(t, dtype, name, numel)
 
     def __call__(self, fn: str, *args):
-        torch = _torch()
         f = getattr(lib(), fn)
-        if self.device.index == torch.cuda.current_device():
-            st = f(*args, torch.cuda.current_stream().cuda_stream)
+        index = self.device.index
+        # the stream's handle as it is: torch.cuda.current_stream() makes an
+        # object around it first (2.7 us of the 9.7 that a small call took)
+        stream = self.torch._C._cuda_getCurrentRawStream(index)
+        if index == self.torch.cuda.current_device():
+            st = f(*args, stream)
         else:
-            with torch.cuda.device(self.device):
-                st = f(*args, torch.cuda.current_stream().cuda_stream)
+            with self.torch.cuda.device(index):
+                st = f(*args, stream)
         if st:
             raise QGError(fn, st)
 
@@ -453,93 +459,86 @@ def _sizes(fn: str, *nbytes: int):
 
 def qdequant_f8(Wp, N: int, K: int, fp16: bool = False, out=None):
     """The values of a packed f8 matrix, [N][K] in fp32 or fp16."""
-    torch = _torch()
     c, nb = _Call(Wp, "Wp"), qpacked_bytes_f8(N, K)
     _sizes("qdequant_f8", nb)
-    dt = torch.float16 if fp16 else torch.float32
-    out = c.out(out, (N, K), dt, "out")
-    c("qdequant_f8", c.ptr(Wp, torch.uint8, "Wp", nb), N, K, int(fp16), c.ptr(out, dt, "out", N * K))
+    out, op = c.result(out, (N, K), c.torch.float16 if fp16 else c.torch.float32, "out", N * K)
+    c("qdequant_f8", c.ptr(Wp, c.torch.uint8, "Wp", nb), N, K, int(fp16), op)
     return out
 
 
 def qtranspose_f8(Wp, N: int, K: int, out=None):
     """The packed N x K matrix as the packed K x N matrix (exact), the operand of dx = f8(dy) W."""
-    torch = _torch()
     c, nb, nt = _Call(Wp, "Wp"), qpacked_bytes_f8(N, K), qpacked_bytes_f8(K, N)
     _sizes("qtranspose_f8", nb, nt)
     if out is None:
-        out = c.new((nt,), torch.uint8)
-    c("qtranspose_f8", c.ptr(Wp, torch.uint8, "Wp", nb), N, K, c.ptr(out, torch.uint8, "out", nt))
+        out = c.new((nt,), c.torch.uint8)
+    c("qtranspose_f8", c.ptr(Wp, c.torch.uint8, "Wp", nb), N, K, c.ptr(out, c.torch.uint8, "out", nt))
     return out
 
 
 def qact_quantize_f8(x, out=None):
     """x[M][K] (fp32, fp16 or bf16; rows may be strided) -> packed f8 activations (uint8)."""
-    torch = _torch()
     c = _Call(x, "x")
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be [M][K] with contiguous rows")
     M, K = x.shape
-    ld = x.stride(0) if M > 1 else K
     nb = qact_bytes_f8(M, K)
     _sizes("qact_quantize_f8", nb)
     if out is None:
-        out = c.new((nb,), torch.uint8)
-    c("qact_quantize_f8", x.data_ptr(), _type(x.dtype), ld, M, K, c.ptr(out, torch.uint8, "out", nb))
+        out = c.new((nb,), c.torch.uint8)
+        op = out.data_ptr()
+    else:
+        op = c.ptr(out, c.torch.uint8, "out", nb)
+    c("qact_quantize_f8", x.data_ptr(), _type(x.dtype), x.stride(0) if M > 1 else K, M, K, op)
     return out
 
 
 def qact_dequant_f8(xq, M: int, K: int, dtype=None, out=None):
     """The values of packed f8 activations, [M][K] (fp32 by default)."""
-    torch = _torch()
     c, nb = _Call(xq, "xq"), qact_bytes_f8(M, K)
     _sizes("qact_dequant_f8", nb)
-    dtype = dtype or (torch.float32 if out is None else out.dtype)
+    dtype = dtype or (c.torch.float32 if out is None else out.dtype)
     code = _type(dtype)
-    out = c.out(out, (M, K), dtype, "out")
-    c("qact_dequant_f8", c.ptr(xq, torch.uint8, "xq", nb), M, K, code, c.ptr(out, dtype, "out", M * K))
+    out, op = c.result(out, (M, K), dtype, "out", M * K)
+    c("qact_dequant_f8", c.ptr(xq, c.torch.uint8, "xq", nb), M, K, code, op)
     return out
 
 
 def qgemv_f8(Wp, x, N: int, K: int, y=None):
     """y[M][N] (fp32) = f8(x)[M][K] @ W^T, 1 <= M <= 8: x (fp32, fp16 or bf16) is quantized inside the launch."""
-    torch = _torch()
     c, nb = _Call(Wp, "Wp"), qpacked_bytes_f8(N, K)
     _sizes("qgemv_f8", nb)
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError(f"x must be [M][{K}]")
     M = x.shape[0]
-    y = c.out(y, (M, N), torch.float32, "y")
-    c("qgemv_f8", c.ptr(Wp, torch.uint8, "Wp", nb), c.ptr(x, x.dtype, "x", M * K), _type(x.dtype),
-      c.ptr(y, torch.float32, "y", M * N), M, N, K)
+    y, yp = c.result(y, (M, N), c.torch.float32, "y", M * N)
+    c("qgemv_f8", c.ptr(Wp, c.torch.uint8, "Wp", nb), c.ptr(x, x.dtype, "x", M * K), _type(x.dtype), yp, M, N, K)
     return y
 
 
 def qgemm_f8(Wp, xq, M: int, N: int, K: int, dtype=None, Y=None):
     """Y[M][N] = X @ W^T on packed f8 activations (fp32 by default, or fp16 / bf16)."""
-    torch = _torch()
     c, nb, na = _Call(Wp, "Wp"), qpacked_bytes_f8(N, K), qact_bytes_f8(M, K)
     _sizes("qgemm_f8", nb, na)
-    dtype = dtype or (torch.float32 if Y is None else Y.dtype)
+    dtype = dtype or (c.torch.float32 if Y is None else Y.dtype)
     code = _type(dtype)
-    Y = c.out(Y, (M, N), dtype, "Y")
-    c("qgemm_f8", c.ptr(Wp, torch.uint8, "Wp", nb), c.ptr(xq, torch.uint8, "xq", na), c.ptr(Y, dtype, "Y", M * N),
-      code, M, N, K)
+    Y, yp = c.result(Y, (M, N), dtype, "Y", M * N)
+    u8 = c.torch.uint8
+    c("qgemm_f8", c.ptr(Wp, u8, "Wp", nb), c.ptr(xq, u8, "xq", na), yp, code, M, N, K)
     return Y
 
 
 def qgemm_f8_wgrad(dY, xq, M: int, N: int, K: int, dW=None, accumulate: bool = False):
     """dW[N][K] (fp32) = dY[M][N]^T @ X from bf16 dY and the packed f8 activations X (added to dW with accumulate)."""
-    torch = _torch()
     c, na = _Call(dY, "dY"), qact_bytes_f8(M, K)
-    _sizes("qgemm_f8_wgrad", na, N)
+    _sizes("qgemm_f8_wgrad", na, qpacked_bytes_f8(N, K))
     if accumulate and dW is None:
         raise ValueError("accumulate needs dW")
-    dW = c.out(dW, (N, K), torch.float32, "dW")
+    dW, wp = c.result(dW, (N, K), c.torch.float32, "dW", N * K)
     ws = int(lib().qgemm_f8_wgrad_workspace(M, N, K))
-    w = c.new((ws,), torch.uint8) if ws else None
-    c("qgemm_f8_wgrad", c.ptr(dY, torch.bfloat16, "dY", M * N), c.ptr(xq, torch.uint8, "xq", na),
-      c.ptr(dW, torch.float32, "dW", N * K), int(accumulate), M, N, K, w.data_ptr() if ws else None)
+    w = c.new((ws,), c.torch.uint8) if ws else None
+    c("qgemm_f8_wgrad", c.ptr(dY, c.torch.bfloat16, "dY", M * N), c.ptr(xq, c.torch.uint8, "xq", na), wp,
+      int(accumulate), M, N, K, w.data_ptr() if ws else None)
     return dW
 
 
@@ -564,7 +563,7 @@ def _logits(logits, mask):
         mask = mask.view(torch.uint8)
     if mask is not None and mask.shape != (T,):
         raise ValueError(f"mask must be [{T}]")
-    return c, T, E, logits.stride(0) if T > 1 else E, c.ptr(mask, torch.uint8, "mask", T, optional=True)
+    return c, T, E, logits.stride(0) if T > 1 else E, c.opt(mask, torch.uint8, "mask", T)
 
 
 def qmoe_route(logits, k: int, mask=None, renormalize: bool = True) -> MoeRoute:
@@ -576,15 +575,16 @@ def qmoe_route(logits, k: int, mask=None, renormalize: bool = True) -> MoeRoute:
     code = _type(logits.dtype)
     if not (1 <= k <= min(E, 16) and 1 <= T <= 1 << 24 and E <= 512):
         raise QGError("qmoe_route", 2)
-    i32 = c.new((T * k * 2 + 2 * (E + 1),), torch.int32)
-    f32 = c.new((T * k + 1,), torch.float32)
-    idx, order, counts, offsets = i32.split([T * k, T * k, E + 1, E + 1])
-    weight, loss = f32.split([T * k, 1])
+    S, i32, f32 = T * k, torch.int32, torch.float32
+    idx, weight, order, loss = c.new((T, k), i32), c.new((T, k), f32), c.new((S,), i32), c.new((1,), f32)
+    both = c.new((2 * E + 2,), i32)
+    at = both.data_ptr()
     ws = int(lib().qmoe_route_workspace(T, E))
     w = c.new((ws,), torch.uint8) if ws else None
     c("qmoe_route", logits.data_ptr(), code, ld, mp, T, E, k, int(renormalize), idx.data_ptr(), weight.data_ptr(),
-      counts.data_ptr(), offsets.data_ptr(), order.data_ptr(), loss.data_ptr(), w.data_ptr() if ws else None)
-    return MoeRoute(idx.view(T, k), weight.view(T, k), counts[:E], counts[E:], offsets, order, loss)
+      at, at + 4 * (E + 1), order.data_ptr(), loss.data_ptr(), w.data_ptr() if ws else None)
+    counts, tokens, offsets = both.split((E, 1, E + 1))
+    return MoeRoute(idx, weight, counts, tokens, offsets, order, loss)
 
 
 def qmoe_route_backward(logits, route: MoeRoute, grad_weight=None, grad_loss=None, mask=None,
@@ -599,12 +599,12 @@ def qmoe_route_backward(logits, route: MoeRoute, grad_weight=None, grad_loss=Non
     for name, t, n in (("grad_weight", grad_weight, (T, k)), ("grad_loss", grad_loss, None)):
         if t is not None and (t.numel() != 1 if n is None else tuple(t.shape) != n):
             raise ValueError(f"{name} has shape {list(t.shape)}")
-    dl = c.out(out, (T, E), logits.dtype, "out")
+    dl, dp = c.result(out, (T, E), logits.dtype, "out", T * E)
     f32, i32 = torch.float32, torch.int32
     c("qmoe_route_backward", logits.data_ptr(), _type(logits.dtype), ld, mp, T, E, k, int(renormalize),
       c.ptr(route.idx, i32, "route.idx", T * k), c.ptr(route.weight, f32, "route.weight", T * k),
-      c.ptr(route.counts, i32, "route.counts", E), c.ptr(grad_weight, f32, "grad_weight", T * k, optional=True),
-      c.ptr(grad_loss, f32, "grad_loss", 1, optional=True), c.ptr(dl, logits.dtype, "out", T * E))
+      c.ptr(route.counts, i32, "route.counts", E), c.opt(grad_weight, f32, "grad_weight", T * k),
+      c.opt(grad_loss, f32, "grad_loss", 1), dp)
     return dl
 
 
@@ -625,10 +625,10 @@ def qmoe_gemm_f8(pool, P: int, xq, T: int, order, offsets, N: int, K: int, dtype
     S, k = _slots(T, order)
     dtype = dtype or (torch.float32 if Y is None else Y.dtype)
     code = _type(dtype)
-    Y = c.out(Y, (S, N), dtype, "Y")
+    Y, yp = c.result(Y, (S, N), dtype, "Y", S * N)
     c("qmoe_gemm_f8", c.ptr(pool, torch.uint8, "pool", P * nb), P, c.ptr(xq, torch.uint8, "xq", na), T, k,
       c.ptr(order, torch.int32, "order", S), c.ptr(offsets, torch.int32, "offsets", P + 1),
-      c.ptr(Y, dtype, "Y", S * N), code, N, K)
+      yp, code, N, K)
     return Y
 
 
@@ -636,14 +636,14 @@ def qmoe_gemm_f8_wgrad(dY, xq, T: int, order, offsets, P: int, N: int, K: int, d
     """dW[P][N][K] (fp32): for each expert, dY^T @ X over its slots (dY bf16 [slots][N], X packed with T rows)."""
     torch = _torch()
     c, na = _Call(dY, "dY"), qact_bytes_f8(T, K)
-    _sizes("qmoe_gemm_f8_wgrad", na, N)
+    _sizes("qmoe_gemm_f8_wgrad", na, qpacked_bytes_f8(N, K))
     S, k = _slots(T, order)
     if accumulate and dW is None:
         raise ValueError("accumulate needs dW")
-    dW = c.out(dW, (P, N, K), torch.float32, "dW")
+    dW, wp = c.result(dW, (P, N, K), torch.float32, "dW", P * N * K)
     c("qmoe_gemm_f8_wgrad", c.ptr(dY, torch.bfloat16, "dY", S * N), c.ptr(xq, torch.uint8, "xq", na), T, k,
       c.ptr(order, torch.int32, "order", S), c.ptr(offsets, torch.int32, "offsets", P + 1), P,
-      c.ptr(dW, torch.float32, "dW", P * N * K), int(accumulate), N, K)
+      wp, int(accumulate), N, K)
     return dW
 
 

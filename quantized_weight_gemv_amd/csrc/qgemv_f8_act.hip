@@ -26,8 +26,7 @@ __device__ __forceinline__ void store_row(T *p, int left, const float (&v)[N])
                 if constexpr (sizeof(T) == 4)
                     r.w[j] = __float_as_uint(v[i * kPer + j]);
                 else
-                    r.w[j] = from_f32<T>(v[i * kPer + 2 * j]).u |
-                             (uint32_t)from_f32<T>(v[i * kPer + 2 * j + 1]).u << 16;
+                    r.w[j] = pack2<T>(v[i * kPer + 2 * j], v[i * kPer + 2 * j + 1]);
             }
             *reinterpret_cast<Raw16 *>(p + i * kPer) = r;
         }
@@ -76,20 +75,8 @@ __global__ __launch_bounds__(256) void act_quantize_kernel(ActArgs a)
     const int k = c * 128 + part * 16;
     float v[16];
     load_row(static_cast<const T *>(a.x) + m * a.ldx + k, a.K - k, v);
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        amax = max(amax, finite_mag(v[i]));
-#pragma unroll
-    for (int s = 1; s < 8; s *= 2)
-        amax = max(amax, (uint32_t)__shfl_xor((int)amax, s));
-    const uint32_t byte = f8_scale_byte(amax);
-    const float inv = f8_inverse(byte);
     uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = f8_pack4(f8_prepare(v[4 * i], inv), f8_prepare(v[4 * i + 1], inv), f8_prepare(v[4 * i + 2], inv),
-                        f8_prepare(v[4 * i + 3], inv));
+    const uint32_t byte = f8_quantize16(v, w);
     *reinterpret_cast<uint4 *>(a.xq + (m * a.cb + c) * 128 + part * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     if (part == 0)
         a.xq[a.scales + m * a.ls + c] = (uint8_t)byte;

@@ -147,12 +147,9 @@ qg_status qgemm_f8_wgrad(const void *dY, const void *xq, float *dW, int accumula
         return QG_ERR_NULL;
     if (!aligned(dY, 2) || !aligned(xq, 256) || !aligned(dW, 4) || !aligned(workspace, 16))
         return QG_ERR_ALIGN;
-    const int cus = device_cus();
-    if (cus <= 0)
-        return QG_ERR_DEVICE;
     const F8Rows r{M, M, nullptr, nullptr, 0, 1, 0};
     return status(launch_f8_wgrad(static_cast<const uint16_t *>(dY), static_cast<const uint8_t *>(xq), dW,
-                                  accumulate != 0, r, N, K, static_cast<float *>(workspace), cus, on(stream)));
+                                  accumulate != 0, r, N, K, static_cast<float *>(workspace), on(stream)));
 }
 
 size_t qmoe_route_workspace(int64_t T, int64_t E)
@@ -172,7 +169,7 @@ qg_status qmoe_route(const void *logits, int type, int64_t ldl, const uint8_t *t
     if (!aligned(offsets, 4) || !aligned(order, 4) || !aligned(loss, 4) || !aligned(workspace, 16))
         return QG_ERR_ALIGN;
     const RouteArgs a{logits, type, ldl, token_mask, T, (int)E, k, renormalize != 0, idx, weight, counts, offsets,
-                      order, loss, workspace};
+                      order, loss, workspace, false};
     return status(launch_route(a, on(stream)));
 }
 
@@ -192,7 +189,7 @@ qg_status qmoe_route_backward(const void *logits, int type, int64_t ldl, const u
     if (cus <= 0)
         return QG_ERR_DEVICE;
     const RouteGradArgs a{logits, type, ldl, token_mask, T, (int)E, k, renormalize != 0, idx, weight, counts,
-                          grad_weight, grad_loss, dlogits};
+                          grad_weight, grad_loss, dlogits, false, false};
     return status(launch_route_backward(a, cus, on(stream)));
 }
 
@@ -232,12 +229,9 @@ qg_status qmoe_gemm_f8_wgrad(const void *dY, const void *xq, int64_t T, int k_sl
         return QG_ERR_SHAPE;
     if (!aligned(dY, 2) || !aligned(xq, 256) || !aligned(dW, 4))
         return QG_ERR_ALIGN;
-    const int cus = device_cus();
-    if (cus <= 0)
-        return QG_ERR_DEVICE;
     const F8Rows r{T * k_slots, T, order, offsets, (int)P, k_slots, 0};
     return status(launch_f8_wgrad(static_cast<const uint16_t *>(dY), static_cast<const uint8_t *>(xq), dW,
-                                  accumulate != 0, r, N, K, nullptr, cus, on(stream)));
+                                  accumulate != 0, r, N, K, nullptr, on(stream)));
 }
 
 }  // extern "C"

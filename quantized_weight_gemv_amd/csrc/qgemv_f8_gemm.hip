@@ -1,27 +1,32 @@
 // f8 products of many rows: Y[m][n] = sum_k X[m][k] W[n][k] on the matrix
 // cores, for one matrix or for the slots of each expert of a pool.
 //
-// A workgroup owns a tile of BM rows of X times BN rows of W.  Per step of
-// 128 columns (one block: one scale byte a row and side) both operands go
+// A workgroup owns a tile of BM rows of X times BN rows of W.  A step is 64
+// columns (half a block: one scale byte a row and side); its operands go
 // straight from memory into LDS (loads that write LDS: no registers):
-//   * X, row-major: rows of 128 bytes, 16-byte chunk c of row r at position
-//     c ^ ((r / 2) % 8), so that the 16 rows of a quarter of an operand read
+//   * X, row-major: rows of 64 bytes, 16-byte chunk c of row r at position
+//     c ^ ((r / 4) % 4), so that the 16 rows of a quarter of an operand read
 //     touch all 64 banks;
 //   * W, whose tiles are in operand order already: copied as they are; an
 //     operand read is 256 consecutive bytes a quarter wave.
-// Two buffers: while a step is multiplied, the next one's copies are in
-// flight; one barrier a step.
+// A ring of four buffers.  During step t the matrix cores multiply operands
+// that were read from LDS during step t - 1, the operands of t + 1 are read
+// from buffer t + 1, and the copies of step t + 3 are issued into the buffer
+// that step t - 1 was read from.  One barrier a step; before it a wave waits
+// for its own copies of step t + 1 only (all but the youngest step's).
 // 16-bit outputs: v_mfma_scale_f32_32x32x64_f8f6f4 with the two block scales
 // as its scale operands, so the fp32 sums need no further instruction.  fp32
 // outputs: the codes are widened to bf16 with their scale (exact) and
 // multiplied with v_mfma_f32_32x32x16_bf16: half the rate, but products and
 // sums exact to fp32, where the 8-bit instructions keep about 13 bits below
 // the largest of a few neighbouring products.
-// W is the first operand, so a lane holds four consecutive n of a row of Y.
+// W is the first operand, so a lane holds four consecutive n of a row of Y;
+// the tile is turned through LDS for whole-line stores.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "qgemv_f8_internal.h"
 
@@ -33,17 +38,10 @@ struct GemmParams {
     void *Y;
     F8Rows rows;
     int64_t w_scales, x_scales;
-    int64_t units;       // tiles along the rows (grouped: an upper bound)
+    uint32_t units;      // tiles along the rows (grouped: an upper bound)
     int N, cb, x_ls, w_ls, rt, tiles_n;
     bool vec;
 };
-
-template <int N>
-__device__ __forceinline__ void wait_vm()
-{
-    static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
 
 __device__ __forceinline__ void copy16(const uint8_t *from, void *to)
 {
@@ -55,221 +53,344 @@ __device__ __forceinline__ void copy16(const uint8_t *from, void *to)
 template <int WM, int WN, int TM, int TN>
 struct Tile {
     static constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, NT = 64 * WM * WN;
-    static constexpr int XC = BM * 8 / NT, WC = BN * 8 / NT;   // 16-byte copies per thread and step
+    static constexpr int XC = BM * 4 / NT, WC = BN * 4 / NT;   // 16-byte copies per thread and step
 };
 
+// Which tile a workgroup takes.  Workgroups go to the eight XCDs in turn, each
+// with an L2 of its own: an XCD gets a contiguous share of the tiles, in
+// bands of kBand tiles of rows of X (dense), so that the tiles it works on at
+// a time share rows of both operands.
+constexpr int kXcds = 8, kBand = 8;
+
+template <bool GROUPED>
+__device__ __forceinline__ bool tile_of(uint32_t item, uint32_t units, int tiles_n, uint32_t &unit, int &tn)
+{
+    const uint32_t total = units * tiles_n;
+    const uint32_t share = (total + kXcds - 1) / kXcds;
+    const uint32_t lin = (item % kXcds) * share + item / kXcds;
+    if (item / kXcds >= share || lin >= total)
+        return false;
+    if constexpr (GROUPED) {
+        unit = lin / (uint32_t)tiles_n;
+        tn = (int)(lin - unit * tiles_n);
+    } else {
+        const uint32_t band = lin / (uint32_t)(kBand * tiles_n);
+        const uint32_t in = lin - band * kBand * tiles_n;
+        const uint32_t rows = min((uint32_t)kBand, units - band * kBand);
+        tn = (int)(in / rows);
+        unit = band * kBand + (in - (uint32_t)tn * rows);
+    }
+    return true;
+}
+
 template <int WM, int WN, int TM, int TN, typename OUT, bool GROUPED>
-__global__ __launch_bounds__(64 * WM *WN) void gemm_kernel(GemmParams p)
+__global__ __launch_bounds__(64 * WM *WN, TM *TN == 16 ? 1 : 2) void gemm_kernel(GemmParams p)
 {
     using T = Tile<WM, WN, TM, TN>;
     constexpr bool kWide = sizeof(OUT) == 4;
-    __shared__ uint4 X0[T::BM * 8], X1[T::BM * 8], W0[T::BN * 8], W1[T::BN * 8];
-    __shared__ int out_row[T::BM];
+    constexpr int kCopies = T::XC + T::WC;
+    // one variable a buffer: the compiler then knows which copies an operand
+    // read has to wait for (none: the waits are the kernel's own)
+    __shared__ uint4 X0[T::BM * 4], X1[T::BM * 4], X2[T::BM * 4], X3[T::BM * 4];
+    __shared__ uint4 W0[T::BN * 4], W1[T::BN * 4], W2[T::BN * 4], W3[T::BN * 4];
+    __shared__ int out_row[GROUPED ? T::BM : 1];
+    auto xbuf = [&](int q) -> uint4 * { return q == 0 ? X0 : q == 1 ? X1 : q == 2 ? X2 : X3; };
+    auto wbuf = [&](int q) -> uint4 * { return q == 0 ? W0 : q == 1 ? W1 : q == 2 ? W2 : W3; };
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const int r32 = lane & 31, half = lane >> 5;
 
-    const int64_t total = p.units * p.tiles_n;
-    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
-        const int64_t unit = item / p.tiles_n;
-        const int tn = (int)(item - unit * p.tiles_n);
-        F8Unit u{0, unit * T::BM, min((unit + 1) * T::BM, p.rows.rows)};
-        if constexpr (GROUPED) {
-            u = f8_unit(p.rows.offsets, p.rows.P, p.rows.rows, T::BM, unit);
-            if (u.r0 >= u.r1)
-                return;   // uniform over the workgroup
-        }
-        const int n0 = tn * T::BN;
-        const int rows = (int)(u.r1 - u.r0);
+    uint32_t unit;
+    int tn;
+    if (!tile_of<GROUPED>(blockIdx.x, p.units, p.tiles_n, unit, tn))
+        return;
+    F8Unit u{0, (int64_t)unit * T::BM, min((int64_t)(unit + 1) * T::BM, p.rows.rows)};
+    if constexpr (GROUPED) {
+        u = f8_unit(p.rows.offsets, p.rows.P, p.rows.rows, T::BM, unit);
+        if (u.r0 >= u.r1)
+            return;   // past the last unit (uniform over the workgroup)
+    }
+    const int n0 = tn * T::BN;
+    const int rows = (int)(u.r1 - u.r0);
 
-        // rows of X of this thread's copies, and of Y
-        const uint8_t *xsrc[T::XC];
-        auto x_row = [&](int r) -> int64_t {
-            const int64_t at = u.r0 + min(r, rows - 1);
-            if constexpr (!GROUPED)
-                return at;
-            const int s = p.rows.order[at];
-            return s >= 0 && s < p.rows.rows ? min((int64_t)((uint32_t)s / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1)
-                                             : 0;
-        };
-        if constexpr (GROUPED) {
-            for (int r = threadIdx.x; r < T::BM; r += T::NT) {
-                int s = r < rows ? p.rows.order[u.r0 + r] : -1;
-                out_row[r] = s >= 0 && s < p.rows.rows ? s : -1;
-            }
+    // row of X for a row of the tile (rows past its end: the last one, never stored)
+    auto x_row = [&](int r) -> int64_t {
+        const int64_t at = u.r0 + min(r, rows - 1);
+        if constexpr (!GROUPED)
+            return at;
+        const int s = p.rows.order[at];
+        return s >= 0 && s < p.rows.rows ? min((int64_t)((uint32_t)s / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1)
+                                         : 0;
+    };
+    if constexpr (GROUPED) {
+        for (int r = threadIdx.x; r < T::BM; r += T::NT) {
+            const int s = r < rows ? p.rows.order[u.r0 + r] : -1;
+            out_row[r] = s >= 0 && s < p.rows.rows ? s : -1;
         }
+    }
+
+    f16v_t acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[i][j][e] = 0.0f;
+
+    if (!GROUPED || u.e < p.rows.P) {
+        const uint8_t *W = p.W + (GROUPED ? u.e * p.rows.stride : 0);
+        const uint8_t *xsrc[T::XC], *wsrc[T::WC];
 #pragma unroll
         for (int i = 0; i < T::XC; ++i) {
             const int idx = threadIdx.x + T::NT * i;
-            const int r = idx >> 3, ch = (idx & 7) ^ ((r >> 1) & 7);
+            const int r = idx >> 2, ch = (idx & 3) ^ ((r >> 2) & 3);
             xsrc[i] = p.xq + x_row(r) * p.cb * 128 + ch * 16;
         }
-        const uint8_t *W = p.W + (GROUPED ? min(u.e, p.rows.P - 1) * p.rows.stride : 0);
-        const uint8_t *wsrc[T::WC];
 #pragma unroll
         for (int i = 0; i < T::WC; ++i) {
             const int idx = threadIdx.x + T::NT * i;
-            const int t = min(n0 / 16 + (idx >> 7), p.rt - 1);   // rows past the matrix are never stored
-            wsrc[i] = W + (int64_t)t * p.cb * 2048 + (idx & 127) * 16;
+            const int t = min(n0 / 16 + (idx >> 6), p.rt - 1);   // rows past the matrix are never stored
+            wsrc[i] = W + (int64_t)t * p.cb * 2048 + (idx & 63) * 16;
         }
-        // scales: four steps' bytes a word
+        // scales: four blocks' bytes a word, this word and the next
         const uint8_t *xs_src[TM];
-        const uint8_t *ws_src;
 #pragma unroll
         for (int i = 0; i < TM; ++i)
             xs_src[i] = p.xq + p.x_scales + x_row((wm * TM + i) * 32 + r32) * p.x_ls;
         static_assert(128 % (32 * TN) == 0, "a wave's rows of W lie in one block");
-        ws_src = W + p.w_scales + (int64_t)min((n0 + wn * TN * 32) >> 7, (p.N - 1) >> 7) * p.w_ls;
+        const uint8_t *ws_src = W + p.w_scales + (int64_t)min((n0 + wn * TN * 32) >> 7, (p.N - 1) >> 7) * p.w_ls;
+        uint32_t xs[TM], ws, xs_next[TM], ws_next;
+        auto load_scales = [&](int word) {
+            const int at = 4 * min(word, p.x_ls / 4 - 1);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                xs_next[i] = *reinterpret_cast<const uint32_t *>(xs_src[i] + at);
+            ws_next = *reinterpret_cast<const uint32_t *>(ws_src + at);
+        };
 
-        f16v_t acc[TM][TN];
+        const int steps = 2 * p.cb;
+        int ahead = 0;   // the next step to copy; past the last one it is copied again (never read)
+        auto copies = [&](uint4 *X, uint4 *Wb) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+            for (int i = 0; i < T::XC; ++i)
+                copy16(xsrc[i], &X[T::NT * i + 64 * wave]);
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+            for (int i = 0; i < T::WC; ++i)
+                copy16(wsrc[i], &Wb[T::NT * i + 64 * wave]);
+            // no branch: the products of a step would be moved across it
+            const int go = ++ahead < steps ? 1 : 0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    acc[i][j][e] = 0.0f;
-
-        if (!GROUPED || u.e < p.rows.P) {
-            uint32_t xs[TM], ws;
-            auto copies = [&](uint4 *X, uint4 *Wb) {
+            for (int i = 0; i < T::XC; ++i)
+                xsrc[i] += 64 * go;
 #pragma unroll
-                for (int i = 0; i < T::XC; ++i) {
-                    copy16(xsrc[i], &X[T::NT * i + 64 * wave]);
-                    xsrc[i] += 128;
+            for (int i = 0; i < T::WC; ++i)
+                wsrc[i] += 1024 * go;
+        };
+        struct Operands {
+            uint4 x[TM][2], w[TN][2];
+        };
+        auto read = [&](Operands &o, const uint4 *X, const uint4 *Wb) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int ch = 2 * half + q;
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int r = (wm * TM + i) * 32 + r32;
+                    o.x[i][q] = X[r * 4 + (ch ^ ((r >> 2) & 3))];
                 }
 #pragma unroll
-                for (int i = 0; i < T::WC; ++i) {
-                    copy16(wsrc[i], &Wb[T::NT * i + 64 * wave]);
-                    wsrc[i] += 2048;
-                }
-            };
-            auto step = [&](const uint4 *X, const uint4 *Wb) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4 xv[TM][2], wv[TN][2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int ch = 4 * h + 2 * half + q;
-#pragma unroll
-                        for (int i = 0; i < TM; ++i) {
-                            const int r = (wm * TM + i) * 32 + r32;
-                            xv[i][q] = X[r * 8 + (ch ^ ((r >> 1) & 7))];
-                        }
-#pragma unroll
-                        for (int j = 0; j < TN; ++j) {
-                            const int t = (wn * TN + j) * 2 + (r32 >> 4);
-                            wv[j][q] = Wb[t * 128 + ch * 16 + (r32 & 15)];
-                        }
-                    }
-                    if constexpr (!kWide) {
-#pragma unroll
-                        for (int i = 0; i < TM; ++i)
-#pragma unroll
-                            for (int j = 0; j < TN; ++j) {
-                                const i8_t a = {(int)wv[j][0].x, (int)wv[j][0].y, (int)wv[j][0].z, (int)wv[j][0].w,
-                                                (int)wv[j][1].x, (int)wv[j][1].y, (int)wv[j][1].z, (int)wv[j][1].w};
-                                const i8_t b = {(int)xv[i][0].x, (int)xv[i][0].y, (int)xv[i][0].z, (int)xv[i][0].w,
-                                                (int)xv[i][1].x, (int)xv[i][1].y, (int)xv[i][1].z, (int)xv[i][1].w};
-                                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 0, 0, 0,
-                                                                                           (int)ws, 0, (int)xs[i]);
-                            }
-                    } else {
-                        const float wf = f8_scale(ws & 255u);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-#pragma unroll
-                            for (int o = 0; o < 2; ++o) {
-                                bf8_t w[TN];
-#pragma unroll
-                                for (int j = 0; j < TN; ++j)
-                                    w[j] = o ? f8_widen(wv[j][q].z, wv[j][q].w, wf)
-                                             : f8_widen(wv[j][q].x, wv[j][q].y, wf);
-#pragma unroll
-                                for (int i = 0; i < TM; ++i) {
-                                    const float xf = f8_scale(xs[i] & 255u);
-                                    const bf8_t x = o ? f8_widen(xv[i][q].z, xv[i][q].w, xf)
-                                                      : f8_widen(xv[i][q].x, xv[i][q].y, xf);
-#pragma unroll
-                                    for (int j = 0; j < TN; ++j)
-                                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x, acc[i][j], 0, 0,
-                                                                                            0);
-                                }
-                            }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    xs[i] >>= 8;
-                ws >>= 8;
-            };
-            copies(X0, W0);
-            for (int s = 0; s < p.cb; s += 4) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (s + q >= p.cb)
-                        break;   // uniform over the grid
-                    if (q == 0) {
-#pragma unroll
-                        for (int i = 0; i < TM; ++i)
-                            xs[i] = *reinterpret_cast<const uint32_t *>(xs_src[i] + s);
-                        ws = *reinterpret_cast<const uint32_t *>(ws_src + s);
-                    }
-                    wait_vm<0>();        // this wave's copies of the step have landed,
-                    __syncthreads();     // everyone's have, and the other buffer is free
-                    if (s + q + 1 < p.cb)
-                        copies(q & 1 ? X0 : X1, q & 1 ? W0 : W1);
-                    step(q & 1 ? X1 : X0, q & 1 ? W1 : W0);
+                for (int j = 0; j < TN; ++j) {
+                    const int t = (wn * TN + j) * 2 + (r32 >> 4);
+                    o.w[j][q] = Wb[t * 64 + ch * 16 + (r32 & 15)];
                 }
             }
-        }
-
-        __syncthreads();   // out_row is written, and the buffers are free for the next tile
+        };
+        auto multiply = [&](const Operands &o) {
+            if constexpr (!kWide) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int r = (wm * TM + i) * 32 + r32;
-            const int64_t y = GROUPED ? out_row[r] : (r < rows ? u.r0 + r : -1);
-            if (y < 0)
-                continue;
-            OUT *row = static_cast<OUT *>(p.Y) + y * p.N;
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int n = n0 + (wn * TN + j) * 32 + 8 * g + 4 * half;
-                    const float *v = reinterpret_cast<const float *>(&acc[i][j]) + 4 * g;
-                    if (p.vec && n + 4 <= p.N) {
-                        if constexpr (kWide)
-                            *reinterpret_cast<f4_t *>(row + n) = f4_t{v[0], v[1], v[2], v[3]};
-                        else
-                            *reinterpret_cast<uint2 *>(row + n) =
-                                make_uint2(from_f32<OUT>(v[0]).u | (uint32_t)from_f32<OUT>(v[1]).u << 16,
-                                           from_f32<OUT>(v[2]).u | (uint32_t)from_f32<OUT>(v[3]).u << 16);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (n + e < p.N)
-                                row[n + e] = from_f32<OUT>(v[e]);
+                    for (int j = 0; j < TN; ++j) {
+                        const i8_t a = {(int)o.w[j][0].x, (int)o.w[j][0].y, (int)o.w[j][0].z, (int)o.w[j][0].w,
+                                        (int)o.w[j][1].x, (int)o.w[j][1].y, (int)o.w[j][1].z, (int)o.w[j][1].w};
+                        const i8_t b = {(int)o.x[i][0].x, (int)o.x[i][0].y, (int)o.x[i][0].z, (int)o.x[i][0].w,
+                                        (int)o.x[i][1].x, (int)o.x[i][1].y, (int)o.x[i][1].z, (int)o.x[i][1].w};
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 0, 0, 0,
+                                                                                   (int)ws, 0, (int)xs[i]);
                     }
+            } else {
+                const float wf = f8_exponent(ws & 255u);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        bf8_t w[TN];
+#pragma unroll
+                        for (int j = 0; j < TN; ++j)
+                            w[j] = h ? f8_widen(o.w[j][q].z, o.w[j][q].w, wf)
+                                     : f8_widen(o.w[j][q].x, o.w[j][q].y, wf);
+#pragma unroll
+                        for (int i = 0; i < TM; ++i) {
+                            const float xf = f8_exponent(xs[i] & 255u);
+                            const bf8_t x = h ? f8_widen(o.x[i][q].z, o.x[i][q].w, xf)
+                                              : f8_widen(o.x[i][q].x, o.x[i][q].y, xf);
+#pragma unroll
+                            for (int j = 0; j < TN; ++j)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x, acc[i][j], 0, 0, 0);
+                        }
+                    }
+            }
+        };
+
+        load_scales(0);
+        copies(X0, W0);
+        copies(X1, W1);
+        copies(X2, W2);
+        Operands even, odd;
+        wait_vm<2 * kCopies>();
+        bare_barrier();
+        read(even, X0, W0);
+        // one step; q: its buffer
+        auto step = [&](auto number) {
+            constexpr int q = decltype(number)::value;
+            wait_vm<kCopies>();
+            bare_barrier();
+            copies(xbuf((q + 3) & 3), wbuf((q + 3) & 3));
+            read(q & 1 ? even : odd, xbuf((q + 1) & 3), wbuf((q + 1) & 3));
+            multiply(q & 1 ? odd : even);
+            // reads and copies behind the first products: left alone they
+            // gather at the end of the step
+            if constexpr (!kWide) {
+                constexpr int kProducts = TM * TN, kReads = 2 * (TM + TN);
+#pragma unroll
+                for (int m = 0; m < kProducts; ++m) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+                    if (2 * m < kReads)
+                        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // LDS reads
+                    if (m < kCopies)
+                        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // copies
                 }
+            }
+        };
+        // two steps of column block b, whose scales are in bytes b % 4
+        uint32_t xword[TM], wword;
+        auto block = [&](int b, auto number) {
+            constexpr int q = decltype(number)::value;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                xs[i] = xword[i] >> (8 * (b & 3));
+            ws = wword >> (8 * (b & 3));
+            step(std::integral_constant<int, q>{});
+            step(std::integral_constant<int, q + 1>{});
+        };
+        // the scales of a pair of blocks are loaded a pair ahead, before
+        // the copies that the following wait leaves in flight
+        auto take_scales = [&](int b) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                xword[i] = xs_next[i];
+            wword = ws_next;
+            load_scales((b + 2) / 4);
+        };
+        int b = 0;
+        for (; b + 1 < p.cb; b += 2) {
+            take_scales(b);
+            block(b, std::integral_constant<int, 0>{});
+            block(b + 1, std::integral_constant<int, 2>{});
         }
-        if constexpr (GROUPED)
-            __syncthreads();   // out_row is read before the next tile's is written
+        if (b < p.cb) {
+            take_scales(b);
+            block(b, std::integral_constant<int, 0>{});
+        }
+        wait_vm<0>();   // no copy is in flight when the buffers are used again
+    }
+
+    __syncthreads();   // out_row is written, and the buffers are free
+    // A lane has four consecutive n of one row, a wave's store of them
+    // would touch 32 rows.  So 32 rows x 32 TN columns at a time go
+    // through LDS (wave-private, 16-byte chunks swizzled by row) and are
+    // stored whole lines at a time.
+    static_assert(WM * WN == 4 && TN * sizeof(OUT) <= 4 * TM, "each wave stages in an X buffer of its own");
+    constexpr int kRow = 32 * TN * (int)sizeof(OUT), kChunks = kRow / 16;
+    uint4 *stage = xbuf(wave);
+    char *bytes = reinterpret_cast<char *>(stage);
+    constexpr int kPer = 16 / (int)sizeof(OUT);   // elements of a chunk
+    constexpr int kStores = 32 * kChunks / 64;    // per lane and 32 rows
+    const bool whole = p.vec && n0 + T::BN <= p.N && (GROUPED || rows == T::BM);   // no edge in this tile
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int at = (32 * j + 8 * g + 4 * half) * (int)sizeof(OUT);
+                char *to = bytes + r32 * kRow + (((at >> 4) ^ (r32 & (kChunks - 1))) << 4) + (at & 15);
+                const f16v_t &a = acc[i][j];
+                if constexpr (kWide)
+                    *reinterpret_cast<f4_t *>(to) = f4_t{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
+                else
+                    *reinterpret_cast<uint2 *>(to) =
+                        make_uint2(pack2<OUT>(a[4 * g], a[4 * g + 1]), pack2<OUT>(a[4 * g + 2], a[4 * g + 3]));
+            }
+        auto at = [&](int c, int &m, int &n) -> const uint4 & {   // the c-th chunk of this lane: its row and column
+            const int r = (64 * c + lane) / kChunks, ch = (64 * c + lane) % kChunks;
+            m = (wm * TM + i) * 32 + r;
+            n = n0 + wn * TN * 32 + ch * kPer;
+            return stage[r * kChunks + (ch ^ (r & (kChunks - 1)))];
+        };
+        if (whole) {
+            uint4 v[kStores];
+            int m[kStores], n;
+#pragma unroll
+            for (int c = 0; c < kStores; ++c)
+                v[c] = at(c, m[c], n);
+#pragma unroll
+            for (int c = 0; c < kStores; ++c) {
+                const int64_t y = GROUPED ? out_row[m[c]] : u.r0 + m[c];
+                if (!GROUPED || y >= 0)
+                    *reinterpret_cast<uint4 *>(static_cast<OUT *>(p.Y) + y * p.N + n) = v[c];
+            }
+        } else {
+#pragma unroll 1
+            for (int c = 0; c < kStores; ++c) {
+                int m, n;
+                const uint4 v = at(c, m, n);
+                const int64_t y = GROUPED ? out_row[m] : u.r0 + m;
+                if (!(GROUPED ? y >= 0 : m < rows) || n >= p.N)
+                    continue;
+                OUT *to = static_cast<OUT *>(p.Y) + y * p.N + n;
+                if (p.vec) {   // N is a multiple of a chunk
+                    *reinterpret_cast<uint4 *>(to) = v;
+                    continue;
+                }
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if (n + e < p.N) {
+                        if constexpr (kWide)
+                            to[e] = __uint_as_float(w[e]);
+                        else
+                            to[e] = OUT{(uint16_t)(w[e / 2] >> (16 * (e & 1)))};
+                    }
+            }
+        }
     }
 }
 
 template <int WM, int WN, int TM, int TN, typename OUT, bool GROUPED>
-hipError_t launch(GemmParams &p, int cus, hipStream_t stream)
+hipError_t launch(GemmParams &p, hipStream_t stream)
 {
     using T = Tile<WM, WN, TM, TN>;
     p.tiles_n = (int)ceil_div(p.N, T::BN);
-    p.units = GROUPED ? f8_units(p.rows.rows, p.rows.P, T::BM) : ceil_div(p.rows.rows, T::BM);
-    const int64_t items = p.units * p.tiles_n;
-    (void)cus;
+    p.units = (uint32_t)(GROUPED ? f8_units(p.rows.rows, p.rows.P, T::BM) : ceil_div(p.rows.rows, T::BM));
+    const int64_t items = ceil_div((int64_t)p.units * p.tiles_n, kXcds) * kXcds;
+    if (items >= 1 << 24)   // a grid holds fewer than 2^32 threads
+        return hipErrorInvalidValue;
     return launch_kernel(reinterpret_cast<const void *>(&gemm_kernel<WM, WN, TM, TN, OUT, GROUPED>),
-                         dim3((unsigned)std::min<int64_t>(items, 1 << 22)), dim3(T::NT), 0, stream, p);
+                         dim3((unsigned)items), dim3(T::NT), 0, stream, p);
 }
 
 template <typename OUT, bool GROUPED>
@@ -277,10 +398,10 @@ hipError_t choose(GemmParams &p, int cus, hipStream_t stream)
 {
     if constexpr (!GROUPED) {
         if (ceil_div(p.rows.rows, 256) * ceil_div(p.N, 256) >= cus)
-            return launch<2, 4, 4, 2, OUT, GROUPED>(p, cus, stream);
-        return launch<2, 2, 2, 2, OUT, GROUPED>(p, cus, stream);
+            return launch<2, 2, 4, 4, OUT, GROUPED>(p, stream);
+        return launch<2, 2, 2, 2, OUT, GROUPED>(p, stream);
     } else {
-        return launch<2, 2, 1, 2, OUT, GROUPED>(p, cus, stream);
+        return launch<2, 2, 2, 2, OUT, GROUPED>(p, stream);
     }
 }
 
@@ -292,7 +413,7 @@ hipError_t launch_f8_gemm(const uint8_t *W, const uint8_t *xq, void *Y, int y_ty
     const F8Weights f = f8_weights(N, K);
     const F8Acts a = f8_acts(r.x_rows, K);
     GemmParams p{W, xq, Y, r, f.scales, a.scales, 0, (int)N, f.cb, a.ls, f.ls, f.rt, 0,
-                 N % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * type_bytes(y_type) - 1)) == 0};
+                 N * type_bytes(y_type) % 16 == 0 && (reinterpret_cast<uintptr_t>(Y) & 15) == 0};
     if (r.order)
         return y_type == QG_F32   ? choose<float, true>(p, cus, stream)
                : y_type == QG_F16 ? choose<Fp16, true>(p, cus, stream)

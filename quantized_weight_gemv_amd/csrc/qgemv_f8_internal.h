@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "qgemv_f8.h"
 #include "qgemv_internal.h"
@@ -117,6 +118,21 @@ __device__ __forceinline__ void load_row(const T *p, int left, float (&v)[N])
     }
 }
 
+// Two values of a 16-bit type in one word (one instruction for bf16).
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<Fp16>(float a, float b)
+{
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, h2{(_Float16)a, (_Float16)b});
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<Bf16>(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, bf2_t{(__bf16)a, (__bf16)b});
+}
+
 // Scale byte of a block whose largest finite magnitude has the fp32 bits
 // `amax`: the smallest e >= -127 with amax <= 448 * 2^e, 448 = 1.75 * 2^8, as
 // e + 127; 127 for an empty or zero block.  From the bits alone, so it is
@@ -130,31 +146,14 @@ __host__ __device__ __forceinline__ uint32_t f8_scale_byte(uint32_t amax)
     return e < 0 ? 0u : (uint32_t)e;
 }
 
-// 2^(byte - 127) and its reciprocal; byte 0 is the subnormal 2^-127, and the
-// reciprocal of the largest scales the quantizer writes (2^120) is normal.
+// 2^(byte - 127); byte 0 is the subnormal 2^-127.
 __device__ __forceinline__ float f8_scale(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x00400000u); }
 
-// v * 2^-(byte - 127) without an intermediate that leaves fp32's range: 2^127
-// is the largest power, all that byte 0 needs.
+// 2^(127 - byte).
 __device__ __forceinline__ float f8_inverse(uint32_t byte) { return byte >= 254 ? 0x1p-127f : __uint_as_float((254u - byte) << 23); }
 
-// |v| of a finite v, 0 of the others, as bits (ordered like the magnitudes).
-__device__ __forceinline__ uint32_t finite_mag(float v)
-{
-    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
-    return b < 0x7F800000u ? b : 0u;
-}
-
-// Four values, scaled, as e4m3 codes in one word.  The conversion rounds to
-// nearest even and saturates nothing here (the scale keeps |v| <= 448); an
-// infinity becomes NaN (v * 0 is added where the value is not finite, because
-// the conversion would clamp it).
-__device__ __forceinline__ float f8_prepare(float v, float inv)
-{
-    const float s = v * inv;
-    return finite_mag(v) == (__float_as_uint(v) & 0x7FFFFFFFu) ? s : __uint_as_float(0x7FC00000u);
-}
-
+// Four values in the codes' range as one word, rounded to nearest even; a NaN
+// becomes a NaN code.
 __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
 {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -162,8 +161,54 @@ __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d)
     return (uint32_t)w;
 }
 
-// Eight codes (two words) times a power of two as a bf16 operand: exact (four
-// significant bits, bf16's exponent range).
+// Largest value over the eight lanes of a block (data-parallel-primitive
+// moves: neighbours, pairs, halves).
+__device__ __forceinline__ float max_of_8(float v)
+{
+    auto moved = [](float x, auto ctrl) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x),
+                                                                     decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    v = fmaxf(v, moved(v, std::integral_constant<int, 0xB1>{}));
+    v = fmaxf(v, moved(v, std::integral_constant<int, 0x4E>{}));
+    return fmaxf(v, moved(v, std::integral_constant<int, 0x141>{}));
+}
+
+// One lane's 16 values of a block held by eight consecutive lanes: their codes
+// and the block's scale byte.  The maximum passes over NaNs by itself and a
+// NaN stays one through the product and the conversion; an infinity, which
+// would become the scale and the largest code, sends the wave over its values
+// once more with NaNs in the place of whatever is not finite.
+__device__ __forceinline__ uint32_t f8_quantize16(float (&v)[16], uint32_t (&w)[4])
+{
+    auto largest = [&] {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2)
+            m = fmaxf(fmaxf(m, fabsf(v[i])), fabsf(v[i + 1]));
+        return max_of_8(m);
+    };
+    float amax = largest();
+    if (__any(amax == __builtin_inff())) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = fabsf(v[i]) < __builtin_inff() ? v[i] : __builtin_nanf("");
+        amax = largest();
+    }
+    const uint32_t byte = f8_scale_byte(__float_as_uint(amax));
+    const float inv = f8_inverse(byte);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = f8_pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    return byte;
+}
+
+// The scale operand of the widening conversions: they read its exponent field
+// alone, and take 0 as 2^-127.
+__device__ __forceinline__ float f8_exponent(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Eight codes (two words) times a power of two (f8_exponent) as a bf16
+// operand: exact (four significant bits, bf16's exponent range).
 __device__ __forceinline__ bf8_t f8_widen(uint32_t lo, uint32_t hi, float scale)
 {
     const bf2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
@@ -173,6 +218,36 @@ __device__ __forceinline__ bf8_t f8_widen(uint32_t lo, uint32_t hi, float scale)
     bf8_t r;
     r[0] = a[0], r[1] = a[1], r[2] = b[0], r[3] = b[1], r[4] = c[0], r[5] = c[1], r[6] = d[0], r[7] = d[1];
     return r;
+}
+
+// Wait until at most N vector memory operations of this wave are in flight
+// (gfx9 encoding of s_waitcnt: vmcnt in bits 3:0 and 15:14, lgkmcnt in 11:8).
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Wait for this wave's LDS operations alone.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4)); }
+
+// At most N vector memory operations, and no LDS operation.
+template <int N>
+__device__ __forceinline__ void wait_vm_lds()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+// A barrier that waits for no memory operation (the fence of __syncthreads
+// waits for all of them, copies in flight included); nothing is moved across.
+__device__ __forceinline__ void bare_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Where a group's rows are: rows r0 .. r1 - 1 of `order` (or of Y and X, dense),
@@ -260,7 +335,7 @@ hipError_t launch_f8_gemm(const uint8_t *W, const uint8_t *xq, void *Y, int y_ty
 
 size_t f8_wgrad_workspace(int64_t M, int64_t N, int64_t K);
 hipError_t launch_f8_wgrad(const uint16_t *dY, const uint8_t *xq, float *dW, bool accumulate, const F8Rows &r,
-                           int64_t N, int64_t K, float *workspace, int cus, hipStream_t stream);
+                           int64_t N, int64_t K, float *workspace, hipStream_t stream);
 
 struct RouteArgs {
     const void *logits;
@@ -275,6 +350,7 @@ struct RouteArgs {
     int32_t *counts, *offsets, *order;
     float *loss;
     void *workspace;
+    bool vec;   // set by the launcher
 };
 struct RouteGradArgs {
     const void *logits;
@@ -289,6 +365,7 @@ struct RouteGradArgs {
     const int32_t *counts;
     const float *grad_weight, *grad_loss;
     void *dlogits;
+    bool vec, vec_out;   // set by the launcher
 };
 size_t route_workspace(int64_t T, int64_t E);
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);

@@ -15,8 +15,8 @@
 // lose what is 13 bits below (1.2e-5 of the result on normal data, against
 // 7e-9), and the widening hides behind the loads.
 // Activations: packed ones are read from L2 by every workgroup; with 1 to 8
-// tokens in fp16, bf16 or fp32 each wave quantizes the column blocks that it
-// multiplies itself into LDS first (wave-private: no barrier).
+// tokens in fp16, bf16 or fp32 the workgroup quantizes them into LDS first,
+// behind the loads of its first weights.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -27,8 +27,9 @@
 namespace qg {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
+struct Packed {
+    uint8_t u;
+};
 
 struct SkinnyParams {
     const uint8_t *W;
@@ -43,11 +44,14 @@ struct SkinnyParams {
     bool vec;             // rows of Y take whole vectors of four
 };
 
-template <int R, int G>
+// One column block of this wave's operands: W's R row tiles, packed X's G
+// token groups (GX = 0: X is read from LDS when it is multiplied).
+template <int R, int GX>
 struct Block {
     uint4 w[R][2];
-    uint4 x[G][2];
-    uint32_t ws[R], xs[G];
+    uint32_t ws[R];
+    uint4 x[GX ? GX : 1][2];
+    uint32_t xs[GX ? GX : 1];
 };
 
 template <typename T>
@@ -59,8 +63,7 @@ __device__ __forceinline__ void store4(void *Y, int64_t at, const f4_t &v, int l
             *reinterpret_cast<f4_t *>(y) = v;
         else
             *reinterpret_cast<uint2 *>(y) =
-                make_uint2(from_f32<T>(v[0]).u | (uint32_t)from_f32<T>(v[1]).u << 16,
-                           from_f32<T>(v[2]).u | (uint32_t)from_f32<T>(v[3]).u << 16);
+                make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -69,71 +72,39 @@ __device__ __forceinline__ void store4(void *Y, int64_t at, const f4_t &v, int l
     }
 }
 
-// SRC: void = packed activations, else the type of x.
-template <typename SRC, int R, int G, bool GROUPED>
-__global__ __launch_bounds__(kThreads) void skinny_kernel(SkinnyParams p)
+// SRC: Packed, or the type of x; R row tiles of W and G token groups a
+// workgroup; NW waves share K; U column blocks in flight (and U more while
+// those are multiplied).
+template <typename SRC, int R, int G, int NW, int U, bool GROUPED>
+__global__ __launch_bounds__(64 * NW, R * G <= 1 ? 4 : 2) void skinny_kernel(SkinnyParams p)
 {
     constexpr bool kPacked = sizeof(SRC) == 1;
-    constexpr int U = R * G == 1 ? 4 : R * G <= 4 ? 2 : 1;   // column blocks in flight, twice
+    constexpr int GX = kPacked ? G : 0;
     extern __shared__ uint4 lds[];
-    f4_t *part = reinterpret_cast<f4_t *>(lds);                      // [wave][R][G][64]
-    uint4 *codes = lds + kWaves * R * G * 64;                        // [cb][2][32], quantizing
+    f4_t *part = reinterpret_cast<f4_t *>(lds);                      // [2][wave][R][G][64]
+    uint4 *codes = lds + 2 * NW * R * G * 64;                        // [cb][2][32], quantizing
     uint8_t *scales = reinterpret_cast<uint8_t *>(codes + p.cb * 64);   // [cb][8]
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, c = lane >> 4;
-    const int mine = (p.cb - wave + kWaves - 1) / kWaves;   // column blocks wave, wave + 8, ..
-
-    if constexpr (!kPacked) {
-        // lane (c, r) holds columns 16 c .. and 64 + 16 c .. of token r of a
-        // block; a block's largest value is over the four lanes of a token
-        const int m = min(r16 & 7, (int)p.rows.rows - 1);
-        const SRC *row = static_cast<const SRC *>(p.x) + (int64_t)m * p.K;
-        for (int j = 0; j < mine; ++j) {
-            const int cb = wave + kWaves * j;
-            float v[2][16];
-            uint32_t amax = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = 128 * cb + 64 * h + 16 * c;
-                load_row(row + k, p.K - k, v[h]);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    amax = max(amax, finite_mag(v[h][i]));
-            }
-            amax = max(amax, (uint32_t)__shfl_xor((int)amax, 16));
-            amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32));
-            const uint32_t byte = f8_scale_byte(amax);
-            const float inv = f8_inverse(byte);
-            if (r16 < 8) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        w[i] = f8_pack4(f8_prepare(v[h][4 * i], inv), f8_prepare(v[h][4 * i + 1], inv),
-                                        f8_prepare(v[h][4 * i + 2], inv), f8_prepare(v[h][4 * i + 3], inv));
-                    codes[(cb * 2 + h) * 32 + c * 8 + r16] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                if (c == 0)
-                    scales[cb * 8 + r16] = (uint8_t)byte;
-            }
-        }
-    }
+    const int mine = (p.cb - wave + NW - 1) / NW;       // this wave's column blocks: wave, wave + NW, ..
+    const int batches = max(1, (mine + U - 1) / U);     // of U blocks, the last one may be short
 
     const int64_t total = p.units * p.row_groups;
-    for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
-        const int64_t unit = GROUPED ? item / p.row_groups : 0;
-        const int rg = (int)(item - unit * p.row_groups);
-        F8Unit u{0, 0, p.rows.rows};
+    int64_t item = blockIdx.x;
+    if (item >= total)
+        return;
+    F8Unit u{0, 0, p.rows.rows};
+    int64_t y_row[G], x_row[G];   // this lane's rows of Y (-1: none) and of X
+    const uint8_t *W = p.W;
+    auto begin_unit = [&](int64_t unit) {
         if constexpr (GROUPED) {
             u = f8_unit(p.rows.offsets, p.rows.P, p.rows.rows, 16 * G, unit);
             if (u.r0 >= u.r1)
-                return;   // later units are past the end as well (uniform over the workgroup)
+                return;
+            W = p.W + min(u.e, p.rows.P - 1) * p.rows.stride;
         }
-        // this lane's tokens: rows of Y (-1: none) and of X
-        int64_t y_row[G], x_row[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const int64_t at = u.r0 + 16 * g + r16;
@@ -146,111 +117,115 @@ __global__ __launch_bounds__(kThreads) void skinny_kernel(SkinnyParams p)
                 x_row[g] = ok ? min((int64_t)((uint32_t)s / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1) : 0;
             }
         }
+    };
+    begin_unit(GROUPED ? item / p.row_groups : 0);
+    if (GROUPED && u.r0 >= u.r1)
+        return;   // past the last unit (uniform over the workgroup)
 
-        f4_t acc[R][G];
+    using B = Block<R, GX>;
+    auto load_w = [&](B(&b)[U], int rg, int j0) {
+        const int t0 = rg * R;
+        const auto rw = make_rsrc(W + (int64_t)t0 * p.cb * 2048, (int64_t)min(R, p.rt - t0) * p.cb * 2048);
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int cb = wave + NW * max(0, min(j0 + q, mine - 1));   // past the wave's last: that one again, unused
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                // a row tile past the matrix lies outside the descriptor: zeros
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    b[q].w[i][h] = stream_load16(rw, (uint32_t)((i * p.cb + cb) * 2048 + 1024 * h + 16 * lane));
+                b[q].ws[i] = W[p.w_scales + (int64_t)(min(t0 + i, p.rt - 1) >> 3) * p.ls + min(cb, p.cb - 1)];
+            }
+        }
+    };
+    auto load_x = [&](B(&b)[U], int j0) {
+        if constexpr (kPacked) {
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                const int cb = min(wave + NW * max(0, min(j0 + q, mine - 1)), p.cb - 1);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const uint8_t *x = p.xq + (x_row[g] * p.cb + cb) * 128 + 16 * c;
+                    b[q].x[g][0] = *reinterpret_cast<const uint4 *>(x);
+                    b[q].x[g][1] = *reinterpret_cast<const uint4 *>(x + 64);
+                    b[q].xs[g] = p.xq[p.x_scales + x_row[g] * p.ls + cb];
+                }
+            }
+        }
+    };
+
+    f4_t acc[R][G];
+    auto clear = [&] {
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int g = 0; g < G; ++g)
                 acc[i][g] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-        if (!GROUPED || u.e < p.rows.P) {
-            const uint8_t *W = p.W + (GROUPED ? u.e * p.rows.stride : 0);
-            const int t0 = rg * R;
-            const auto rw = make_rsrc(W + (int64_t)t0 * p.cb * 2048, (int64_t)min(R, p.rt - t0) * p.cb * 2048);
-            auto load = [&](Block<R, G>(&b)[U], int j0) {
+    };
+    auto multiply = [&](const B(&b)[U], int j0) {
 #pragma unroll
-                for (int q = 0; q < U; ++q) {
-                    const int cb = wave + kWaves * min(j0 + q, mine - 1);
+        for (int q = 0; q < U; ++q) {
+            if (j0 + q >= mine)
+                break;   // uniform over the wave
+            const int cb = wave + NW * (j0 + q);
+            uint4 xv[G][2];
+            float xs[G];
 #pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        // a row tile past the matrix lies outside the descriptor: zeros
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            b[q].w[i][h] = GROUPED ? [&] {
-                                const auto t = __builtin_amdgcn_raw_buffer_load_b128(
-                                    rw, (uint32_t)((i * p.cb + cb) * 2048 + 1024 * h + 16 * lane), 0, 0);
-                                return make_uint4(t[0], t[1], t[2], t[3]);
-                            }() : stream_load16(rw, (uint32_t)((i * p.cb + cb) * 2048 + 1024 * h + 16 * lane));
-                        b[q].ws[i] = W[p.w_scales + (int64_t)(min(t0 + i, p.rt - 1) >> 3) * p.ls + cb];
-                    }
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        if constexpr (kPacked) {
-                            const uint8_t *x = p.xq + (x_row[g] * p.cb + cb) * 128 + 16 * c;
-                            b[q].x[g][0] = *reinterpret_cast<const uint4 *>(x);
-                            b[q].x[g][1] = *reinterpret_cast<const uint4 *>(x + 64);
-                            b[q].xs[g] = p.xq[p.x_scales + x_row[g] * p.ls + cb];
-                        } else {
-                            b[q].x[g][0] = codes[cb * 64 + c * 8 + (r16 & 7)];
-                            b[q].x[g][1] = codes[cb * 64 + 32 + c * 8 + (r16 & 7)];
-                            b[q].xs[g] = scales[cb * 8 + (r16 & 7)];
-                        }
-                    }
+            for (int g = 0; g < G; ++g)
+                if constexpr (kPacked) {
+                    xv[g][0] = b[q].x[g][0], xv[g][1] = b[q].x[g][1];
+                    xs[g] = f8_exponent(b[q].xs[g]);
+                } else {
+                    // tokens from M on hold what is in LDS: their sums are never stored
+                    xv[g][0] = codes[cb * 64 + c * 8 + (r16 & 7)];
+                    xv[g][1] = codes[cb * 64 + 32 + c * 8 + (r16 & 7)];
+                    xs[g] = f8_exponent(scales[cb * 8 + (r16 & 7)]);
                 }
-            };
-            auto multiply = [&](const Block<R, G>(&b)[U], int j0) {
 #pragma unroll
-                for (int q = 0; q < U; ++q) {
-                    if (j0 + q >= mine)
-                        break;   // uniform over the wave
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int o = 0; o < 2; ++o) {
+                    bf8_t w[R], x[G];
 #pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            bf8_t w[R], x[G];
+                    for (int i = 0; i < R; ++i)
+                        w[i] = o ? f8_widen(b[q].w[i][h].z, b[q].w[i][h].w, f8_exponent(b[q].ws[i]))
+                                 : f8_widen(b[q].w[i][h].x, b[q].w[i][h].y, f8_exponent(b[q].ws[i]));
 #pragma unroll
-                            for (int i = 0; i < R; ++i)
-                                w[i] = o ? f8_widen(b[q].w[i][h].z, b[q].w[i][h].w, f8_scale(b[q].ws[i]))
-                                         : f8_widen(b[q].w[i][h].x, b[q].w[i][h].y, f8_scale(b[q].ws[i]));
+                    for (int g = 0; g < G; ++g)
+                        x[g] = o ? f8_widen(xv[g][h].z, xv[g][h].w, xs[g]) : f8_widen(xv[g][h].x, xv[g][h].y, xs[g]);
 #pragma unroll
-                            for (int g = 0; g < G; ++g)
-                                x[g] = o ? f8_widen(b[q].x[g][h].z, b[q].x[g][h].w, f8_scale(b[q].xs[g]))
-                                         : f8_widen(b[q].x[g][h].x, b[q].x[g][h].y, f8_scale(b[q].xs[g]));
+                    for (int i = 0; i < R; ++i)
 #pragma unroll
-                            for (int i = 0; i < R; ++i)
-#pragma unroll
-                                for (int g = 0; g < G; ++g)
-                                    acc[i][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[g], acc[i][g], 0, 0, 0);
-                        }
+                        for (int g = 0; g < G; ++g)
+                            acc[i][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[g], acc[i][g], 0, 0, 0);
                 }
-            };
-            if (mine > 0) {
-                Block<R, G> b0[U], b1[U];
-                load(b0, 0);
-                for (int j = 0; j < mine; j += 2 * U) {
-                    if (j + U < mine)
-                        load(b1, j + U);
-                    __builtin_amdgcn_sched_barrier(0);   // the next loads stay ahead of the products
-                    multiply(b0, j);
-                    if (j + 2 * U < mine)
-                        load(b0, j + 2 * U);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (j + U < mine)
-                        multiply(b1, j + U);
-                }
-            }
         }
-
-        // D of a 16 x 16 product: lane (c, r) holds rows 4 c .. 4 c + 3 (of W)
-        // of column r (token r)
+    };
+    // D of a 16 x 16 product: lane (c, r) holds rows 4 c .. 4 c + 3 (of W) of
+    // column r (token r).  The R G 64 vectors of four are summed over the
+    // waves through LDS, pair (i, g) by wave (i G + g) % NW.  Two buffers in
+    // turn: one barrier an item.
+    int turn = 0;
+    auto finish = [&](int rg) {
+        f4_t *buf = part + turn * NW * R * G * 64;
+        turn ^= 1;
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                part[((wave * R + i) * G + g) * 64 + lane] = acc[i][g];
-        __syncthreads();
-        // the R G 64 vectors of four are spread over the waves: wave w adds
-        // the pairs (i, g) w, w + 8, ..
+                buf[((wave * R + i) * G + g) * 64 + lane] = acc[i][g];
+        wait_lds();
+        bare_barrier();   // the next row group's loads stay in flight
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int g = 0; g < G; ++g)
-                if (((i * G + g) & (kWaves - 1)) == wave) {
-                    f4_t v = part[(i * G + g) * 64 + lane];
+                if ((i * G + g) % NW == wave) {
+                    f4_t v = buf[(i * G + g) * 64 + lane];
 #pragma unroll
-                    for (int w = 1; w < kWaves; ++w)
-                        v += part[((w * R + i) * G + g) * 64 + lane];
+                    for (int w = 1; w < NW; ++w)
+                        v += buf[((w * R + i) * G + g) * 64 + lane];
                     const int n = (rg * R + i) * 16 + 4 * c;
                     if (y_row[g] >= 0 && n < p.N) {
                         const int64_t at = y_row[g] * p.N + n;
@@ -262,31 +237,136 @@ __global__ __launch_bounds__(kThreads) void skinny_kernel(SkinnyParams p)
                             store4<Bf16>(p.Y, at, v, p.N - n, p.vec);
                     }
                 }
-        __syncthreads();   // part is free again
+        clear();
+    };
+
+    // The batches of `items` row groups from rg on, gridDim.x apart, as one
+    // sequence: the next batch's loads are issued before a batch is multiplied,
+    // across row groups as well.  b0 holds the first batch.  The loads of a
+    // pair of batches stand on one path without branches, so that a wait for
+    // a batch leaves the next one's loads in flight.
+    B b0[U], b1[U];
+    auto run = [&](int rg, int items) {
+        int t = 0;
+        auto turn = [&](B(&cur)[U], B(&nxt)[U], bool more) {
+            const bool last = t + 1 == batches;
+            const int nt = last ? 0 : t + 1, nrg = last ? rg + (int)gridDim.x : rg;
+            if (more) {   // known where it is called
+                load_x(nxt, nt * U);
+                load_w(nxt, nrg, nt * U);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            multiply(cur, t * U);
+            if (last)
+                finish(rg);
+            t = nt, rg = nrg;
+        };
+        int left = items * batches;
+        for (; left > 2; left -= 2) {
+            turn(b0, b1, true);
+            turn(b1, b0, true);
+        }
+        if (left == 2) {
+            turn(b0, b1, true);
+            turn(b1, b0, false);
+        } else {
+            turn(b0, b1, false);
+        }
+    };
+    clear();
+    if constexpr (GROUPED) {
+        // one item after the other: its expert and its tokens have to be found
+        for (;;) {
+            const int rg = (int)(item % p.row_groups);
+            if (u.e < p.rows.P) {
+                load_x(b0, 0);
+                load_w(b0, rg, 0);
+                run(rg, 1);
+            } else {
+                finish(rg);   // no expert: zeros
+            }
+            item += gridDim.x;
+            if (item >= total)
+                return;
+            begin_unit(item / p.row_groups);
+            if (u.r0 >= u.r1)
+                return;
+        }
+    } else {
+        // Quantizing: a lane takes 16 columns of a token's block, eight lanes
+        // the block; the workgroup's threads share the M cb blocks.
+        constexpr int QB = 2;   // of a lane's pieces at a time
+        float raw[kPacked ? 1 : QB][16];
+        const int pieces = 8 * p.cb * (int)p.rows.rows;
+        auto piece = [&](int q, int &m, int &blk, int &chunk) {
+            const int id = threadIdx.x + 64 * NW * q;
+            chunk = id & 7;
+            m = (id >> 3) / p.cb;
+            blk = (id >> 3) - m * p.cb;
+            return id < pieces;   // whole groups of eight lanes
+        };
+        auto load_raw = [&](int q0) {
+            if constexpr (!kPacked) {
+#pragma unroll
+                for (int q = 0; q < QB; ++q) {
+                    int m, blk, chunk;
+                    const bool in = piece(q0 + q, m, blk, chunk);
+                    const int k = 128 * blk + 16 * chunk;
+                    load_row(static_cast<const SRC *>(p.x) + (in ? (int64_t)m * p.K + k : 0), in ? p.K - k : 0,
+                             raw[q]);
+                }
+            }
+        };
+        auto quantize = [&](int q0) {
+            if constexpr (!kPacked) {
+#pragma unroll
+                for (int q = 0; q < QB; ++q) {
+                    int m, blk, chunk;
+                    const bool in = piece(q0 + q, m, blk, chunk);
+                    uint32_t w[4];
+                    const uint32_t byte = f8_quantize16(raw[q], w);
+                    if (in) {
+                        // columns 16 c .. of half h: read by lanes 16 c + r, r % 8 = token
+                        codes[blk * 64 + (chunk >> 2) * 32 + (chunk & 3) * 8 + m] = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (chunk == 0)
+                            scales[blk * 8 + m] = (uint8_t)byte;
+                    }
+                }
+            }
+        };
+        if constexpr (!kPacked)
+            load_raw(0);
+        load_x(b0, 0);
+        load_w(b0, (int)item, 0);
+        if constexpr (!kPacked) {
+            __builtin_amdgcn_sched_barrier(0);   // x first, the weights right behind it, then the conversion
+            quantize(0);
+            for (int q = QB; 64 * NW * q < pieces; q += QB) {
+                load_raw(q);
+                quantize(q);
+            }
+            wait_lds();
+            bare_barrier();   // the weights stay in flight
+        }
+        run((int)item, (p.row_groups - (int)item + (int)gridDim.x - 1) / (int)gridDim.x);
     }
 }
 
-struct Packed {
-    uint8_t u;
-};
-
-template <typename SRC, int R, int G, bool GROUPED>
+template <typename SRC, int R, int G, int NW, int U, bool GROUPED>
 hipError_t launch(SkinnyParams &p, int cus, hipStream_t stream)
 {
     p.row_groups = (p.rt + R - 1) / R;
     p.units = GROUPED ? f8_units(p.rows.rows, p.rows.P, 16 * G) : 1;
-    const size_t lds = (size_t)kWaves * R * G * 1024 + (sizeof(SRC) == 1 ? 0 : (size_t)p.cb * (1024 + 8));
-    const void *fn = reinterpret_cast<const void *>(&skinny_kernel<SRC, R, G, GROUPED>);
+    const size_t lds = (size_t)2 * NW * R * G * 1024 + (sizeof(SRC) == 1 ? 0 : (size_t)p.cb * (1024 + 8));
+    const void *fn = reinterpret_cast<const void *>(&skinny_kernel<SRC, R, G, NW, U, GROUPED>);
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess)
             return e;
     }
-    // quantizing workgroups stay (each repeats the conversion); the others
-    // come and go, so that one's loads cover another's sums
     const int64_t items = p.units * p.row_groups;
-    const int64_t most = sizeof(SRC) == 1 ? (int64_t)1 << 22 : 2LL * cus;
-    return launch_kernel(fn, dim3((unsigned)std::min(items, most)), dim3(kThreads), lds, stream, p);
+    const int64_t most = GROUPED ? (int64_t)1 << 22 : 3LL * cus;
+    return launch_kernel(fn, dim3((unsigned)std::min(items, most)), dim3(64 * NW), lds, stream, p);
 }
 
 }  // namespace
@@ -295,19 +375,19 @@ hipError_t launch_f8_skinny(const uint8_t *W, const uint8_t *xq, const void *x, 
                             const F8Rows &r, int64_t N, int64_t K, int cus, hipStream_t stream)
 {
     const F8Weights f = f8_weights(N, K);
-    SkinnyParams p{W, xq, x, Y, r, f.scales, f8_acts(r.x_rows, K).scales, 1, (int)N, (int)K, f.cb, f.ls, f.rt, 0,
-                   y_type, N % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * type_bytes(y_type) - 1)) == 0};
+    const F8Acts a = f8_acts(r.x_rows, K);
+    SkinnyParams p{W, xq, x, Y, r, f.scales, a.scales, 1, (int)N, (int)K, f.cb, f.ls, f.rt, 0, y_type, N % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * type_bytes(y_type) - 1)) == 0};
     if (x)
-        return x_type == QG_F32   ? launch<float, 1, 1, false>(p, cus, stream)
-               : x_type == QG_F16 ? launch<Fp16, 1, 1, false>(p, cus, stream)
-                                  : launch<Bf16, 1, 1, false>(p, cus, stream);
+        return x_type == QG_F32   ? launch<float, 1, 1, 8, 2, false>(p, cus, stream)
+               : x_type == QG_F16 ? launch<Fp16, 1, 1, 8, 2, false>(p, cus, stream)
+                                  : launch<Bf16, 1, 1, 8, 2, false>(p, cus, stream);
     if (r.order)
-        return launch<Packed, 1, 1, true>(p, cus, stream);
+        return launch<Packed, 1, 1, 4, 1, true>(p, cus, stream);
     if (r.rows <= 16)
-        return launch<Packed, 1, 1, false>(p, cus, stream);
+        return launch<Packed, 1, 1, 8, 2, false>(p, cus, stream);
     if (r.rows <= 32)
-        return launch<Packed, 1, 2, false>(p, cus, stream);
-    return launch<Packed, 2, 4, false>(p, cus, stream);
+        return launch<Packed, 1, 2, 8, 2, false>(p, cus, stream);
+    return launch<Packed, 1, 4, 8, 2, false>(p, cus, stream);
 }
 
 }  // namespace qg

@@ -13,22 +13,29 @@
 // banks, in eight segments of 32 bytes; segment s of row r is at position
 // s ^ 2 (r % 4), so that the four rows and two segments that half a wave reads
 // lie in different banks.
-// A workgroup owns a 128 x 128 tile of dW, which is one block of X's scales;
-// dY's rows go straight from memory into LDS.  With few tiles the rows are
-// split among workgroups, whose sums are added by a second kernel in a fixed
-// order (workspace; no atomics).
+// A workgroup of 2 x 2 waves owns a tile of 64 TN rows x 64 TM columns of dW.
+// A step is 32 rows of both operands; dY's go straight from memory into LDS.
+// A ring of four buffers: during step t the products run on operands read
+// from buffers t and t + 1 (16 rows ahead), X's codes of step t + 3 are
+// widened into their buffer, dY's copies of step t + 3 and the loads of X's
+// codes of step t + 4 are issued.  One barrier a step.
+// Tiles beyond whole rounds of the card's compute units are split along the
+// rows among the units that would be idle; their parts go to the workspace
+// and a second kernel adds them in a fixed order (no atomics).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "qgemv_f8_internal.h"
 
 namespace qg {
 namespace {
 
-constexpr int kStep = 64;     // rows per step
+constexpr int kStep = 32;     // rows per step
 constexpr int kThreads = 256;
+constexpr int kCus = 256;     // compute units that a round of tiles fills
 
 typedef short s4_t __attribute__((ext_vector_type(4)));
 typedef short s8_t __attribute__((ext_vector_type(8)));
@@ -36,12 +43,15 @@ typedef short s8_t __attribute__((ext_vector_type(8)));
 struct WgradParams {
     const uint16_t *dY;
     const uint8_t *xq;
-    float *dW;            // or the partial sums [splits][N][K]
+    float *dW;
+    float *part;          // [split tiles][parts][BN][BK]
     F8Rows rows;
     int64_t x_scales;
     int N, K, cb, x_ls;
-    int tiles_n, splits;
-    int64_t split_rows;   // rows of a split, a multiple of kStep
+    int tiles_n, tiles;   // tiles of one matrix
+    int whole;            // dense: tiles that are not split (the first ones)
+    int parts;            // of each of the others
+    int64_t part_rows;    // rows of a part, a multiple of kStep
     bool accumulate, vec;
 };
 
@@ -49,173 +59,299 @@ __device__ const uint4 g_zero = {0u, 0u, 0u, 0u};
 
 __device__ __forceinline__ int seg_at(int row, int seg) { return seg ^ (2 * (row & 3)); }
 
-// ALIGNED: rows of dY start at multiples of 16 bytes.
-template <bool ALIGNED, bool GROUPED>
-__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p)
+// ALIGNED: rows of dY start at multiples of 16 bytes and are copied straight
+// into LDS; otherwise they go through registers, like X's.
+template <int TM, int TN, bool ALIGNED, bool GROUPED>
+__global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradParams p)
 {
-    __shared__ uint4 Y0[kStep * 16], Y1[kStep * 16], X0[kStep * 16], X1[kStep * 16];
+    constexpr int BK = 64 * TM, BN = 64 * TN;
+    constexpr int YC = BN / 8, XC = BK / 16;                 // chunks of 16 bytes of a row: dY's, X's codes
+    constexpr int NY = YC * kStep / kThreads, NX = XC * kStep / kThreads;   // per thread and step
+    __shared__ uint4 Y0[kStep * YC], Y1[kStep * YC], Y2[kStep * YC], Y3[kStep * YC];
+    __shared__ uint4 X0[kStep * XC * 2], X1[kStep * XC * 2], X2[kStep * XC * 2], X3[kStep * XC * 2];
+    auto ybuf = [&](int q) -> uint4 * { return q == 0 ? Y0 : q == 1 ? Y1 : q == 2 ? Y2 : Y3; };
+    auto xbuf = [&](int q) -> uint4 * { return q == 0 ? X0 : q == 1 ? X1 : q == 2 ? X2 : X3; };
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave & 1, wk = wave >> 1;
 
-    // blockIdx: (expert or split, column block of X, tile of dY's columns)
-    const int tn = blockIdx.x % p.tiles_n;
-    const int kb = (int)(blockIdx.x / p.tiles_n) % p.cb;
-    const int part = (int)(blockIdx.x / p.tiles_n) / p.cb;
-    const int n0 = tn * 128, k0 = kb * 128;
-    int64_t r0, r1;
-    float *out = p.dW + (int64_t)part * p.N * p.K;
+    // blockIdx.x: dense: the whole tiles, then the others' parts; else
+    // (expert, tile)
+    int tile, part = -1;
+    int64_t r0 = 0, r1 = p.rows.rows;
+    float *out = p.dW;
     if constexpr (GROUPED) {
-        const int64_t all = p.rows.rows;
-        r0 = min(max((int64_t)p.rows.offsets[part], (int64_t)0), all);
-        r1 = max(r0, min(max((int64_t)p.rows.offsets[part + 1], (int64_t)0), all));
+        const int e = blockIdx.x / p.tiles;
+        tile = blockIdx.x - e * p.tiles;
+        r0 = min(max((int64_t)p.rows.offsets[e], (int64_t)0), p.rows.rows);
+        r1 = max(r0, min(max((int64_t)p.rows.offsets[e + 1], (int64_t)0), p.rows.rows));
         if (r0 == r1 && p.accumulate)
             return;
+        out += (int64_t)e * p.N * p.K;
     } else {
-        r0 = min(part * p.split_rows, p.rows.rows);
-        r1 = min(r0 + p.split_rows, p.rows.rows);
+        tile = blockIdx.x;
+        if (tile >= p.whole) {
+            part = (tile - p.whole) % p.parts;
+            tile = p.whole + (tile - p.whole) / p.parts;
+            r0 = min(part * p.part_rows, p.rows.rows);
+            r1 = min(r0 + p.part_rows, p.rows.rows);
+        }
     }
+    const int n0 = (tile % p.tiles_n) * BN, k0 = (tile / p.tiles_n) * BK;
 
-    // row of dY and of X of the at-th row; -1: none (zeros)
-    auto rows_of = [&](int64_t at, int64_t &y, int64_t &x) {
-        y = x = at < r1 ? at : -1;
+    // Rows are numbered from r0 on, 0 .. count - 1.  Rows past the end, and
+    // slots that name no row, become zeros: dY's are read from g_zero, X's
+    // codes are masked.  No branch: the loads of a step stay in one sequence,
+    // which the waits below count.
+    const int count = (int)(r1 - r0);
+    const uint8_t *const dY = reinterpret_cast<const uint8_t *>(p.dY);
+    const uint8_t *const zero = reinterpret_cast<const uint8_t *>(&g_zero);
+    const int64_t y_bytes = 2LL * p.N, x_bytes = 128LL * p.cb;
+    auto pick = [](bool ok, const uint8_t *a, const uint8_t *b) {
+        return reinterpret_cast<const uint8_t *>(ok ? reinterpret_cast<uintptr_t>(a) : reinterpret_cast<uintptr_t>(b));
+    };
+    // this thread's chunks: row inside a step, column
+    int y_r[NY], y_n[NY], x_r[NX];
+    const uint8_t *y_at[NY], *x_at[NX], *s_at[NX];   // dense: row r0 + r; grouped: row 0
+#pragma unroll
+    for (int i = 0; i < NY; ++i) {
+        const int idx = threadIdx.x + kThreads * i, pos = idx % YC;
+        y_r[i] = idx / YC;
+        y_n[i] = n0 + 8 * (ALIGNED ? 2 * seg_at(y_r[i], pos >> 1) + (pos & 1) : pos);
+        y_at[i] = dY + (GROUPED ? 0 : r0 + y_r[i]) * y_bytes + 2LL * y_n[i];
+    }
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+        const int idx = threadIdx.x + kThreads * i;
+        x_r[i] = idx / XC;
+        const int col = k0 + 16 * (idx % XC), blk = min(col >> 7, p.cb - 1);
+        x_at[i] = p.xq + (GROUPED ? 0 : r0 + x_r[i]) * x_bytes + 128LL * blk + (col & 127);
+        s_at[i] = p.xq + p.x_scales + (GROUPED ? 0 : r0 + x_r[i]) * (int64_t)p.x_ls + blk;
+    }
+    int y_slot[NY], x_slot[NX];   // grouped: slots of the step whose loads come next
+    auto load_y_slots = [&](int m) {
         if constexpr (GROUPED) {
-            const int s = at < r1 ? p.rows.order[at] : -1;
-            const bool ok = s >= 0 && s < p.rows.rows;
-            y = ok ? s : -1;
-            x = ok ? min((int64_t)((uint32_t)s / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1) : -1;
+#pragma unroll
+            for (int i = 0; i < NY; ++i)
+                y_slot[i] = p.rows.order[r0 + min(m + y_r[i], count - 1)];
         }
     };
-    // copies of dY: thread -> (row, 16-byte position) idx / 16, idx % 16
-    auto copy_y = [&](uint4 *Y, int64_t m) {
+    auto load_x_slots = [&](int m) {
+        if constexpr (GROUPED) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int idx = threadIdx.x + kThreads * i;
-            const int r = idx >> 4, pos = idx & 15;
-            const int n = n0 + 8 * (2 * seg_at(r, pos >> 1) + (pos & 1));
-            int64_t y, x;
-            rows_of(m + r, y, x);
-            const uint16_t *src = p.dY + y * p.N + n;
-            if constexpr (ALIGNED) {
-                const void *from = y >= 0 && n < p.N ? static_cast<const void *>(src) : &g_zero;
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                                 (__attribute__((address_space(3))) void *)&Y[kThreads * i + 64 * wave],
-                                                 16, 0, 0);
-            } else {
-                uint32_t w[4];
+            for (int i = 0; i < NX; ++i)
+                x_slot[i] = p.rows.order[r0 + min(m + x_r[i], count - 1)];
+        }
+    };
+    auto is_slot = [&](int s) { return (uint32_t)s < (uint32_t)p.rows.rows; };
+    auto y_from = [&](int i, int m, bool &ok) -> const uint8_t * {
+        ok = (m + y_r[i] < count) & (y_n[i] < p.N);
+        if constexpr (GROUPED) {
+            ok &= is_slot(y_slot[i]);
+            return y_at[i] + (ok ? y_slot[i] : 0) * y_bytes;
+        }
+        return y_at[i] + m * y_bytes;
+    };
+    // dY straight into LDS: thread -> (row, 16-byte position)
+    auto copy_y = [&](uint4 *Y, int m) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t lo = y >= 0 && n + 2 * e < p.N ? src[2 * e] : 0u;
-                    const uint32_t hi = y >= 0 && n + 2 * e + 1 < p.N ? src[2 * e + 1] : 0u;
-                    w[e] = lo | hi << 16;
+        for (int i = 0; i < NY; ++i) {
+            bool ok;
+            const uint8_t *at = y_from(i, m, ok);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)pick(ok, at, zero),
+                                             (__attribute__((address_space(3))) void *)&Y[kThreads * i + 64 * wave],
+                                             16, 0, 0);
+        }
+    };
+    // or through registers
+    uint4 yreg[NY];
+    auto load_y = [&](int m) {
+#pragma unroll
+        for (int i = 0; i < NY; ++i) {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            bool ok;
+            const uint8_t *at = y_from(i, m, ok);
+            if (ok) {
+                if (y_n[i] + 8 <= p.N) {
+                    const Raw16 raw = *reinterpret_cast<const Raw16 *>(at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = raw.w[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (y_n[i] + e < p.N)
+                            w[e / 2] |= (uint32_t) reinterpret_cast<const uint16_t *>(at)[e] << (16 * (e & 1));
                 }
-                Y[idx] = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            yreg[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     };
-    // codes of X: thread -> (row, segment) idx / 8, idx % 8
-    uint4 codes[2];
-    float scale[2];
-    auto load_x = [&](int64_t m) {
+    auto store_y = [&](uint4 *Y) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int idx = threadIdx.x + kThreads * i;
-            int64_t y, x;
-            rows_of(m + (idx >> 3), y, x);
-            codes[i] = make_uint4(0u, 0u, 0u, 0u);
-            scale[i] = 1.0f;
-            if (x >= 0) {
-                codes[i] = *reinterpret_cast<const uint4 *>(p.xq + (x * p.cb + kb) * 128 + (idx & 7) * 16);
-                scale[i] = f8_scale(p.xq[p.x_scales + x * p.x_ls + kb]);
+        for (int i = 0; i < NY; ++i) {
+            const int ch = (threadIdx.x + kThreads * i) % YC;
+            Y[y_r[i] * YC + 2 * seg_at(y_r[i], ch >> 1) + (ch & 1)] = yreg[i];
+        }
+    };
+    // X: thread -> (row, 16 columns); columns past the last block repeat it
+    // (never stored)
+    uint4 codes[NX];
+    uint32_t sbyte[NX], keep[NX];
+    auto load_x = [&](int m) {
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            bool ok = m + x_r[i] < count;
+            int64_t row = m;
+            if constexpr (GROUPED) {
+                ok &= is_slot(x_slot[i]);
+                row = min((int64_t)((uint32_t)(ok ? x_slot[i] : 0) / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1);
             }
+            codes[i] = *reinterpret_cast<const uint4 *>(pick(ok, x_at[i] + row * x_bytes, p.xq));
+            sbyte[i] = *pick(ok, s_at[i] + row * p.x_ls, p.xq);
+            keep[i] = ok ? ~0u : 0u;
         }
     };
     auto store_x = [&](uint4 *X) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int idx = threadIdx.x + kThreads * i;
-            const int r = idx >> 3;
-            const int at = r * 16 + 2 * seg_at(r, idx & 7);
-            X[at] = __builtin_bit_cast(uint4, f8_widen(codes[i].x, codes[i].y, scale[i]));
-            X[at + 1] = __builtin_bit_cast(uint4, f8_widen(codes[i].z, codes[i].w, scale[i]));
+        for (int i = 0; i < NX; ++i) {
+            const int at = x_r[i] * XC * 2 + 2 * seg_at(x_r[i], (threadIdx.x + kThreads * i) % XC);
+            // what was loaded a step ago is first touched here: without the
+            // pin its users move up behind the load and wait for it there
+            asm volatile("" : "+v"(sbyte[i]), "+v"(codes[i].x), "+v"(codes[i].y), "+v"(codes[i].z), "+v"(codes[i].w));
+            const float s = f8_exponent(sbyte[i]);
+            const uint32_t k = keep[i];
+            X[at] = __builtin_bit_cast(uint4, f8_widen(codes[i].x & k, codes[i].y & k, s));
+            X[at + 1] = __builtin_bit_cast(uint4, f8_widen(codes[i].z & k, codes[i].w & k, s));
         }
     };
-    // eight consecutive rows 16 q + 8 (lane / 32) .. of column 32 t + lane % 32
-    auto operand = [&](const uint4 *S, int q, int t) -> bf8_t {
+    // eight consecutive rows 16 h + 8 (lane / 32) .. of column 32 t + lane % 32
+    auto operand = [&](const uint4 *S, int row_bytes, int h, int t) -> bf8_t {
         const int i = lane & 15;
         const int seg = 2 * t + ((lane >> 4) & 1);
         const char *base = reinterpret_cast<const char *>(S);
         s4_t v[2];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
-            const int row = 16 * q + 8 * (lane >> 5) + 4 * o + (i >> 2);
+            const int row = 16 * h + 8 * (lane >> 5) + 4 * o + (i >> 2);
             v[o] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4_t *)(
-                base + row * 256 + 32 * seg_at(row, seg) + 8 * (i & 3)));
+                base + row * row_bytes + 32 * seg_at(row, seg) + 8 * (i & 3)));
         }
         const s8_t w = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
         return __builtin_bit_cast(bf8_t, w);
     };
+    struct Operands {
+        bf8_t x[TM], y[TN];
+    };
+    auto read = [&](Operands &o, const uint4 *X, const uint4 *Y, int h) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            o.x[i] = operand(X, XC * 32, h, wk * TM + i);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            o.y[j] = operand(Y, YC * 16, h, wn * TN + j);
+    };
 
-    f16v_t acc[2][2];
+    f16v_t acc[TM][TN];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 acc[i][j][e] = 0.0f;
+    auto multiply = [&](const Operands &o) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.x[i], o.y[j], acc[i][j], 0, 0, 0);
+    };
 
-    auto multiply = [&](const uint4 *Y, const uint4 *X) {
-#pragma unroll
-        for (int q = 0; q < kStep / 16; ++q) {
-            bf8_t x[2], y[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                x[i] = operand(X, q, wk * 2 + i);
-                y[i] = operand(Y, q, wn * 2 + i);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
-        }
-    };
-    auto turn = [&](int64_t m, uint4 *Y, uint4 *X, uint4 *Yn) {
-        store_x(X);
-        __builtin_amdgcn_s_waitcnt((0 & 15) | (7 << 4) | (15 << 8));   // this wave's copies have landed
-        __syncthreads();
-        if (m + kStep < r1) {
-            copy_y(Yn, m + kStep);
-            load_x(m + kStep);
-        }
-        multiply(Y, X);
-    };
     if (r0 < r1) {
-        copy_y(Y0, r0);
-        load_x(r0);
-        for (int64_t m = r0; m < r1; m += 2 * kStep) {
-            turn(m, Y0, X0, Y1);
-            if (m + kStep < r1)
-                turn(m + kStep, Y1, X1, Y0);
+        // Vector memory operations of a step (a lower bound): what may still
+        // be in flight when the copies issued a step earlier, and all before
+        // them, have to have landed.
+        constexpr int kOps = (ALIGNED ? NY : 0) + 2 * NX;
+        auto fill = [&](int q) {   // before the loop: buffer q
+            load_y_slots(q * kStep);
+            load_x_slots(q * kStep);
+            if constexpr (ALIGNED)
+                copy_y(ybuf(q), q * kStep);
+            else
+                load_y(q * kStep);
+            load_x(q * kStep);
+            if constexpr (!ALIGNED)
+                store_y(ybuf(q));
+            store_x(xbuf(q));
+        };
+        fill(0);
+        fill(1);
+        fill(2);
+        // in registers at the start of a step that multiplies rows m ..: X's
+        // codes (and dY's, unaligned) of m + 3 steps, the slots of what is
+        // loaded next
+        load_x_slots(3 * kStep);
+        load_x(3 * kStep);
+        load_x_slots(4 * kStep);
+        load_y_slots(3 * kStep);
+        if constexpr (!ALIGNED) {
+            load_y(3 * kStep);
+            load_y_slots(4 * kStep);
+        }
+        Operands first, second;
+        wait_vm_lds<0>();
+        bare_barrier();
+        read(first, X0, Y0, 0);
+        auto step = [&](int m, auto number) {
+            constexpr int q = decltype(number)::value;
+            wait_vm_lds<kOps>();   // and this wave's LDS writes are done
+            bare_barrier();
+            // buffer (q + 3) % 4 was last read in the step before
+            if constexpr (ALIGNED) {
+                copy_y(ybuf((q + 3) & 3), m + 3 * kStep);
+                load_y_slots(m + 4 * kStep);
+            } else {
+                store_y(ybuf((q + 3) & 3));
+                load_y(m + 4 * kStep);
+                load_y_slots(m + 5 * kStep);
+            }
+            store_x(xbuf((q + 3) & 3));
+            load_x(m + 4 * kStep);
+            load_x_slots(m + 5 * kStep);
+            read(second, xbuf(q), ybuf(q), 1);
+            multiply(first);
+            read(first, xbuf((q + 1) & 3), ybuf((q + 1) & 3), 0);
+            multiply(second);
+        };
+        // whole rounds of four steps: rows past the end are zeros
+        for (int m = 0; m < count; m += 4 * kStep) {
+            step(m, std::integral_constant<int, 0>{});
+            step(m + kStep, std::integral_constant<int, 1>{});
+            step(m + 2 * kStep, std::integral_constant<int, 2>{});
+            step(m + 3 * kStep, std::integral_constant<int, 3>{});
         }
     }
 
-    // lane: columns n of dY (lane % 32), four consecutive k each
+    // lane: column n of dY (lane % 32), four consecutive k each
+    float *tile_out = part < 0 ? nullptr
+                               : p.part + ((int64_t)(tile - p.whole) * p.parts + part) * BN * BK;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int n = n0 + (wn * 2 + j) * 32 + (lane & 31);
-        if (n >= p.N)
+    for (int j = 0; j < TN; ++j) {
+        const int nn = (wn * TN + j) * 32 + (lane & 31);
+        if (n0 + nn >= p.N)
             continue;
-        float *row = out + (int64_t)n * p.K;
+        float *row = out + (int64_t)(n0 + nn) * p.K;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int k = k0 + (wk * 2 + i) * 32 + 8 * g + 4 * (lane >> 5);
-                const float *v = reinterpret_cast<const float *>(&acc[i][j]) + 4 * g;
-                if (p.vec && k + 4 <= p.K) {
-                    f4_t w = {v[0], v[1], v[2], v[3]};
+                const int kk = (wk * TM + i) * 32 + 8 * g + 4 * (lane >> 5);
+                const int k = k0 + kk;
+                f4_t w = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+                if (part >= 0) {
+                    *reinterpret_cast<f4_t *>(tile_out + nn * BK + kk) = w;
+                } else if (p.vec && k + 4 <= p.K) {
                     if (p.accumulate)
                         w += *reinterpret_cast<const f4_t *>(row + k);
                     *reinterpret_cast<f4_t *>(row + k) = w;
@@ -223,7 +359,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (k + e < p.K)
-                            row[k + e] = v[e] + (p.accumulate ? row[k + e] : 0.0f);
+                            row[k + e] = w[e] + (p.accumulate ? row[k + e] : 0.0f);
                 }
             }
     }
@@ -232,68 +368,89 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradParams p)
 struct JoinParams {
     const float *part;
     float *dW;
-    int64_t n;
-    int splits;
+    int N, K, BN, BK, tiles_n, whole, parts;
     bool accumulate;
 };
 
+// A workgroup per four rows of a split tile, a lane per column.
 __global__ __launch_bounds__(256) void join_kernel(JoinParams p)
 {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.n; i += (int64_t)gridDim.x * 256) {
-        float v = p.accumulate ? p.dW[i] : 0.0f;
-        for (int s = 0; s < p.splits; ++s)
-            v += p.part[s * p.n + i];
-        p.dW[i] = v;
+    const int tile = blockIdx.x / (p.BN / 4), group = blockIdx.x % (p.BN / 4);
+    const int n0 = ((p.whole + tile) % p.tiles_n) * p.BN, k0 = ((p.whole + tile) / p.tiles_n) * p.BK;
+    const float *from = p.part + (int64_t)tile * p.parts * p.BN * p.BK;
+    for (int i = threadIdx.x; i < 4 * p.BK; i += 256) {
+        const int nn = 4 * group + i / p.BK, kk = i % p.BK;
+        const int n = n0 + nn, k = k0 + kk;
+        if (n >= p.N || k >= p.K)
+            continue;
+        float *to = p.dW + (int64_t)n * p.K + k;
+        float v = p.accumulate ? *to : 0.0f;
+        for (int s = 0; s < p.parts; ++s)
+            v += from[((int64_t)s * p.BN + nn) * p.BK + kk];
+        *to = v;
     }
 }
 
-// Splits of the rows: enough for two workgroups on each of 256 CUs, at least
-// 512 rows each.
-int splits_of(int64_t M, int64_t N, int64_t K)
+// How a dense dW is cut: tiles of 256 x 256 where they fill most of a round
+// of compute units, else of 128 x 128; the tiles beyond whole rounds in as
+// many parts as idle units allow, of at least 256 rows.
+struct Cut {
+    int size, tiles_n, tiles, whole, parts;
+};
+
+Cut cut_of(int64_t M, int64_t N, int64_t K)
 {
-    const int64_t tiles = ceil_div(N, 128) * ceil_div(K, 128);
-    const int64_t want = std::min<int64_t>(512 / std::max<int64_t>(1, tiles), M / 512);
-    return (int)std::max<int64_t>(1, want);
+    Cut c;
+    c.size = ceil_div(N, 256) * ceil_div(K, 256) >= kCus * 3 / 4 ? 256 : 128;
+    c.tiles_n = (int)ceil_div(N, c.size);
+    c.tiles = (int)(c.tiles_n * ceil_div(K, c.size));
+    const int round = c.size == 256 ? kCus : 2 * kCus;   // two workgroups of the small tiles a unit
+    const int rest = c.tiles % round;
+    c.parts = rest ? (int)std::min<int64_t>(round / rest, M / 256) : 1;
+    if (c.parts < 2)
+        c.parts = 1;
+    c.whole = c.parts > 1 ? c.tiles - rest : c.tiles;
+    return c;
 }
 
-template <bool GROUPED>
-hipError_t launch(const WgradParams &p, int64_t parts, hipStream_t stream)
+template <int T, bool GROUPED>
+hipError_t launch(const WgradParams &p, int64_t wgs, hipStream_t stream)
 {
     const bool al = p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.dY) & 15) == 0;
-    const void *fn = al ? reinterpret_cast<const void *>(&wgrad_kernel<true, GROUPED>)
-                        : reinterpret_cast<const void *>(&wgrad_kernel<false, GROUPED>);
-    return launch_kernel(fn, dim3((unsigned)(parts * p.tiles_n * p.cb)), dim3(kThreads), 0, stream, p);
+    const void *fn = al ? reinterpret_cast<const void *>(&wgrad_kernel<T, T, true, GROUPED>)
+                        : reinterpret_cast<const void *>(&wgrad_kernel<T, T, false, GROUPED>);
+    return launch_kernel(fn, dim3((unsigned)wgs), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace
 
 size_t f8_wgrad_workspace(int64_t M, int64_t N, int64_t K)
 {
-    const int s = splits_of(M, N, K);
-    return s > 1 ? (size_t)s * N * K * sizeof(float) : 0;
+    const Cut c = cut_of(M, N, K);
+    return (size_t)(c.tiles - c.whole) * c.parts * c.size * c.size * sizeof(float);
 }
 
 hipError_t launch_f8_wgrad(const uint16_t *dY, const uint8_t *xq, float *dW, bool accumulate, const F8Rows &r,
-                           int64_t N, int64_t K, float *workspace, int cus, hipStream_t stream)
+                           int64_t N, int64_t K, float *workspace, hipStream_t stream)
 {
     const F8Acts a = f8_acts(r.x_rows, K);
-    WgradParams p{dY, xq, dW, r, a.scales, (int)N, (int)K, a.cb, a.ls, (int)ceil_div(N, 128), 1, r.rows, accumulate,
+    WgradParams p{dY, xq, dW, workspace, r, a.scales, (int)N, (int)K, a.cb, a.ls, 0, 0, 0, 1, r.rows, accumulate,
                   K % 4 == 0 && (reinterpret_cast<uintptr_t>(dW) & 15) == 0};
-    if (r.order)
-        return launch<true>(p, r.P, stream);
-    p.splits = splits_of(r.rows, N, K);
-    if (p.splits == 1)
-        return launch<false>(p, 1, stream);
-    p.split_rows = ceil_div(ceil_div(r.rows, p.splits), kStep) * kStep;
-    p.dW = workspace;
-    p.accumulate = false;
-    p.vec = K % 4 == 0;
-    const hipError_t e = launch<false>(p, p.splits, stream);
-    if (e != hipSuccess)
+    if (r.order) {
+        p.tiles_n = (int)ceil_div(N, 128);
+        p.tiles = (int)(p.tiles_n * ceil_div(K, 128));
+        return launch<2, true>(p, (int64_t)r.P * p.tiles, stream);
+    }
+    const Cut c = cut_of(r.rows, N, K);
+    p.tiles_n = c.tiles_n, p.tiles = c.tiles, p.whole = c.whole, p.parts = c.parts;
+    p.part_rows = ceil_div(ceil_div(r.rows, c.parts), kStep) * kStep;
+    const int64_t wgs = c.whole + (int64_t)(c.tiles - c.whole) * c.parts;
+    const hipError_t e = c.size == 256 ? launch<4, false>(p, wgs, stream) : launch<2, false>(p, wgs, stream);
+    if (e != hipSuccess || c.whole == c.tiles)
         return e;
-    const JoinParams j{workspace, dW, N * K, p.splits, accumulate};
+    const JoinParams j{workspace, dW, (int)N, (int)K, c.size, c.size, c.tiles_n, c.whole, c.parts, accumulate};
     return launch_kernel(reinterpret_cast<const void *>(&join_kernel),
-                         dim3((unsigned)std::min<int64_t>(ceil_div(j.n, 256), 8LL * cus)), dim3(256), 0, stream, j);
+                         dim3((unsigned)((c.tiles - c.whole) * (c.size / 4))), dim3(256), 0, stream, j);
 }
 
 }  // namespace qg

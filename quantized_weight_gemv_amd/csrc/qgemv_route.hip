@@ -25,8 +25,8 @@
 namespace qg {
 namespace {
 
-constexpr int kChunkTokens = 64;   // tokens of a workgroup
-constexpr int kWaves = 8;
+constexpr int kChunkTokens = 64;   // tokens of a workgroup: the bits of a mask
+constexpr int kWaves = 16;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kBins = kMaxExperts + 1;   // the last: slots without an expert
 
@@ -45,56 +45,159 @@ __device__ __forceinline__ float value_of(uint32_t key)
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
+// Reductions over the wave with data-parallel-primitive moves: a few cycles a
+// step where a shuffle through LDS takes over a hundred, and the k rounds of
+// the selection are a chain of them.  Neighbours, pairs, halves and whole rows
+// of 16 first, then the rows' results one row on and two rows on; lane 63 has
+// all of it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+
+template <typename OP>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, OP op)
+{
+    v = op(v, moved<0xB1, 0xF>(v));    // lanes 1 0 3 2 of each quad
+    v = op(v, moved<0x4E, 0xF>(v));    // lanes 2 3 0 1
+    v = op(v, moved<0x141, 0xF>(v));   // mirror of each half row
+    v = op(v, moved<0x140, 0xF>(v));   // mirror of each row
+    v = op(v, moved<0x142, 0xA>(v));   // lane 15 of a row into rows 1 and 3
+    v = op(v, moved<0x143, 0xC>(v));   // lane 31 into rows 2 and 3
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2)
-        v = max(v, (uint32_t)__shfl_xor((int)v, s));
-    return v;
+    return wave_reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
 __device__ __forceinline__ float wave_sum(float v)
 {
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2)
-        v += __shfl_xor(v, s);
-    return v;
+    return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
 }
 
 // Softmax of a token: this lane's p of its J experts.  `any` = the token is
 // live; a NaN or +infinity among its logits makes every p NaN (the sum is).
+// VEC: rows start at multiples of a lane's J elements and E is one, too.
 template <int J, typename T>
-__device__ __forceinline__ void load_logits(const T *row, int E, int lane, bool routed, float (&x)[J])
+__device__ __forceinline__ void load_logits(const T *row, int E, int lane, bool vec, T (&raw)[J])
 {
+    if (vec) {
+        if (lane * J < E)
+            __builtin_memcpy(raw, __builtin_assume_aligned(row + lane * J, sizeof(raw) < 16 ? sizeof(raw) : 16), sizeof(raw));
+    } else {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int e = lane * J + j;
-        x[j] = routed && e < E ? to_f32(row[e]) : -__builtin_inff();
+        for (int j = 0; j < J; ++j)
+            if (lane * J + j < E)
+                raw[j] = row[lane * J + j];
     }
 }
 
+template <int J, typename T>
+__device__ __forceinline__ void open_logits(const T (&raw)[J], int E, int lane, bool routed, float (&x)[J])
+{
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        x[j] = routed && lane * J + j < E ? to_f32(raw[j]) : -__builtin_inff();
+}
+
+// e^x for x <= 0, within two units of the last place: 2^t for t = x log2(e),
+// the rounding of t put right to first order.
+__device__ __forceinline__ float exp_of(float x)
+{
+    constexpr float kLog2e = 0x1.715476p+0f, kRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+    const float t = x * kLog2e;
+    const float low = __builtin_fmaf(x, kRest, __builtin_fmaf(x, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return x < -104.0f ? 0.0f : __builtin_fmaf(e * kLn2, low, e);
+}
+
 template <int J>
-__device__ __forceinline__ bool softmax(const float (&x)[J], const uint32_t (&key)[J], float (&p)[J], float &top,
-                                        float &sum)
+__device__ __forceinline__ bool softmax(const float (&x)[J], float (&p)[J], float &top, float &inv)
 {
     uint32_t best = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j)
-        best = max(best, key[j]);
+        best = max(best, key_of(x[j]));
     best = wave_max(best);
     const bool live = best != 0;   // uniform
     top = value_of(best);
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        p[j] = live ? expf(x[j] - top) : 0.0f;
+        p[j] = live ? exp_of(x[j] - top) : 0.0f;
         s += p[j];
     }
-    sum = wave_sum(s);
+    inv = 1.0f / wave_sum(s);
 #pragma unroll
     for (int j = 0; j < J; ++j)
-        p[j] = live ? p[j] / sum : 0.0f;
+        p[j] = live ? p[j] * inv : 0.0f;
     return live;
+}
+
+// The k largest logits of a token, one after the other; lane q gets the q-th
+// one's expert (-1: none is open any more) and its value.
+//   16-bit logits: a word holds the logit's 16-bit key and below it the
+//   expert's number, inverted, so the wave's largest word is the choice, ties
+//   and all.
+//   fp32: the wave's largest key, the first lane that holds it, that lane's
+//   first such expert.
+template <int J, typename T>
+__device__ __forceinline__ void choose(const T (&raw)[J], const float (&x)[J], int lane, int k, int &my_idx,
+                                       float &my_value)
+{
+    constexpr bool kHalf = sizeof(T) == 2;
+    uint32_t key[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        if constexpr (kHalf) {
+            const uint32_t b = raw[j].u == 0x8000u ? 0u : raw[j].u;   // -0 as +0
+            const uint32_t ordered = (b & 0x8000u ? ~b : b | 0x8000u) << 16;
+            key[j] = x[j] > -__builtin_inff() ? ordered | (0xFFFFu - (uint32_t)(lane * J + j)) : 0u;
+        } else {
+            key[j] = key_of(x[j]);
+        }
+    }
+    my_idx = -1;
+    uint32_t my_key = 0;
+    for (int q = 0; q < k; ++q) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            best = max(best, key[j]);
+        const uint32_t all = wave_max(best);
+        if (all == 0)
+            break;   // uniform
+        int e;
+        if constexpr (kHalf) {
+            e = (int)(0xFFFFu - (all & 0xFFFFu));
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                key[j] = key[j] == all ? 0 : key[j];
+        } else {
+            const int src = __ffsll((unsigned long long)__ballot(best == all)) - 1;
+            int at = 0;
+#pragma unroll
+            for (int j = J - 1; j >= 0; --j)
+                at = key[j] == all ? j : at;
+            e = __builtin_amdgcn_readlane(lane * J + at, src);
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                key[j] = lane * J + j == e ? 0 : key[j];
+        }
+        my_idx = lane == q ? e : my_idx;
+        my_key = lane == q ? all : my_key;
+    }
+    if constexpr (kHalf) {
+        const uint32_t b = my_key >> 16;
+        my_value = to_f32(T{(uint16_t)(b & 0x8000u ? b & 0x7FFFu : ~b)});
+    } else {
+        my_value = value_of(my_key);
+    }
 }
 
 struct Route {
@@ -107,81 +210,96 @@ struct Route {
 };
 
 struct Lds {
-    int32_t hist[kBins + 1];
+    unsigned long long tokens[kMaxExperts];   // bit t: token t of the chunk chose the expert
+    int32_t dropped[kChunkTokens];            // slots of a token without an expert (always its last ones)
+    int32_t live;
     float sums[kWaves][kMaxExperts];
-    int32_t expert[kChunkTokens * kMaxTopK];
 };
 
+__device__ __forceinline__ void clear(Lds &s, int E)
+{
+    for (int i = threadIdx.x; i < E; i += kThreads)
+        s.tokens[i] = 0;
+    if (threadIdx.x < kChunkTokens)
+        s.dropped[threadIdx.x] = 0;
+    if (threadIdx.x == 0)
+        s.live = 0;
+    __syncthreads();
+}
+
+// Marks the slots of token i of the chunk; idx: the choice of lane `lane` < k.
+__device__ __forceinline__ void mark(Lds &s, int i, int lane, int k, int idx)
+{
+    if (lane < k && idx >= 0)
+        atomicOr(&s.tokens[idx], 1ull << i);
+    const unsigned long long chosen = __ballot(lane < k && idx >= 0);
+    if (lane == 0)
+        s.dropped[i] = k - __popcll(chosen);
+}
+
+// Slots of the chunk per expert, without one (E) and live tokens (E + 1).
+__device__ __forceinline__ int count_of(const Lds &s, int e, int E)
+{
+    if (e < E)
+        return __popcll(s.tokens[e]);
+    if (e > E)
+        return s.live;
+    int n = 0;
+    for (int t = 0; t < kChunkTokens; ++t)
+        n += s.dropped[t];
+    return n;
+}
+
 // Routes the tokens t0 .. t0 + n - 1 of a workgroup: idx and weight to memory,
-// the slots' experts (E: none), the counts and the waves' sums of p to LDS.
+// marks and the waves' sums of p to LDS.
 template <int J, typename T>
 __device__ __forceinline__ void route_tokens(const RouteArgs &a, int64_t t0, int n, Lds &s)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int E = a.E, k = a.k;
-    for (int i = threadIdx.x; i < E + 2; i += kThreads)
-        s.hist[i] = 0;
-    __syncthreads();
+    const T *const logits = static_cast<const T *>(a.logits);
+    T raw[J], next[J];
+    int routed = 0, next_routed = 0;
+    auto load = [&](int i, T(&r)[J], int &on) {
+        const int64_t t = t0 + min(i, n - 1);
+        load_logits<J>(logits + t * a.ldl, E, lane, a.vec, r);
+        on = a.mask ? a.mask[t] : 1;
+    };
+    load(wave, raw, routed);
+    clear(s, E);
     float psum[J];
 #pragma unroll
     for (int j = 0; j < J; ++j)
         psum[j] = 0.0f;
     for (int i = wave; i < n; i += kWaves) {
+        load(i + kWaves, next, next_routed);   // in flight while this token is worked on
         const int64_t t = t0 + i;
-        const bool routed = !a.mask || a.mask[t] != 0;
         float x[J], p[J];
-        uint32_t key[J];
-        load_logits<J>(static_cast<const T *>(a.logits) + t * a.ldl, E, lane, routed, x);
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-            key[j] = key_of(x[j]);
-        float top, sum;
-        const bool live = softmax<J>(x, key, p, top, sum);
+        open_logits<J>(raw, E, lane, routed != 0, x);
+        float top, inv;
+        const bool live = softmax<J>(x, p, top, inv);
 #pragma unroll
         for (int j = 0; j < J; ++j)
             psum[j] += p[j];
-        // the k largest, one after the other: the wave's largest key, the
-        // first lane that holds it, that lane's first such expert
-        int my_idx = -1;
-        float my_w = 0.0f;
-        for (int q = 0; q < k; ++q) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                best = max(best, key[j]);
-            const uint32_t all = wave_max(best);
-            int e = -1;
-            if (all != 0) {   // uniform
-                const int src = __ffsll((unsigned long long)__ballot(best == all)) - 1;
-                int at = 0;
-#pragma unroll
-                for (int j = J - 1; j >= 0; --j)
-                    at = key[j] == all ? j : at;
-                if (lane == src) {
-#pragma unroll
-                    for (int j = 0; j < J; ++j)
-                        key[j] = j == at ? 0 : key[j];
-                }
-                e = __shfl(lane * J + at, src);
-            }
-            if (lane == q) {
-                my_idx = e;
-                my_w = e >= 0 ? expf(value_of(all) - top) / sum : 0.0f;
-            }
-        }
+        int my_idx;
+        float my_value;
+        choose<J, T>(raw, x, lane, k, my_idx, my_value);
+        float my_w = my_idx >= 0 ? exp_of(my_value - top) * inv : 0.0f;
         if (a.renormalize) {
-            const float total = wave_sum(lane < k ? my_w : 0.0f);
+            const float total = wave_sum(my_w);
             my_w = my_idx >= 0 && total != 0.0f ? my_w / total : 0.0f;
         }
         if (lane < k) {
             a.idx[t * k + lane] = my_idx;
             a.weight[t * k + lane] = my_w;
-            const int e = my_idx < 0 ? E : my_idx;
-            s.expert[i * k + lane] = e;
-            atomicAdd(&s.hist[e], 1);
         }
+        mark(s, i, lane, k, my_idx);
         if (lane == 0 && live)
-            atomicAdd(&s.hist[E + 1], 1);
+            atomicAdd(&s.live, 1);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            raw[j] = next[j];
+        routed = next_routed;
     }
 #pragma unroll
     for (int j = 0; j < J; ++j)
@@ -259,18 +377,25 @@ __device__ __forceinline__ void write_totals(const RouteArgs &a, const int32_t *
     }
 }
 
-// Places of a chunk's slots: the base of the expert plus the number of
-// earlier slots of the chunk with the same expert (every thread counts for
-// its own slots; the reads are the same for all lanes).
-__device__ __forceinline__ void place_slots(const int32_t *expert, int slots, const int32_t *base, int64_t first,
-                                            int32_t *order)
+// Places of a chunk's slots.  Tokens choose an expert at most once, so a slot
+// comes after as many slots of its expert as earlier tokens have its bit set;
+// the slots without an expert come after those of the earlier tokens and of
+// their own.
+__device__ __forceinline__ void place_slots(const RouteArgs &a, const Lds &s, const int32_t *base, int64_t t0, int n)
 {
-    for (int i = threadIdx.x; i < slots; i += kThreads) {
-        const int e = expert[i];
-        int rank = 0;
-        for (int j = 0; j < i; ++j)
-            rank += expert[j] == e ? 1 : 0;
-        order[base[e] + rank] = (int32_t)(first + i);
+    const int k = a.k;
+    for (int i = threadIdx.x; i < n * k; i += kThreads) {
+        const int t = i / k;
+        const int e = a.idx[t0 * k + i];
+        int at;
+        if (e >= 0)
+            at = base[e] + __popcll(s.tokens[e] & ((1ull << t) - 1));
+        else {
+            at = base[a.E] + i - t * k - (k - s.dropped[t]);
+            for (int u = 0; u < t; ++u)
+                at += s.dropped[u];
+        }
+        a.order[at] = (int32_t)(t0 * k + i);
     }
 }
 
@@ -280,11 +405,15 @@ __global__ __launch_bounds__(kThreads) void route_one_kernel(Route r)
     __shared__ Lds s;
     __shared__ int32_t base[kBins + 1];
     __shared__ double scratch[kWaves];
+    __shared__ int32_t counts[kBins + 1];
     const RouteArgs &a = r.a;
     route_tokens<J, T>(a, 0, (int)a.T, s);
-    bases(s.hist, a.E, base);
-    write_totals(a, s.hist, base, [&](int e) { return waves_sum(s, e); }, scratch);
-    place_slots(s.expert, (int)a.T * a.k, base, 0, a.order);
+    for (int e = threadIdx.x; e < a.E + 2; e += kThreads)
+        counts[e] = count_of(s, e, a.E);
+    __syncthreads();   // idx is read back below by other threads of this workgroup
+    bases(counts, a.E, base);
+    write_totals(a, counts, base, [&](int e) { return waves_sum(s, e); }, scratch);
+    place_slots(a, s, base, 0, (int)a.T);
 }
 
 template <int J, typename T>
@@ -295,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void route_tokens_kernel(Route r)
     const int64_t t0 = (int64_t)blockIdx.x * kChunkTokens;
     route_tokens<J, T>(a, t0, (int)min((int64_t)kChunkTokens, a.T - t0), s);
     for (int e = threadIdx.x; e < a.E + 2; e += kThreads)
-        r.chunk_counts[(int64_t)blockIdx.x * (a.E + 2) + e] = s.hist[e];
+        r.chunk_counts[(int64_t)blockIdx.x * (a.E + 2) + e] = count_of(s, e, a.E);
     for (int e = threadIdx.x; e < a.E; e += kThreads)
         r.chunk_sums[(int64_t)blockIdx.x * a.E + e] = waves_sum(s, e);
 }
@@ -311,22 +440,30 @@ __global__ __launch_bounds__(256) void route_experts_kernel(Route r)
         return;
     int before = 0;
     double sum = 0.0;
-    for (int c0 = 0; c0 < r.chunks; c0 += 64) {
-        const int c = c0 + lane;
-        int32_t *p = r.chunk_counts + (int64_t)c * (E + 2) + e;
-        const int v = c < r.chunks ? *p : 0;
-        int incl = v;
+    constexpr int kAt = 8;   // loads in flight
+    for (int c0 = 0; c0 < r.chunks; c0 += 64 * kAt) {
+        int v[kAt];
+        float f[kAt];
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(incl, d);
-            incl += lane >= d ? o : 0;
+        for (int q = 0; q < kAt; ++q) {
+            const int c = c0 + 64 * q + lane;
+            v[q] = c < r.chunks ? r.chunk_counts[(int64_t)c * (E + 2) + e] : 0;
+            f[q] = c < r.chunks && e < E ? r.chunk_sums[(int64_t)c * E + e] : 0.0f;
         }
-        if (c < r.chunks) {
-            *p = before + incl - v;
-            if (e < E)
-                sum += (double)r.chunk_sums[(int64_t)c * E + e];
+#pragma unroll
+        for (int q = 0; q < kAt; ++q) {
+            const int c = c0 + 64 * q + lane;
+            int incl = v[q];
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int o = __shfl_up(incl, d);
+                incl += lane >= d ? o : 0;
+            }
+            if (c < r.chunks)
+                r.chunk_counts[(int64_t)c * (E + 2) + e] = before + incl - v[q];
+            sum += (double)f[q];
+            before += __builtin_amdgcn_readlane(incl, 63);
         }
-        before += __shfl(incl, 63);
     }
 #pragma unroll
     for (int s = 1; s < 64; s *= 2)
@@ -342,18 +479,17 @@ __global__ __launch_bounds__(kThreads) void route_slots_kernel(Route r)
 {
     __shared__ int32_t counts[kBins + 1];
     __shared__ int32_t base[kBins + 1];
-    __shared__ int32_t expert[kChunkTokens * kMaxTopK];
+    __shared__ Lds s;
     __shared__ double scratch[kWaves];
     const RouteArgs &a = r.a;
-    const int E = a.E;
+    const int E = a.E, lane = threadIdx.x & 63;
     const int64_t t0 = (int64_t)blockIdx.x * kChunkTokens;
-    const int slots = (int)min((int64_t)kChunkTokens, a.T - t0) * a.k;
+    const int n = (int)min((int64_t)kChunkTokens, a.T - t0);
     for (int e = threadIdx.x; e < E + 2; e += kThreads)
         counts[e] = r.totals[e];
-    for (int i = threadIdx.x; i < slots; i += kThreads) {
-        const int e = a.idx[t0 * a.k + i];
-        expert[i] = e < 0 ? E : e;
-    }
+    clear(s, E);
+    for (int i = threadIdx.x >> 6; i < n; i += kWaves)
+        mark(s, i, lane, a.k, lane < a.k ? a.idx[(t0 + i) * a.k + lane] : -1);
     __syncthreads();
     bases(counts, E, base);
     if (blockIdx.x == 0) {
@@ -363,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void route_slots_kernel(Route r)
     for (int e = threadIdx.x; e <= E; e += kThreads)
         base[e] += r.chunk_counts[(int64_t)blockIdx.x * (E + 2) + e];
     __syncthreads();
-    place_slots(expert, slots, base, t0 * a.k, a.order);
+    place_slots(a, s, base, t0, n);
 }
 
 // dlogits of a token: p (dp - sum p dp) with dp[e] = grad_loss E counts[e] /
@@ -383,41 +519,62 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a)
         const int e = lane * J + j;
         dp0[j] = e < E && a.grad_loss ? unit * (float)a.counts[e] : 0.0f;
     }
-    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += (int64_t)gridDim.x * 4) {
-        const bool routed = !a.mask || a.mask[t] != 0;
-        float x[J], p[J], dp[J], own[J];
-        uint32_t key[J];
-        load_logits<J>(static_cast<const T *>(a.logits) + t * a.ldl, E, lane, routed, x);
-        int my_idx = -1;
-        float w = 0.0f, g = 0.0f;
+    __shared__ float given[4][64 * J];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        given[threadIdx.x >> 6][lane * J + j] = 0.0f;
+    const T *const logits = static_cast<const T *>(a.logits);
+    const int64_t first = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), stride = (int64_t)gridDim.x * 4;
+    struct Row {
+        T raw[J];
+        int routed, idx;
+        float w, g;
+    };
+    auto load = [&](int64_t t, Row &r) {
+        t = min(t, a.T - 1);
+        load_logits<J>(logits + t * a.ldl, E, lane, a.vec, r.raw);
+        r.routed = a.mask ? a.mask[t] : 1;
+        r.idx = -1, r.w = r.g = 0.0f;
         if (lane < k && a.grad_weight) {
-            my_idx = a.idx[t * k + lane];
-            w = my_idx >= 0 ? a.weight[t * k + lane] : 0.0f;
-            g = my_idx >= 0 ? a.grad_weight[t * k + lane] : 0.0f;
+            const int e = a.idx[t * k + lane];
+            r.idx = (uint32_t)e < (uint32_t)E ? e : -1;
+            r.w = a.weight[t * k + lane];
+            r.g = a.grad_weight[t * k + lane];
         }
+    };
+    Row row, next;
+    load(first, row);
+    for (int64_t t = first; t < a.T; t += stride) {
+        load(t + stride, next);   // in flight while this token is worked on
+        float x[J], p[J], dp[J], own[J];
+        open_logits<J>(row.raw, E, lane, row.routed != 0, x);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            key[j] = key_of(x[j]);
             dp[j] = dp0[j];
             own[j] = 0.0f;
         }
-        float top, sum;
-        const bool live = softmax<J>(x, key, p, top, sum);
+        float top, inv;
+        const bool live = softmax<J>(x, p, top, inv);
         if (a.grad_weight) {
+            const float w = row.idx >= 0 ? row.w : 0.0f, g = row.idx >= 0 ? row.g : 0.0f;
             const float c = a.renormalize ? wave_sum(w * g) : 0.0f;
             const float d = a.renormalize ? w * (g - c) : g;
-            for (int q = 0; q < k; ++q) {
-                const int e = __shfl(my_idx, q);
-                const float v = __shfl(d, q);
+            // from the lanes of the k choices to the lanes of their experts,
+            // through this wave's row in LDS (zeros but for the choices)
+            float *mine = &given[threadIdx.x >> 6][0];
+            if (row.idx >= 0)
+                mine[row.idx] = d;
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (e == lane * J + j) {
-                        if (a.renormalize)
-                            own[j] += v;
-                        else
-                            dp[j] += v;
-                    }
+            for (int j = 0; j < J; ++j) {
+                const float v = mine[lane * J + j];
+                own[j] = a.renormalize ? v : 0.0f;
+                dp[j] += a.renormalize ? 0.0f : v;
             }
+            __builtin_amdgcn_wave_barrier();
+            if (row.idx >= 0)
+                mine[row.idx] = 0.0f;
+            __builtin_amdgcn_wave_barrier();
         }
         float s = 0.0f;
 #pragma unroll
@@ -425,12 +582,20 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a)
             s += p[j] * dp[j];
         s = wave_sum(s);
         T *out = static_cast<T *>(a.dlogits) + t * E;
+        T res[J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int e = lane * J + j;
-            if (e < E)
-                out[e] = from_f32<T>(live && key[j] ? own[j] + p[j] * (dp[j] - s) : 0.0f);
+        for (int j = 0; j < J; ++j)
+            res[j] = from_f32<T>(live && x[j] > -__builtin_inff() ? own[j] + p[j] * (dp[j] - s) : 0.0f);
+        if (a.vec_out) {
+            if (lane * J < E)
+                __builtin_memcpy(__builtin_assume_aligned(out + lane * J, sizeof(res) < 16 ? sizeof(res) : 16), res, sizeof(res));
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (lane * J + j < E)
+                    out[lane * J + j] = res[j];
         }
+        row = next;
     }
 }
 
@@ -463,6 +628,18 @@ inline int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
 }  // namespace
 
+namespace {
+
+// Whether a lane's elements of every row are one aligned vector.
+bool whole_vectors(const void *p, int64_t ld, int E, int type)
+{
+    const int J = E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : 8;
+    const uintptr_t bytes = (uintptr_t)J * type_bytes(type);
+    return E % J == 0 && ld % J == 0 && (reinterpret_cast<uintptr_t>(p) & (std::min<uintptr_t>(bytes, 16) - 1)) == 0;
+}
+
+}  // namespace
+
 size_t route_workspace(int64_t T, int64_t E)
 {
     if (T <= kChunkTokens)
@@ -475,6 +652,7 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream)
 {
     Route r{};
     r.a = a;
+    r.a.vec = whole_vectors(a.logits, a.ldl, a.E, a.type);
     if (a.T <= kChunkTokens) {
         return with_types(a.E, a.type, [&](auto j, auto t) {
             return go(&route_one_kernel<decltype(j)::value, decltype(t)>, dim3(1), dim3(kThreads), r, stream);
@@ -500,8 +678,11 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream)
     return e;
 }
 
-hipError_t launch_route_backward(const RouteGradArgs &a, int cus, hipStream_t stream)
+hipError_t launch_route_backward(const RouteGradArgs &args, int cus, hipStream_t stream)
 {
+    RouteGradArgs a = args;
+    a.vec = whole_vectors(a.logits, a.ldl, a.E, a.type);
+    a.vec_out = whole_vectors(a.dlogits, a.E, a.E, a.type);
     const unsigned wgs = (unsigned)std::min<int64_t>(ceil_div(a.T, 4), 8LL * cus);
     return with_types(a.E, a.type, [&](auto j, auto t) {
         return go(&route_backward_kernel<decltype(j)::value, decltype(t)>, dim3(wgs), dim3(256), a, stream);
