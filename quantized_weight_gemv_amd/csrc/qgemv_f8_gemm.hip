@@ -4,16 +4,20 @@
 // A workgroup owns a tile of BM rows of X times BN rows of W.  A step is 64
 // columns (half a block: one scale byte a row and side); its operands go
 // straight from memory into LDS (loads that write LDS: no registers):
-//   * X, row-major: rows of 64 bytes, 16-byte chunk c of row r at position
-//     c ^ ((r / 4) % 4), so that the 16 rows of a quarter of an operand read
+//   * X, row-major, a block of 128 columns at a time: rows of 128 bytes, whole
+//     lines (the caches deliver 30 TB/s to loads of 8 rows x 128 bytes and 9.5
+//     to loads of 16 rows x 64 bytes), 16-byte chunk c of row r at position
+//     c ^ ((r / 2) % 8), so that the 16 rows of a quarter of an operand read
 //     touch all 64 banks;
-//   * W, whose tiles are in operand order already: copied as they are; an
-//     operand read is 256 consecutive bytes a quarter wave.
-// A ring of four buffers.  During step t the matrix cores multiply operands
-// that were read from LDS during step t - 1, the operands of t + 1 are read
-// from buffer t + 1, and the copies of step t + 3 are issued into the buffer
-// that step t - 1 was read from.  One barrier a step; before it a wave waits
-// for its own copies of step t + 1 only (all but the youngest step's).
+//   * W, whose tiles are in operand order already: copied as they are, a step
+//     at a time; an operand read is 256 consecutive bytes a quarter wave.
+// X has two buffers (blocks), W four (steps).  During step t the matrix cores
+// multiply operands that were read from LDS during step t - 1, the operands of
+// t + 1 are read, W's copies of step t + 3 are issued and, in a block's second
+// step, X's copies of the block after the next one, both into buffers whose
+// last reads fed products of step t - 1.  One barrier a step; before it a wave
+// waits for those of its own copies that step t reads (issued in step t - 2 at
+// the latest).
 // 16-bit outputs: v_mfma_scale_f32_32x32x64_f8f6f4 with the two block scales
 // as its scale operands, so the fp32 sums need no further instruction.  fp32
 // outputs: the codes are widened to bf16 with their scale (exact) and
@@ -53,7 +57,7 @@ __device__ __forceinline__ void copy16(const uint8_t *from, void *to)
 template <int WM, int WN, int TM, int TN>
 struct Tile {
     static constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, NT = 64 * WM * WN;
-    static constexpr int XC = BM * 4 / NT, WC = BN * 4 / NT;   // 16-byte copies per thread and step
+    static constexpr int XC = BM * 8 / NT, WC = BN * 4 / NT;   // 16-byte copies per thread: X's a block, W's a step
 };
 
 // Which tile a workgroup takes.  Workgroups go to the eight XCDs in turn, each
@@ -88,13 +92,12 @@ __global__ __launch_bounds__(64 * WM *WN, TM *TN == 16 ? 1 : 2) void gemm_kernel
 {
     using T = Tile<WM, WN, TM, TN>;
     constexpr bool kWide = sizeof(OUT) == 4;
-    constexpr int kCopies = T::XC + T::WC;
     // one variable a buffer: the compiler then knows which copies an operand
     // read has to wait for (none: the waits are the kernel's own)
-    __shared__ uint4 X0[T::BM * 4], X1[T::BM * 4], X2[T::BM * 4], X3[T::BM * 4];
+    __shared__ uint4 X0[T::BM * 8], X1[T::BM * 8];
     __shared__ uint4 W0[T::BN * 4], W1[T::BN * 4], W2[T::BN * 4], W3[T::BN * 4];
     __shared__ int out_row[GROUPED ? T::BM : 1];
-    auto xbuf = [&](int q) -> uint4 * { return q == 0 ? X0 : q == 1 ? X1 : q == 2 ? X2 : X3; };
+    auto xbuf = [&](int q) -> uint4 * { return q == 0 ? X0 : X1; };
     auto wbuf = [&](int q) -> uint4 * { return q == 0 ? W0 : q == 1 ? W1 : q == 2 ? W2 : W3; };
 
     const int lane = threadIdx.x & 63;
@@ -146,7 +149,7 @@ __global__ __launch_bounds__(64 * WM *WN, TM *TN == 16 ? 1 : 2) void gemm_kernel
 #pragma unroll
         for (int i = 0; i < T::XC; ++i) {
             const int idx = threadIdx.x + T::NT * i;
-            const int r = idx >> 2, ch = (idx & 3) ^ ((r >> 2) & 3);
+            const int r = idx >> 3, ch = (idx & 7) ^ ((r >> 1) & 7);
             xsrc[i] = p.xq + x_row(r) * p.cb * 128 + ch * 16;
         }
 #pragma unroll
@@ -171,35 +174,40 @@ __global__ __launch_bounds__(64 * WM *WN, TM *TN == 16 ? 1 : 2) void gemm_kernel
             ws_next = *reinterpret_cast<const uint32_t *>(ws_src + at);
         };
 
+        // the next block of X and step of W to copy; past the last one that
+        // one again (never read).  No branch: the products of a step would be
+        // moved across it
         const int steps = 2 * p.cb;
-        int ahead = 0;   // the next step to copy; past the last one it is copied again (never read)
-        auto copies = [&](uint4 *X, uint4 *Wb) {
+        int x_ahead = 0, w_ahead = 0;
+        auto copy_x = [&](uint4 *X) {
 #pragma unroll
             for (int i = 0; i < T::XC; ++i)
                 copy16(xsrc[i], &X[T::NT * i + 64 * wave]);
+            const int go = ++x_ahead < p.cb ? 128 : 0;
+#pragma unroll
+            for (int i = 0; i < T::XC; ++i)
+                xsrc[i] += go;
+        };
+        auto copy_w = [&](uint4 *Wb) {
 #pragma unroll
             for (int i = 0; i < T::WC; ++i)
                 copy16(wsrc[i], &Wb[T::NT * i + 64 * wave]);
-            // no branch: the products of a step would be moved across it
-            const int go = ++ahead < steps ? 1 : 0;
-#pragma unroll
-            for (int i = 0; i < T::XC; ++i)
-                xsrc[i] += 64 * go;
+            const int go = ++w_ahead < steps ? 1024 : 0;
 #pragma unroll
             for (int i = 0; i < T::WC; ++i)
-                wsrc[i] += 1024 * go;
+                wsrc[i] += go;
         };
         struct Operands {
             uint4 x[TM][2], w[TN][2];
         };
-        auto read = [&](Operands &o, const uint4 *X, const uint4 *Wb) {
+        auto read = [&](Operands &o, const uint4 *X, int h, const uint4 *Wb) {   // h: half of X's block
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int ch = 2 * half + q;
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     const int r = (wm * TM + i) * 32 + r32;
-                    o.x[i][q] = X[r * 4 + (ch ^ ((r >> 2) & 3))];
+                    o.x[i][q] = X[r * 8 + ((4 * h + ch) ^ ((r >> 1) & 7))];
                 }
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
@@ -246,64 +254,68 @@ __global__ __launch_bounds__(64 * WM *WN, TM *TN == 16 ? 1 : 2) void gemm_kernel
         };
 
         load_scales(0);
-        copies(X0, W0);
-        copies(X1, W1);
-        copies(X2, W2);
+        copy_x(X0);
+        copy_w(W0);
+        copy_w(W1);
+        copy_x(X1);
+        copy_w(W2);
         Operands even, odd;
-        wait_vm<2 * kCopies>();
+        wait_vm<T::XC + 2 * T::WC>();
         bare_barrier();
-        read(even, X0, W0);
-        // one step; q: its buffer
-        auto step = [&](auto number) {
+        read(even, X0, 0, W0);
+        uint32_t xword[TM], wword;
+        // step q of a pair of blocks, the first of which is b
+        auto step = [&](int b, auto number) {
             constexpr int q = decltype(number)::value;
-            wait_vm<kCopies>();
+            // an even step leaves the copies of the step before it in flight
+            // (X's and W's), an odd one's predecessor copied W only
+            wait_vm<q & 1 ? T::WC : T::XC + T::WC>();
             bare_barrier();
-            copies(xbuf((q + 3) & 3), wbuf((q + 3) & 3));
-            read(q & 1 ? even : odd, xbuf((q + 1) & 3), wbuf((q + 1) & 3));
+            if constexpr (q == 0) {
+                // the scales of a pair of blocks are loaded a pair ahead
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    xword[i] = xs_next[i];
+                wword = ws_next;
+                load_scales((b + 2) / 4);
+            }
+            if constexpr ((q & 1) == 0) {
+                const int shift = 8 * ((b + q / 2) & 3);
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    xs[i] = xword[i] >> shift;
+                ws = wword >> shift;
+            }
+            if constexpr (q & 1)
+                copy_x(xbuf(q >> 1));
+            copy_w(wbuf((q + 3) & 3));
+            read(q & 1 ? even : odd, xbuf(((q + 1) & 3) >> 1), (q + 1) & 1, wbuf((q + 1) & 3));
             multiply(q & 1 ? odd : even);
             // reads and copies behind the first products: left alone they
             // gather at the end of the step
             if constexpr (!kWide) {
-                constexpr int kProducts = TM * TN, kReads = 2 * (TM + TN);
+                constexpr int kProducts = TM * TN, kReads = 2 * (TM + TN), kCopies = T::WC + (q & 1 ? T::XC : 0);
+                constexpr int kPer = (kCopies + kProducts - 1) / kProducts;
 #pragma unroll
                 for (int m = 0; m < kProducts; ++m) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
                     if (2 * m < kReads)
                         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // LDS reads
-                    if (m < kCopies)
-                        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // copies
+                    if (kPer * m < kCopies)
+                        __builtin_amdgcn_sched_group_barrier(0x020, kPer, 0);   // copies
                 }
             }
         };
-        // two steps of column block b, whose scales are in bytes b % 4
-        uint32_t xword[TM], wword;
-        auto block = [&](int b, auto number) {
-            constexpr int q = decltype(number)::value;
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                xs[i] = xword[i] >> (8 * (b & 3));
-            ws = wword >> (8 * (b & 3));
-            step(std::integral_constant<int, q>{});
-            step(std::integral_constant<int, q + 1>{});
-        };
-        // the scales of a pair of blocks are loaded a pair ahead, before
-        // the copies that the following wait leaves in flight
-        auto take_scales = [&](int b) {
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                xword[i] = xs_next[i];
-            wword = ws_next;
-            load_scales((b + 2) / 4);
-        };
         int b = 0;
         for (; b + 1 < p.cb; b += 2) {
-            take_scales(b);
-            block(b, std::integral_constant<int, 0>{});
-            block(b + 1, std::integral_constant<int, 2>{});
+            step(b, std::integral_constant<int, 0>{});
+            step(b, std::integral_constant<int, 1>{});
+            step(b, std::integral_constant<int, 2>{});
+            step(b, std::integral_constant<int, 3>{});
         }
         if (b < p.cb) {
-            take_scales(b);
-            block(b, std::integral_constant<int, 0>{});
+            step(b, std::integral_constant<int, 0>{});
+            step(b, std::integral_constant<int, 1>{});
         }
         wait_vm<0>();   // no copy is in flight when the buffers are used again
     }
@@ -313,51 +325,53 @@ __global__ __launch_bounds__(64 * WM *WN, TM *TN == 16 ? 1 : 2) void gemm_kernel
     // would touch 32 rows.  So 32 rows x 32 TN columns at a time go
     // through LDS (wave-private, 16-byte chunks swizzled by row) and are
     // stored whole lines at a time.
-    static_assert(WM * WN == 4 && TN * sizeof(OUT) <= 4 * TM, "each wave stages in an X buffer of its own");
-    constexpr int kRow = 32 * TN * (int)sizeof(OUT), kChunks = kRow / 16;
-    uint4 *stage = xbuf(wave);
+    constexpr int JN = kWide ? TN / 2 : TN;       // column tiles staged at a time
+    constexpr int kRow = 32 * JN * (int)sizeof(OUT), kChunks = kRow / 16;
+    static_assert(WM * WN == 4 && 4 * 32 * kRow <= T::BM * 128, "each wave stages in a quarter of X0");
+    uint4 *stage = X0 + wave * (T::BM * 2);
     char *bytes = reinterpret_cast<char *>(stage);
     constexpr int kPer = 16 / (int)sizeof(OUT);   // elements of a chunk
     constexpr int kStores = 32 * kChunks / 64;    // per lane and 32 rows
     const bool whole = p.vec && n0 + T::BN <= p.N && (GROUPED || rows == T::BM);   // no edge in this tile
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    for (int part = 0; part < TM * TN / JN; ++part) {
+        const int i = part / (TN / JN), j0 = part % (TN / JN) * JN;
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+        for (int j = 0; j < JN; ++j)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int at = (32 * j + 8 * g + 4 * half) * (int)sizeof(OUT);
                 char *to = bytes + r32 * kRow + (((at >> 4) ^ (r32 & (kChunks - 1))) << 4) + (at & 15);
-                const f16v_t &a = acc[i][j];
+                const f16v_t &a = acc[i][j0 + j];
                 if constexpr (kWide)
                     *reinterpret_cast<f4_t *>(to) = f4_t{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
                 else
                     *reinterpret_cast<uint2 *>(to) =
                         make_uint2(pack2<OUT>(a[4 * g], a[4 * g + 1]), pack2<OUT>(a[4 * g + 2], a[4 * g + 3]));
             }
-        auto at = [&](int c, int &m, int &n) -> const uint4 & {   // the c-th chunk of this lane: its row and column
+        // the c-th chunk of this lane: its row and column in the tile
+        auto row_at = [&](int c) { return (wm * TM + i) * 32 + (64 * c + lane) / kChunks; };
+        auto chunk_at = [&](int c) {
             const int r = (64 * c + lane) / kChunks, ch = (64 * c + lane) % kChunks;
-            m = (wm * TM + i) * 32 + r;
-            n = n0 + wn * TN * 32 + ch * kPer;
             return stage[r * kChunks + (ch ^ (r & (kChunks - 1)))];
         };
+        const int n = n0 + (wn * TN + j0) * 32 + lane % kChunks * kPer;   // 64 is a multiple of kChunks
         if (whole) {
             uint4 v[kStores];
-            int m[kStores], n;
 #pragma unroll
             for (int c = 0; c < kStores; ++c)
-                v[c] = at(c, m[c], n);
+                v[c] = chunk_at(c);
 #pragma unroll
             for (int c = 0; c < kStores; ++c) {
-                const int64_t y = GROUPED ? out_row[m[c]] : u.r0 + m[c];
+                const int64_t y = GROUPED ? out_row[row_at(c)] : u.r0 + row_at(c);
                 if (!GROUPED || y >= 0)
                     *reinterpret_cast<uint4 *>(static_cast<OUT *>(p.Y) + y * p.N + n) = v[c];
             }
         } else {
 #pragma unroll 1
             for (int c = 0; c < kStores; ++c) {
-                int m, n;
-                const uint4 v = at(c, m, n);
+                const int m = row_at(c);
+                const uint4 v = chunk_at(c);
                 const int64_t y = GROUPED ? out_row[m] : u.r0 + m;
                 if (!(GROUPED ? y >= 0 : m < rows) || n >= p.N)
                     continue;
