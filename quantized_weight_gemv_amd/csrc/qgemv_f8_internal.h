@@ -255,6 +255,8 @@ __device__ __forceinline__ void bare_barrier()
 struct F8Unit {
     int e;
     int64_t r0, r1;
+    int first, tiles;   // the expert's first unit and how many it has
+    int64_t begin, end; // all of its rows
 };
 
 // The unit-th tile of `tile` rows, counting expert by expert, each expert
@@ -288,7 +290,7 @@ __device__ __forceinline__ F8Unit f8_unit(const int32_t *offsets, int P, int64_t
     }
     const unsigned long long holds = __ballot((int64_t)incl > unit);
     if (holds == 0)
-        return F8Unit{P, 0, 0};
+        return F8Unit{P, 0, 0, 0, 1, 0, 0};
     const int src = __ffsll(holds) - 1;
     int left = (int)unit - __builtin_amdgcn_readlane(incl - mine, src);
     for (int j = 0; j < per; ++j) {
@@ -299,10 +301,18 @@ __device__ __forceinline__ F8Unit f8_unit(const int32_t *offsets, int P, int64_t
         span(e, a, b);
         const int tiles = (b - a + tile - 1) / tile;
         if (left < tiles)
-            return F8Unit{e, a + (int64_t)left * tile, min((int64_t)b, a + (int64_t)(left + 1) * tile)};
+            return F8Unit{e, a + (int64_t)left * tile, min((int64_t)b, a + (int64_t)(left + 1) * tile),
+                          (int)unit - left, tiles, a, b};
         left -= tiles;
     }
-    return F8Unit{P, 0, 0};
+    return F8Unit{P, 0, 0, 0, 1, 0, 0};
+}
+
+// Another tile of the same expert, the index-th of its tiles.
+__device__ __forceinline__ void f8_tile_of(F8Unit &u, int index, int tile)
+{
+    u.r0 = u.begin + (int64_t)index * tile;
+    u.r1 = min(u.end, u.r0 + tile);
 }
 
 // An upper bound of the tiles that f8_unit counts.

@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * NW, R * G <= 1 ? 4 : 2) void skinny_kernel(Ski
     int64_t item = blockIdx.x;
     if (item >= total)
         return;
-    F8Unit u{0, 0, p.rows.rows};
+    F8Unit u{0, 0, p.rows.rows, 0, 1, 0, 0};
     int64_t y_row[G], x_row[G];   // this lane's rows of Y (-1: none) and of X
     const uint8_t *W = p.W;
     auto begin_unit = [&](int64_t unit) {
