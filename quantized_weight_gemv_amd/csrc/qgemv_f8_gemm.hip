@@ -90,12 +90,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const Source &s)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(s.base), (short)0, (int)s.bytes, kRsrcWord3);
 }
 
-// 16 bytes a lane from `at` + `off` of the buffer to consecutive LDS from `to`.
-__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, uint4 *to, uint32_t at, int off)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, at, off, 0, 0);
-}
-
 template <int TM, int TN, int D, typename OUT, bool GROUPED>
 __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_kernel(GemmParams p)
 {

@@ -250,6 +250,12 @@ __device__ __forceinline__ void bare_barrier()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// 16 bytes a lane from `at` + `off` of the buffer to consecutive LDS from `to`.
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, uint4 *to, uint32_t at, int off)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, at, off, 0, 0);
+}
+
 // Where a group's rows are: rows r0 .. r1 - 1 of `order` (or of Y and X, dense),
 // at most `tile` of them, of expert e; e = P: slots without an expert.
 struct F8Unit {
@@ -265,22 +271,25 @@ struct F8Unit {
 // over the lanes and one ballot find the share that holds the unit.  Offsets
 // are device data: they are held to 0 .. rows and to their order, so a tile
 // never leaves `order`.
-__device__ __forceinline__ F8Unit f8_unit(const int32_t *offsets, int P, int64_t rows, int tile, int64_t unit)
+template <int kPer>
+__device__ __forceinline__ F8Unit f8_unit_of(const int32_t *offsets, int P, int64_t rows, int tile, int64_t unit)
 {
     const int lane = threadIdx.x & 63;
-    const int per = (P + 1 + 63) / 64;
+    const int per = (P + 1 + 63) / 64;   // experts a lane, the last one: slots without an expert
     const int n = (int)rows;
-    auto span = [&](int e, int &a, int &b) {
-        a = min(max(offsets[e], 0), n);
-        b = e < P ? max(a, min(max(offsets[e + 1], 0), n)) : n;
-    };
-    int mine = 0;
-    for (int j = 0; j < per; ++j) {
+    int at[kPer + 1];   // all loads first: one latency
+#pragma unroll
+    for (int j = 0; j <= kPer; ++j) {
         const int e = lane * per + j;
-        int a = 0, b = 0;
-        if (e <= P)
-            span(e, a, b);
-        mine += (b - a + tile - 1) / tile;
+        at[j] = j <= per && e <= P ? offsets[e] : n;
+    }
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = lane * per + j;
+        at[j] = min(max(at[j], 0), n);
+        const int end = e < P ? max(at[j], min(max(at[j + 1], 0), n)) : n;
+        mine += j < per && e <= P ? (end - at[j] + tile - 1) / tile : 0;
     }
     int incl = mine;
 #pragma unroll
@@ -293,19 +302,32 @@ __device__ __forceinline__ F8Unit f8_unit(const int32_t *offsets, int P, int64_t
         return F8Unit{P, 0, 0, 0, 1, 0, 0};
     const int src = __ffsll(holds) - 1;
     int left = (int)unit - __builtin_amdgcn_readlane(incl - mine, src);
-    for (int j = 0; j < per; ++j) {
+    F8Unit u{P, 0, 0, 0, 1, 0, 0};
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
         const int e = src * per + j;
-        if (e > P)
-            break;
-        int a, b;
-        span(e, a, b);
-        const int tiles = (b - a + tile - 1) / tile;
-        if (left < tiles)
-            return F8Unit{e, a + (int64_t)left * tile, min((int64_t)b, a + (int64_t)(left + 1) * tile),
-                          (int)unit - left, tiles, a, b};
-        left -= tiles;
+        const int a = __builtin_amdgcn_readlane(at[j], src);
+        const int next = min(max(__builtin_amdgcn_readlane(at[j + 1], src), 0), n);
+        const int b = e < P ? max(a, next) : n;
+        const int tiles = j < per && e <= P ? (b - a + tile - 1) / tile : 0;
+        if (!found && left < tiles) {
+            u = F8Unit{e, a + (int64_t)left * tile, min((int64_t)b, a + (int64_t)(left + 1) * tile), (int)unit - left,
+                       tiles, a, b};
+            found = true;
+        }
+        left -= found ? 0 : tiles;
     }
-    return F8Unit{P, 0, 0, 0, 1, 0, 0};
+    return u;
+}
+
+__device__ __forceinline__ F8Unit f8_unit(const int32_t *offsets, int P, int64_t rows, int tile, int64_t unit)
+{
+    if (P < 64)
+        return f8_unit_of<1>(offsets, P, rows, tile, unit);
+    if (P < 192)
+        return f8_unit_of<3>(offsets, P, rows, tile, unit);
+    return f8_unit_of<(kMaxExperts + 1 + 63) / 64>(offsets, P, rows, tile, unit);
 }
 
 // Another tile of the same expert, the index-th of its tiles.

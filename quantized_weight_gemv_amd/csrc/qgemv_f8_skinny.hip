@@ -39,7 +39,7 @@ struct SkinnyParams {
     F8Rows rows;
     int64_t w_scales, x_scales;
     int64_t units;        // tiles of tokens (grouped: an upper bound)
-    int N, K, cb, ls, rt, row_groups;
+    int N, K, cb, ls, x_ls, rt, row_groups;
     int y_type;
     bool vec;             // rows of Y take whole vectors of four
 };
@@ -352,6 +352,161 @@ __global__ __launch_bounds__(64 * NW, R * G <= 1 ? 4 : 2) void skinny_kernel(Ski
     }
 }
 
+// 17 to 64 tokens of one matrix (G groups of 16): the same streaming of W, with
+// X's blocks copied into LDS a block ahead (buffer loads that write LDS), by
+// each wave for itself.  An operand read straight from memory takes 16 rows x
+// 64 bytes, and the caches deliver 9.5 TB/s to such loads against 30 to the 8
+// rows x 128 bytes of a copy; X, read by every workgroup, is most of what is
+// read here.  Rows are 128 bytes, 16-byte chunk c of row r at position
+// c ^ ((r / 2) % 8): the 16 rows of a quarter of an operand read touch all 64
+// banks.
+template <int G>
+__global__ __launch_bounds__(512, 2) void skinny_lds_kernel(SkinnyParams p)
+{
+    constexpr int NW = 8, kRows = 16 * G, kCopies = kRows / 8;
+    // one variable a buffer, as the compiler then knows which copies a read waits for
+    __shared__ uint4 XA[NW * kRows * 8], XB[NW * kRows * 8];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, c = lane >> 4;
+    const int mine = (p.cb - wave + NW - 1) / NW;   // this wave's column blocks: wave, wave + 8, ..
+    const int rows = (int)p.rows.rows;
+    const auto rx = make_rsrc(p.xq, (int64_t)rows * p.cb * 128);
+
+    uint32_t x_at[kCopies], xs_at[G];
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const int r = 8 * i + (lane >> 3);
+        x_at[i] = (uint32_t)(min(r, rows - 1) * p.cb * 128 + ((lane & 7) ^ ((r >> 1) & 7)) * 16);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        xs_at[g] = (uint32_t)(min(16 * g + r16, rows - 1) * p.x_ls);
+
+    struct Regs {
+        uint4 w[2];
+        uint32_t ws, xs[G];
+    };
+    f4_t acc[G];
+    auto clear = [&] {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            acc[g] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    auto load = [&](Regs &b, uint4 *X, int rg, int j) {
+        const int cb = min(wave + NW * j, p.cb - 1);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+            copy16(rx, &X[(wave * kRows + 8 * i) * 8], x_at[i], cb * 128);
+        const auto rw = make_rsrc(p.W + (int64_t)rg * p.cb * 2048, (int64_t)p.cb * 2048);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            b.w[h] = stream_load16(rw, (uint32_t)(cb * 2048 + 1024 * h + 16 * lane));
+        b.ws = p.W[p.w_scales + (int64_t)(rg >> 3) * p.ls + cb];
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            b.xs[g] = p.xq[p.x_scales + xs_at[g] + cb];
+    };
+    auto multiply = [&](const Regs &b, const uint4 *X) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 x[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int r = 16 * g + r16;
+                x[g] = X[(wave * kRows + r) * 8 + ((c + 4 * h) ^ ((r >> 1) & 7))];
+            }
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const bf8_t w = o ? f8_widen(b.w[h].z, b.w[h].w, f8_exponent(b.ws))
+                                  : f8_widen(b.w[h].x, b.w[h].y, f8_exponent(b.ws));
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const bf8_t v = o ? f8_widen(x[g].z, x[g].w, f8_exponent(b.xs[g]))
+                                      : f8_widen(x[g].x, x[g].y, f8_exponent(b.xs[g]));
+                    acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, v, acc[g], 0, 0, 0);
+                }
+            }
+        }
+    };
+    // the waves' sums are added through LDS, group g by wave g; XA or XB,
+    // whichever the next block is not copied into, holds them
+    auto finish = [&](int rg, uint4 *X) {
+        f4_t *buf = reinterpret_cast<f4_t *>(X);
+        bare_barrier();   // every wave has read its last block from X
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            buf[(wave * G + g) * 64 + lane] = acc[g];
+        wait_lds();
+        bare_barrier();
+        if (wave < G) {
+            f4_t v = buf[wave * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < NW; ++w)
+                v += buf[(w * G + wave) * 64 + lane];
+            const int n = rg * 16 + 4 * c, m = 16 * wave + r16;
+            if (m < rows && n < p.N) {
+                const int64_t at = (int64_t)m * p.N + n;
+                if (p.y_type == QG_F32)
+                    store4<float>(p.Y, at, v, p.N - n, p.vec);
+                else if (p.y_type == QG_F16)
+                    store4<Fp16>(p.Y, at, v, p.N - n, p.vec);
+                else
+                    store4<Bf16>(p.Y, at, v, p.N - n, p.vec);
+            }
+            wait_lds();
+        }
+        bare_barrier();   // X may be copied into again
+        clear();
+    };
+
+    // a wave without column blocks multiplies the last one with zero sums: it
+    // copies it, like the others, and leaves the products out
+    const int batches = max(mine, 1);
+    constexpr int kOps = kCopies + 3 + G;   // vector memory operations of a load
+    Regs r0, r1;
+    clear();
+    for (int rg = blockIdx.x; rg < p.row_groups; rg += gridDim.x) {
+        load(r0, XA, rg, 0);
+        int t = 0;
+        for (; t + 2 < batches; t += 2) {
+            load(r1, XB, rg, t + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm<kOps>();   // block t is there, block t + 1 in flight
+            multiply(r0, XA);
+            wait_lds();   // what is copied into has been read
+            __builtin_amdgcn_sched_barrier(0);
+            load(r0, XA, rg, t + 2);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm<kOps>();
+            multiply(r1, XB);
+            wait_lds();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if (t + 1 < batches) {
+            load(r1, XB, rg, t + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm<kOps>();
+            multiply(r0, XA);
+            wait_vm<0>();
+            multiply(r1, XB);
+        } else {
+            wait_vm<0>();
+            if (mine > 0)
+                multiply(r0, XA);
+        }
+        finish(rg, XA);
+    }
+}
+
+template <int G>
+hipError_t launch_lds(SkinnyParams &p, int cus, hipStream_t stream)
+{
+    p.row_groups = p.rt;
+    return launch_kernel(reinterpret_cast<const void *>(&skinny_lds_kernel<G>),
+                         dim3((unsigned)std::min(p.rt, cus * (G == 2 ? 2 : 1))), dim3(512), 0, stream, p);
+}
+
 template <typename SRC, int R, int G, int NW, int U, bool GROUPED>
 hipError_t launch(SkinnyParams &p, int cus, hipStream_t stream)
 {
@@ -376,7 +531,7 @@ hipError_t launch_f8_skinny(const uint8_t *W, const uint8_t *xq, const void *x, 
 {
     const F8Weights f = f8_weights(N, K);
     const F8Acts a = f8_acts(r.x_rows, K);
-    SkinnyParams p{W, xq, x, Y, r, f.scales, a.scales, 1, (int)N, (int)K, f.cb, f.ls, f.rt, 0, y_type, N % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * type_bytes(y_type) - 1)) == 0};
+    SkinnyParams p{W, xq, x, Y, r, f.scales, a.scales, 1, (int)N, (int)K, f.cb, f.ls, a.ls, f.rt, 0, y_type, N % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * type_bytes(y_type) - 1)) == 0};
     if (x)
         return x_type == QG_F32   ? launch<float, 1, 1, 8, 2, false>(p, cus, stream)
                : x_type == QG_F16 ? launch<Fp16, 1, 1, 8, 2, false>(p, cus, stream)
@@ -386,8 +541,8 @@ hipError_t launch_f8_skinny(const uint8_t *W, const uint8_t *xq, const void *x, 
     if (r.rows <= 16)
         return launch<Packed, 1, 1, 8, 2, false>(p, cus, stream);
     if (r.rows <= 32)
-        return launch<Packed, 1, 2, 8, 2, false>(p, cus, stream);
-    return launch<Packed, 1, 4, 8, 2, false>(p, cus, stream);
+        return launch_lds<2>(p, cus, stream);
+    return launch_lds<4>(p, cus, stream);
 }
 
 }  // namespace qg
