@@ -18,7 +18,7 @@
 // A ring of four buffers: during step t the products run on operands read
 // from buffers t and t + 1 (16 rows ahead), X's codes of step t + 3 are
 // widened into their buffer, dY's copies of step t + 3 and the loads of X's
-// codes of step t + 4 are issued.  One barrier a step.
+// codes of step t + 5 are issued.  One barrier a step.
 // Tiles beyond whole rounds of the card's compute units are split along the
 // rows among the units that would be idle; their parts go to the workspace
 // and a second kernel adds them in a fixed order (no atomics).
@@ -36,6 +36,7 @@ namespace {
 constexpr int kStep = 32;     // rows per step
 constexpr int kThreads = 256;
 constexpr int kCus = 256;     // compute units that a round of tiles fills
+constexpr int kPartRows = 1024;
 
 typedef short s4_t __attribute__((ext_vector_type(4)));
 typedef short s8_t __attribute__((ext_vector_type(8)));
@@ -196,9 +197,11 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
     };
     // X: thread -> (row, 16 columns); columns past the last block repeat it
     // (never stored)
-    uint4 codes[NX];
-    uint32_t sbyte[NX], keep[NX];
-    auto load_x = [&](int m) {
+    struct Codes {   // of a step, in registers from two steps before they go to LDS
+        uint4 code[NX];
+        uint32_t sbyte[NX], keep[NX];
+    };
+    auto load_x = [&](Codes &c, int m) {
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
             bool ok = m + x_r[i] < count;
@@ -207,22 +210,23 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
                 ok &= is_slot(x_slot[i]);
                 row = min((int64_t)((uint32_t)(ok ? x_slot[i] : 0) / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1);
             }
-            codes[i] = *reinterpret_cast<const uint4 *>(pick(ok, x_at[i] + row * x_bytes, p.xq));
-            sbyte[i] = *pick(ok, s_at[i] + row * p.x_ls, p.xq);
-            keep[i] = ok ? ~0u : 0u;
+            c.code[i] = *reinterpret_cast<const uint4 *>(pick(ok, x_at[i] + row * x_bytes, p.xq));
+            c.sbyte[i] = *pick(ok, s_at[i] + row * p.x_ls, p.xq);
+            c.keep[i] = ok ? ~0u : 0u;
         }
     };
-    auto store_x = [&](uint4 *X) {
+    auto store_x = [&](Codes &c, uint4 *X) {
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
             const int at = x_r[i] * XC * 2 + 2 * seg_at(x_r[i], (threadIdx.x + kThreads * i) % XC);
-            // what was loaded a step ago is first touched here: without the
+            // what was loaded two steps ago is first touched here: without the
             // pin its users move up behind the load and wait for it there
-            asm volatile("" : "+v"(sbyte[i]), "+v"(codes[i].x), "+v"(codes[i].y), "+v"(codes[i].z), "+v"(codes[i].w));
-            const float s = f8_exponent(sbyte[i]);
-            const uint32_t k = keep[i];
-            X[at] = __builtin_bit_cast(uint4, f8_widen(codes[i].x & k, codes[i].y & k, s));
-            X[at + 1] = __builtin_bit_cast(uint4, f8_widen(codes[i].z & k, codes[i].w & k, s));
+            asm volatile("" : "+v"(c.sbyte[i]), "+v"(c.code[i].x), "+v"(c.code[i].y), "+v"(c.code[i].z),
+                         "+v"(c.code[i].w));
+            const float s = f8_exponent(c.sbyte[i]);
+            const uint32_t k = c.keep[i];
+            X[at] = __builtin_bit_cast(uint4, f8_widen(c.code[i].x & k, c.code[i].y & k, s));
+            X[at + 1] = __builtin_bit_cast(uint4, f8_widen(c.code[i].z & k, c.code[i].w & k, s));
         }
     };
     // eight consecutive rows 16 h + 8 (lane / 32) .. of column 32 t + lane % 32
@@ -280,20 +284,24 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
                 copy_y(ybuf(q), q * kStep);
             else
                 load_y(q * kStep);
-            load_x(q * kStep);
+            Codes c;
+            load_x(c, q * kStep);
             if constexpr (!ALIGNED)
                 store_y(ybuf(q));
-            store_x(xbuf(q));
+            store_x(c, xbuf(q));
         };
         fill(0);
         fill(1);
         fill(2);
         // in registers at the start of a step that multiplies rows m ..: X's
-        // codes (and dY's, unaligned) of m + 3 steps, the slots of what is
-        // loaded next
+        // codes of m + 3 and m + 4 steps (and dY's, unaligned, of m + 3), the
+        // slots of what is loaded next
+        Codes c0, c1;
         load_x_slots(3 * kStep);
-        load_x(3 * kStep);
+        load_x(c0, 3 * kStep);
         load_x_slots(4 * kStep);
+        load_x(c1, 4 * kStep);
+        load_x_slots(5 * kStep);
         load_y_slots(3 * kStep);
         if constexpr (!ALIGNED) {
             load_y(3 * kStep);
@@ -316,13 +324,36 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
                 load_y(m + 4 * kStep);
                 load_y_slots(m + 5 * kStep);
             }
-            store_x(xbuf((q + 3) & 3));
-            load_x(m + 4 * kStep);
-            load_x_slots(m + 5 * kStep);
+            store_x(q & 1 ? c1 : c0, xbuf((q + 3) & 3));
+            // one half's products hide the other half's reads; the copies and
+            // the writes go with the first half, the loads with the second
+            constexpr int kProducts = TM * TN, kReads = 2 * (TM + TN);
+            constexpr int kReadsPer = (kReads + kProducts - 1) / kProducts;
             read(second, xbuf(q), ybuf(q), 1);
             multiply(first);
+#pragma unroll
+            for (int i = 0; i < kProducts; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+                if (i * kReadsPer < kReads)
+                    __builtin_amdgcn_sched_group_barrier(0x100, kReadsPer, 0);   // LDS reads
+                if (ALIGNED && i < NY)
+                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // a copy
+                if (i >= kProducts / 2 && i < kProducts / 2 + 2 * NX)
+                    __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);   // an LDS write
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            load_x(q & 1 ? c1 : c0, m + 5 * kStep);
+            load_x_slots(m + 6 * kStep);
             read(first, xbuf((q + 1) & 3), ybuf((q + 1) & 3), 0);
             multiply(second);
+#pragma unroll
+            for (int i = 0; i < kProducts; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (i * kReadsPer < kReads)
+                    __builtin_amdgcn_sched_group_barrier(0x100, kReadsPer, 0);
+                if (i < 2 * NX)
+                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // a load
+            }
         };
         // whole rounds of four steps: rows past the end are zeros
         for (int m = 0; m < count; m += 4 * kStep) {
@@ -368,32 +399,51 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
 struct JoinParams {
     const float *part;
     float *dW;
-    int N, K, BN, BK, tiles_n, whole, parts;
-    bool accumulate;
+    int N, K, size, tiles_n, whole, parts;
+    bool accumulate, vec;
 };
 
-// A workgroup per four rows of a split tile, a lane per column.
+// A workgroup per 1024 values of a split tile, four columns of a row per lane.
 __global__ __launch_bounds__(256) void join_kernel(JoinParams p)
 {
-    const int tile = blockIdx.x / (p.BN / 4), group = blockIdx.x % (p.BN / 4);
-    const int n0 = ((p.whole + tile) % p.tiles_n) * p.BN, k0 = ((p.whole + tile) / p.tiles_n) * p.BK;
-    const float *from = p.part + (int64_t)tile * p.parts * p.BN * p.BK;
-    for (int i = threadIdx.x; i < 4 * p.BK; i += 256) {
-        const int nn = 4 * group + i / p.BK, kk = i % p.BK;
-        const int n = n0 + nn, k = k0 + kk;
-        if (n >= p.N || k >= p.K)
-            continue;
-        float *to = p.dW + (int64_t)n * p.K + k;
-        float v = p.accumulate ? *to : 0.0f;
-        for (int s = 0; s < p.parts; ++s)
-            v += from[((int64_t)s * p.BN + nn) * p.BK + kk];
-        *to = v;
+    const int groups = p.size * p.size / 1024;
+    const int tile = blockIdx.x / groups, at = (blockIdx.x % groups) * 1024 + 4 * threadIdx.x;
+    const int n = ((p.whole + tile) % p.tiles_n) * p.size + at / p.size;
+    const int k = ((p.whole + tile) / p.tiles_n) * p.size + at % p.size;
+    if (n >= p.N || k >= p.K)
+        return;
+    const float *from = p.part + (int64_t)tile * p.parts * p.size * p.size + at;
+    float *to = p.dW + (int64_t)n * p.K + k;
+    f4_t v = {0, 0, 0, 0};
+    if (p.accumulate) {
+        if (p.vec) {
+            v = *reinterpret_cast<const f4_t *>(to);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = k + e < p.K ? to[e] : 0.0f;
+        }
+    }
+    for (int s = 0; s < p.parts; ++s)
+        v += *reinterpret_cast<const f4_t *>(from + (int64_t)s * p.size * p.size);
+    if (p.vec) {   // K is a multiple of four
+        *reinterpret_cast<f4_t *>(to) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (k + e < p.K)
+                to[e] = v[e];
     }
 }
 
-// How a dense dW is cut: tiles of 256 x 256 where they fill most of a round
-// of compute units, else of 128 x 128; the tiles beyond whole rounds in as
-// many parts as idle units allow, of at least 256 rows.
+// How a dense dW is cut.  Tiles of 256 x 256 where they fill most of a round
+// of compute units (8192 x 6144 x 4096: 406 us, 1016 TFLOP/s), else of
+// 128 x 128, two to a unit.  The tiles beyond whole rounds are cut along the
+// rows in as many parts as idle units allow: 8192 x 6144 x 4096 takes 406 us
+// for 476 without, 16384 x 1024 x 1024 takes 53 for 202.  A part has at least
+// 1024 rows, since the parts' way through memory and the second launch cost
+// more than they save on fewer: 1024 x 2048 x 2048 takes 21 us whole and 34 in
+// parts of 512 rows, 519 x 1288 x 2056 takes 15 whole and 23 in two parts.
 struct Cut {
     int size, tiles_n, tiles, whole, parts;
 };
@@ -406,7 +456,7 @@ Cut cut_of(int64_t M, int64_t N, int64_t K)
     c.tiles = (int)(c.tiles_n * ceil_div(K, c.size));
     const int round = c.size == 256 ? kCus : 2 * kCus;   // two workgroups of the small tiles a unit
     const int rest = c.tiles % round;
-    c.parts = rest ? (int)std::min<int64_t>(round / rest, M / 256) : 1;
+    c.parts = rest ? (int)std::min<int64_t>(round / rest, M / kPartRows) : 1;
     if (c.parts < 2)
         c.parts = 1;
     c.whole = c.parts > 1 ? c.tiles - rest : c.tiles;
@@ -448,9 +498,9 @@ hipError_t launch_f8_wgrad(const uint16_t *dY, const uint8_t *xq, float *dW, boo
     const hipError_t e = c.size == 256 ? launch<4, false>(p, wgs, stream) : launch<2, false>(p, wgs, stream);
     if (e != hipSuccess || c.whole == c.tiles)
         return e;
-    const JoinParams j{workspace, dW, (int)N, (int)K, c.size, c.size, c.tiles_n, c.whole, c.parts, accumulate};
+    const JoinParams j{workspace, dW, (int)N, (int)K, c.size, c.tiles_n, c.whole, c.parts, accumulate, p.vec};
     return launch_kernel(reinterpret_cast<const void *>(&join_kernel),
-                         dim3((unsigned)((c.tiles - c.whole) * (c.size / 4))), dim3(256), 0, stream, j);
+                         dim3((unsigned)((c.tiles - c.whole) * (c.size * c.size / 1024))), dim3(256), 0, stream, j);
 }
 
 }  // namespace qg
