@@ -60,7 +60,7 @@ enum { QG_F32 = 0, QG_F16 = 1, QG_BF16 = 2 };
 /* ------------------------------------------------------------ host side */
 
 /* Bytes of one packed N x K weight matrix, and of packed M x K activations;
- * 0 if a size is < 1, K > 2^20 or a row count > 2^31 - 1. */
+ * 0 if a size is < 1, K > 2^20 or a row count > 2^30. */
 size_t qpacked_bytes_f8(int64_t N, int64_t K);
 size_t qact_bytes_f8(int64_t M, int64_t K);
 
@@ -71,7 +71,7 @@ qg_status qquantize_f8(const float *w, int64_t N, int64_t K, void *packed, size_
 
 /* ----------------------------------------------------------- device side
  * Packed buffers are 256-byte aligned, workspaces 16-byte, other pointers to
- * the size of their elements.  1 <= N, M <= 2^31 - 1,
+ * the size of their elements.  1 <= N, M <= 2^30,
  * 1 <= K <= 2^20 (and N <= 2^20 where N is the summed side). */
 
 /* Packed weights -> out[N][K], fp32 (out_fp16 = 0) or fp16 rounded to nearest
@@ -156,8 +156,9 @@ qg_status qmoe_route_backward(const void *logits, int type, int64_t ldl, const u
  *   Y[s][n] = sum_k X[s / k_slots][k] W_e[n][k],
  * and Y[s] = 0 for the slots from offsets[P] on.  pool: P packed N x K
  * matrices, qpacked_bytes_f8(N, K) apart, 1 <= P <= 512; xq: packed T x K
- * activations, 1 <= k_slots <= 16, T k_slots <= 2^31 - 1; order int32 [T k_slots], offsets int32 [P + 1] (device, as
- * qmoe_route writes them); Y: y_type [T k_slots][N].  With k_slots = 1, X has
+ * activations, 1 <= k_slots <= 16, T k_slots <= 2^30, T ceil(K / 128) <=
+ * 2^25 - 2 (X's codes within 4 GiB); order int32 [T k_slots], offsets int32
+ * [P + 1] (device, as qmoe_route writes them); Y: y_type [T k_slots][N].  With k_slots = 1, X has
  * a row for each slot (the second product of an expert).  An entry of order
  * outside 0 .. T k_slots - 1 is skipped, offsets are held to 0 .. T k_slots. */
 qg_status qmoe_gemm_f8(const void *pool, int64_t P, const void *xq, int64_t T, int k_slots, const int32_t *order,

@@ -131,16 +131,18 @@ struct WeightArgs {
 template <typename T>
 __global__ __launch_bounds__(256) void f8_dequant_kernel(WeightArgs a)
 {
-    const int t = blockIdx.x;
-    for (int i = threadIdx.x; i < 16 * 8 * a.cb; i += 256) {
-        const int r = i / (8 * a.cb), ch = i % (8 * a.cb);
-        const int n = 16 * t + r, k = 16 * ch;
-        if (n >= a.N || k >= a.K)
-            continue;
-        float v[16];
-        widen16(*reinterpret_cast<const uint4 *>(a.W + ((int64_t)t * a.cb + ch / 8) * 2048 + 256 * (ch & 7) + 16 * r),
-                f8_scale(a.W[a.scales + (int64_t)(n >> 7) * a.ls + (ch >> 3)]), v);
-        store_row(static_cast<T *>(a.out) + (int64_t)n * a.K + k, a.K - k, v);
+    for (int t = blockIdx.x; t < a.rt; t += gridDim.x) {
+        for (int i = threadIdx.x; i < 16 * 8 * a.cb; i += 256) {
+            const int r = i / (8 * a.cb), ch = i % (8 * a.cb);
+            const int n = 16 * t + r, k = 16 * ch;
+            if (n >= a.N || k >= a.K)
+                continue;
+            float v[16];
+            widen16(*reinterpret_cast<const uint4 *>(a.W + ((int64_t)t * a.cb + ch / 8) * 2048 + 256 * (ch & 7) +
+                                                     16 * r),
+                    f8_scale(a.W[a.scales + (int64_t)(n >> 7) * a.ls + (ch >> 3)]), v);
+            store_row(static_cast<T *>(a.out) + (int64_t)n * a.K + k, a.K - k, v);
+        }
     }
 }
 
@@ -236,7 +238,7 @@ hipError_t launch_f8_dequant(const uint8_t *W, int64_t N, int64_t K, bool fp16, 
 {
     WeightArgs a = weight_args(W, N, K);
     a.out = out;
-    return go(fp16 ? &f8_dequant_kernel<Fp16> : &f8_dequant_kernel<float>, dim3(a.rt), a, stream);
+    return go(fp16 ? &f8_dequant_kernel<Fp16> : &f8_dequant_kernel<float>, dim3((unsigned)std::min(a.rt, 1 << 22)), a, stream);
 }
 
 hipError_t launch_f8_transpose(const uint8_t *W, int64_t N, int64_t K, uint8_t *WT, hipStream_t stream)

@@ -10,6 +10,9 @@
 namespace qg {
 namespace {
 
+// Rows of X of an expert call are gathered with 32-bit offsets.
+constexpr int64_t kF8MaxMoeBlocks = ((int64_t)1 << 25) - 2;
+
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 inline qg_status status(hipError_t e) { return e == hipSuccess ? QG_OK : QG_ERR_LAUNCH; }
@@ -36,8 +39,8 @@ qg_status check_route(const void *logits, int type, int64_t ldl, int64_t T, int6
 {
     if (!logits || !idx || !weight || !counts)
         return QG_ERR_NULL;
-    if (!type_ok(type) || T < 1 || T > kRouteMaxTokens || E < 1 || E > kMaxExperts || ldl < E || k < 1 || k > E ||
-        k > kMaxTopK)
+    if (!type_ok(type) || T < 1 || T > kRouteMaxTokens || E < 1 || E > kMaxExperts || ldl < E || ldl > INT64_MAX / 4 / T ||
+        k < 1 || k > E || k > kMaxTopK)
         return QG_ERR_SHAPE;
     if (!aligned(logits, type_bytes(type)) || !aligned(idx, 4) || !aligned(weight, 4) || !aligned(counts, 4))
         return QG_ERR_ALIGN;
@@ -201,7 +204,7 @@ qg_status qmoe_gemm_f8(const void *pool, int64_t P, const void *xq, int64_t T, i
     const qg_status st = check_slots(P, T, k_slots, order, offsets);
     if (st != QG_OK)
         return st;
-    if (!type_ok(y_type) || !rows_ok(N) || !k_ok(K))
+    if (!type_ok(y_type) || !rows_ok(N) || !k_ok(K) || T * ceil_div(K, 128) > kF8MaxMoeBlocks)
         return QG_ERR_SHAPE;
     if (!aligned(pool, 256) || !aligned(xq, 256) || !aligned(Y, type_bytes(y_type)))
         return QG_ERR_ALIGN;

@@ -14,7 +14,7 @@
 namespace qg {
 
 constexpr int64_t kF8MaxK = 1 << 20;
-constexpr int64_t kF8MaxRows = INT32_MAX;
+constexpr int64_t kF8MaxRows = 1 << 30;       // row numbers, a tile or a few steps on, fit 31 bits
 constexpr int64_t kF8MaxGemvK = 16384;        // 128 KiB of codes in LDS
 constexpr int64_t kRouteMaxTokens = 1 << 24;
 constexpr int kMaxExperts = 512;

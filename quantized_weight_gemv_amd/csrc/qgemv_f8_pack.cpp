@@ -12,6 +12,7 @@
 namespace {
 
 constexpr int64_t kMaxK = 1 << 20;
+constexpr int64_t kMaxRows = 1 << 30;
 
 // The e4m3 code of v, |v| <= 448: the grid's step is 2^(x - 3) for 2^x <= |v|
 // < 2^(x + 1) and 2^-9 below 2^-6.  nearbyint rounds ties to even (the
@@ -40,7 +41,7 @@ extern "C" {
 
 size_t qpacked_bytes_f8(int64_t N, int64_t K)
 {
-    if (N < 1 || K < 1 || N > INT32_MAX || K > kMaxK)
+    if (N < 1 || K < 1 || N > kMaxRows || K > kMaxK)
         return 0;
     const size_t cb = (K + 127) / 128, rt = (N + 15) / 16, rb = (N + 127) / 128;
     return (rt * cb * 2048 + rb * ((cb + 3) / 4 * 4) + 255) / 256 * 256;
@@ -48,7 +49,7 @@ size_t qpacked_bytes_f8(int64_t N, int64_t K)
 
 size_t qact_bytes_f8(int64_t M, int64_t K)
 {
-    if (M < 1 || K < 1 || M > INT32_MAX || K > kMaxK)
+    if (M < 1 || K < 1 || M > kMaxRows || K > kMaxK)
         return 0;
     const size_t cb = (K + 127) / 128, m = M;
     return ((m * cb * 128 + 255) / 256 * 256 + m * ((cb + 3) / 4 * 4) + 255) / 256 * 256;

@@ -223,8 +223,8 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
             // pin its users move up behind the load and wait for it there
             asm volatile("" : "+v"(c.sbyte[i]), "+v"(c.code[i].x), "+v"(c.code[i].y), "+v"(c.code[i].z),
                          "+v"(c.code[i].w));
-            const float s = f8_exponent(c.sbyte[i]);
-            const uint32_t k = c.keep[i];
+            const uint32_t k = c.keep[i];   // a masked row's byte is any byte: not the scale of its zeros
+            const float s = f8_exponent(c.sbyte[i] & k);
             X[at] = __builtin_bit_cast(uint4, f8_widen(c.code[i].x & k, c.code[i].y & k, s));
             X[at + 1] = __builtin_bit_cast(uint4, f8_widen(c.code[i].z & k, c.code[i].w & k, s));
         }

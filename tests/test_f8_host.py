@@ -133,3 +133,20 @@ def test_binding_refuses_host_tensors_and_bad_sizes():
                  lambda: q.qmoe_gemm_f8(t, 1, t, 4, t, t, 8, 8), lambda: q.qtranspose_f8(t, 8, 8)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_limits_of_rows_and_slots():
+    """Sizes whose row numbers or gathered offsets would not fit are refused before the device is touched."""
+    q = _qg()
+    L = q.lib()
+    a = 1 << 20
+    assert q.qact_bytes_f8(2 ** 30, 1) == 2 ** 30 * 132 and q.qact_bytes_f8(2 ** 30 + 1, 1) == 0
+    assert L.qgemm_f8(a, a, a, 0, 2 ** 30 + 1, 8, 8, None) == 2
+    assert L.qgemm_f8_wgrad(a, a, a, 0, 2 ** 30 + 1, 8, 8, a, None) == 2
+    assert L.qgemm_f8_wgrad_workspace(2 ** 30 + 1, 8, 8) == 0
+    assert L.qmoe_gemm_f8(a, 4, a, 2 ** 26 + 1, 16, a, a, a, 0, 8, 8, None) == 2             # slots
+    assert L.qmoe_gemm_f8_wgrad(a, a, 2 ** 26 + 1, 16, a, a, 4, a, 0, 8, 8, None) == 2
+    assert L.qmoe_gemm_f8(a, 4, a, 2 ** 20, 2, a, a, a, 0, 64, 4096, None) == 2               # 4 GiB of codes
+    assert L.qmoe_gemm_f8(a, 4, a, 2 ** 25 - 1, 1, a, a, a, 0, 64, 1, None) == 2
+    route = [a, 0, 2 ** 60, None, 8, 64, 4, 1, a, a, a, a, a, a, None, None]
+    assert L.qmoe_route(*route) == 2                                                          # rows beyond 63 bits
