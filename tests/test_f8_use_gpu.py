@@ -285,10 +285,12 @@ def test_far_rows_of_weights():
     for M in (12, 30, 64, 70):
         xq = q.qact_quantize_f8(x[:M])
         a, b = q.qgemm_f8(W, xq, M, N, K), q.qgemm_f8(small, xq, M, last, K)
-        if M <= 64:
+        if M <= 32:
             assert torch.equal(a[:, N - last:], b), M
         else:
-            d = (a[:, N - last:] - b).abs().double()     # another tile shape: another order of the sums
+            # other kernels for other N, so another order of the sums: each result is within the stated bound of
+            # the exact sum, and two of them within twice that of each other
+            d = (a[:, N - last:] - b).abs().double()
             xv = q.qact_dequant_f8(xq, M, K).abs().double()
             size = xv @ q.qdequant_f8(small, last, K).abs().double().t().contiguous()
             assert (d <= 2 * fu.sum_bound(1.0, K) * size).all()
