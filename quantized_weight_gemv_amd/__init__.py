@@ -575,15 +575,17 @@ def qmoe_route(logits, k: int, mask=None, renormalize: bool = True) -> MoeRoute:
     code = _type(logits.dtype)
     if not (1 <= k <= min(E, 16) and 1 <= T <= 1 << 24 and E <= 512):
         raise QGError("qmoe_route", 2)
-    S, i32, f32 = T * k, torch.int32, torch.float32
-    idx, weight, order, loss = c.new((T, k), i32), c.new((T, k), f32), c.new((S,), i32), c.new((1,), f32)
-    both = c.new((2 * E + 2,), i32)
-    at = both.data_ptr()
+    # one buffer a type: tensors are made faster by splitting one (0.4 us each) than one by one (1.5)
+    S = T * k
+    ints, floats = c.new((2 * S + 2 * E + 2,), torch.int32), c.new((S + 1,), torch.float32)
+    ip, fp = ints.data_ptr(), floats.data_ptr()
     ws = int(lib().qmoe_route_workspace(T, E))
     w = c.new((ws,), torch.uint8) if ws else None
-    c("qmoe_route", logits.data_ptr(), code, ld, mp, T, E, k, int(renormalize), idx.data_ptr(), weight.data_ptr(),
-      at, at + 4 * (E + 1), order.data_ptr(), loss.data_ptr(), w.data_ptr() if ws else None)
-    counts, tokens, offsets = both.split((E, 1, E + 1))
+    c("qmoe_route", logits.data_ptr(), code, ld, mp, T, E, k, int(renormalize), ip, fp, ip + 8 * S,
+      ip + 8 * S + 4 * (E + 1), ip + 4 * S, fp + 4 * S, w.data_ptr() if ws else None)
+    idx, order, counts, tokens, offsets = ints.split_with_sizes((S, S, E, 1, E + 1))
+    weight, loss = floats.split_with_sizes((S, 1))
+    idx, weight = idx.view(T, k), weight.view(T, k)
     return MoeRoute(idx, weight, counts, tokens, offsets, order, loss)
 
 

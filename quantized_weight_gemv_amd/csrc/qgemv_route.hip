@@ -1,19 +1,31 @@
 // Expert routing: top-k softmax, per-expert counts, the slots sorted by
 // expert, the balance loss and its gradient (definitions in qgemv_f8.h).
 //
-// A wave holds a token: lane l has the J = ceil(E / 64) logits of experts
-// l J .. l J + J - 1, so that the lowest lane of a tie is the lowest expert.
-// The forward pass reads each logit once.  Beyond one workgroup's tokens it
-// is three launches, because the sorted order of a slot needs the counts of
-// every expert:
+// L lanes hold a token, a wave 64 / L of them: lane l has the logits of experts
+// l J .. l J + J - 1.  Bound by instructions (the k rounds of the selection),
+// not by the logits' bytes: in each round a lane's J values cost a few
+// instructions each, for all of the wave's tokens at once, the reduction over
+// the lanes four to six.  Measured forward + backward (us, bf16; L 16 / 32 /
+// 64): 16384 tokens of 256 experts, 8 each: 23 + 15 / 24 + 15 / 28 + 11; of
+// 512, 10 each: 46 + 31 / 34 + 25 / 37 + 21; of 64, 6 each: 16 + 5 / 18 + 5 /
+// 21 + 6; 4 tokens of 128, 10 each (one workgroup): 7 / 6 / 6 forward; 64
+// tokens: 9 / 11 / 15.  So many tokens take L = 16, with 512 experts 32, the
+// one workgroup of a decode step 32, the backward pass, which has no rounds
+// and many values in registers, 32 and from 256 experts on 64.
+// The forward pass reads each logit once.  Beyond one workgroup's tokens it is
+// three launches, because the sorted order of a slot needs the counts of every
+// expert:
 //   1. tokens: each workgroup ("chunk") routes its tokens and leaves its
 //      counts and its sums of p per expert;
 //   2. experts: the counts of the chunks before each chunk, the totals;
 //   3. slots: offsets from the totals, every slot to its place, the loss.
-// Up to kOneChunk tokens one workgroup does all of it in one launch (a decode
-// step is bound by launches, not by bytes).
-// All sums run in a fixed order (a lane's tokens, the waves, the chunks), so
-// results repeat bit for bit; only whole numbers are counted with atomics.
+// 16384 x 256: 14, 6 and 5 us (the launches' own latencies in the last two),
+// the backward pass 11; 8.4 MB of logits, read twice, and their gradient would
+// take 5 us at the copy rate.  Up to kChunkTokens tokens one workgroup does all
+// of it in one launch.
+// All sums run in a fixed order (a lane's tokens, the wave's, the waves, the
+// chunks), so results repeat bit for bit; only whole numbers are counted with
+// atomics.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -45,44 +57,56 @@ __device__ __forceinline__ float value_of(uint32_t key)
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
-// Reductions over the wave with data-parallel-primitive moves: a few cycles a
-// step where a shuffle through LDS takes over a hundred, and the k rounds of
-// the selection are a chain of them.  Neighbours, pairs, halves and whole rows
-// of 16 first, then the rows' results one row on and two rows on; lane 63 has
-// all of it.
-template <int CTRL, int ROWS>
+// Reductions over a token's L lanes with data-parallel-primitive moves, every
+// lane gets the result: neighbours, pairs, halves and whole rows of 16; a few
+// cycles a step where a shuffle through LDS takes over a hundred.  Rows and
+// halves of the wave are exchanged by register swaps.
+template <int CTRL>
 __device__ __forceinline__ uint32_t moved(uint32_t v)
 {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
 
-template <typename OP>
-__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, OP op)
+template <int L, typename OP>
+__device__ __forceinline__ uint32_t reduce(uint32_t v, OP op)
 {
-    v = op(v, moved<0xB1, 0xF>(v));    // lanes 1 0 3 2 of each quad
-    v = op(v, moved<0x4E, 0xF>(v));    // lanes 2 3 0 1
-    v = op(v, moved<0x141, 0xF>(v));   // mirror of each half row
-    v = op(v, moved<0x140, 0xF>(v));   // mirror of each row
-    v = op(v, moved<0x142, 0xA>(v));   // lane 15 of a row into rows 1 and 3
-    v = op(v, moved<0x143, 0xC>(v));   // lane 31 into rows 2 and 3
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    v = op(v, moved<0xB1>(v));    // lanes 1 0 3 2 of each quad
+    v = op(v, moved<0x4E>(v));    // lanes 2 3 0 1
+    v = op(v, moved<0x141>(v));   // mirror of each half row
+    v = op(v, moved<0x140>(v));   // mirror of each row
+    if constexpr (L >= 32) {   // rows 0 0 2 2 and 1 1 3 3
+        const auto rows = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = op(rows[0], rows[1]);
+    }
+    if constexpr (L == 64) {   // lower halves and upper halves
+        const auto halves = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = op(halves[0], halves[1]);
+    }
+    return v;
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+template <int L>
+__device__ __forceinline__ uint32_t max_of(uint32_t v)
 {
-    return wave_reduce(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+    return reduce<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+template <int L>
+__device__ __forceinline__ uint32_t min_of(uint32_t v)
 {
-    return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return reduce<L>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+
+template <int L>
+__device__ __forceinline__ float sum_of(float v)
+{
+    return __uint_as_float(reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
 }
 
-// Softmax of a token: this lane's p of its J experts.  `any` = the token is
-// live; a NaN or +infinity among its logits makes every p NaN (the sum is).
-// VEC: rows start at multiples of a lane's J elements and E is one, too.
+// This lane's logits of a token; vec: a lane's J elements are aligned vectors,
+// and E is a multiple of J.
 template <int J, typename T>
 __device__ __forceinline__ void load_logits(const T *row, int E, int lane, bool vec, T (&raw)[J])
 {
@@ -116,15 +140,18 @@ __device__ __forceinline__ float exp_of(float x)
     return x < -104.0f ? 0.0f : __builtin_fmaf(e * kLn2, low, e);
 }
 
-template <int J>
+// Softmax of a token: this lane's p of its J experts; returns whether the
+// token is live.  A NaN or +infinity among its logits makes every p NaN (the
+// sum is).
+template <int L, int J>
 __device__ __forceinline__ bool softmax(const float (&x)[J], float (&p)[J], float &top, float &inv)
 {
     uint32_t best = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j)
         best = max(best, key_of(x[j]));
-    best = wave_max(best);
-    const bool live = best != 0;   // uniform
+    best = max_of<L>(best);
+    const bool live = best != 0;
     top = value_of(best);
     float s = 0.0f;
 #pragma unroll
@@ -132,7 +159,7 @@ __device__ __forceinline__ bool softmax(const float (&x)[J], float (&p)[J], floa
         p[j] = live ? exp_of(x[j] - top) : 0.0f;
         s += p[j];
     }
-    inv = 1.0f / wave_sum(s);
+    inv = 1.0f / sum_of<L>(s);
 #pragma unroll
     for (int j = 0; j < J; ++j)
         p[j] = live ? p[j] * inv : 0.0f;
@@ -142,12 +169,10 @@ __device__ __forceinline__ bool softmax(const float (&x)[J], float (&p)[J], floa
 // The k largest logits of a token, one after the other; lane q gets the q-th
 // one's expert (-1: none is open any more) and its value.
 //   16-bit logits: a word holds the logit's 16-bit key and below it the
-//   expert's number, inverted, so the wave's largest word is the choice, ties
-//   and all.
-//   fp32: the wave's largest key, the first lane that holds it, that lane's
-//   first such expert.
-template <int J, typename T>
-__device__ __forceinline__ void choose(const T (&raw)[J], const float (&x)[J], int lane, int k, int &my_idx,
+//   expert's number, inverted, so the largest word is the choice, ties and all.
+//   fp32: the largest key, then the lowest expert that has it.
+template <int L, int J, typename T>
+__device__ __forceinline__ void choose(const T (&raw)[J], const float (&x)[J], int l, int k, int &my_idx,
                                        float &my_value)
 {
     constexpr bool kHalf = sizeof(T) == 2;
@@ -156,8 +181,9 @@ __device__ __forceinline__ void choose(const T (&raw)[J], const float (&x)[J], i
     for (int j = 0; j < J; ++j) {
         if constexpr (kHalf) {
             const uint32_t b = raw[j].u == 0x8000u ? 0u : raw[j].u;   // -0 as +0
-            const uint32_t ordered = (b & 0x8000u ? ~b : b | 0x8000u) << 16;
-            key[j] = x[j] > -__builtin_inff() ? ordered | (0xFFFFu - (uint32_t)(lane * J + j)) : 0u;
+            const uint32_t ordered = (b ^ (b & 0x8000u ? 0xFFFFu : 0x8000u)) << 16;
+            const uint32_t word = ordered | (0xFFFFu - (uint32_t)(l * J + j));
+            key[j] = x[j] > -__builtin_inff() ? word : 0u;
         } else {
             key[j] = key_of(x[j]);
         }
@@ -169,28 +195,26 @@ __device__ __forceinline__ void choose(const T (&raw)[J], const float (&x)[J], i
 #pragma unroll
         for (int j = 0; j < J; ++j)
             best = max(best, key[j]);
-        const uint32_t all = wave_max(best);
-        if (all == 0)
-            break;   // uniform
-        int e;
+        const uint32_t all = max_of<L>(best);
+        uint32_t e;
         if constexpr (kHalf) {
-            e = (int)(0xFFFFu - (all & 0xFFFFu));
+            e = 0xFFFFu - (all & 0xFFFFu);
 #pragma unroll
             for (int j = 0; j < J; ++j)
                 key[j] = key[j] == all ? 0 : key[j];
         } else {
-            const int src = __ffsll((unsigned long long)__ballot(best == all)) - 1;
-            int at = 0;
+            uint32_t at = ~0u;
 #pragma unroll
             for (int j = J - 1; j >= 0; --j)
-                at = key[j] == all ? j : at;
-            e = __builtin_amdgcn_readlane(lane * J + at, src);
+                at = key[j] == all ? (uint32_t)(l * J + j) : at;
+            e = min_of<L>(at);
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                key[j] = lane * J + j == e ? 0 : key[j];
+                key[j] = (uint32_t)(l * J + j) == e ? 0 : key[j];
         }
-        my_idx = lane == q ? e : my_idx;
-        my_key = lane == q ? all : my_key;
+        const bool mine = l == q && all != 0;
+        my_idx = mine ? (int)e : my_idx;
+        my_key = mine ? all : my_key;
     }
     if constexpr (kHalf) {
         const uint32_t b = my_key >> 16;
@@ -227,14 +251,13 @@ __device__ __forceinline__ void clear(Lds &s, int E)
     __syncthreads();
 }
 
-// Marks the slots of token i of the chunk; idx: the choice of lane `lane` < k.
-__device__ __forceinline__ void mark(Lds &s, int i, int lane, int k, int idx)
+// Marks a slot of token i of the chunk.
+__device__ __forceinline__ void mark(Lds &s, int i, int idx)
 {
-    if (lane < k && idx >= 0)
+    if (idx >= 0)
         atomicOr(&s.tokens[idx], 1ull << i);
-    const unsigned long long chosen = __ballot(lane < k && idx >= 0);
-    if (lane == 0)
-        s.dropped[i] = k - __popcll(chosen);
+    else
+        atomicAdd(&s.dropped[i], 1);
 }
 
 // Slots of the chunk per expert, without one (E) and live tokens (E + 1).
@@ -252,59 +275,64 @@ __device__ __forceinline__ int count_of(const Lds &s, int e, int E)
 
 // Routes the tokens t0 .. t0 + n - 1 of a workgroup: idx and weight to memory,
 // marks and the waves' sums of p to LDS.
-template <int J, typename T>
+template <int L, int J, typename T>
 __device__ __forceinline__ void route_tokens(const RouteArgs &a, int64_t t0, int n, Lds &s)
 {
+    constexpr int kTokens = 64 / L;   // of a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int l = lane % L, own = wave * kTokens + lane / L;
     const int E = a.E, k = a.k;
     const T *const logits = static_cast<const T *>(a.logits);
-    T raw[J], next[J];
-    int routed = 0, next_routed = 0;
-    auto load = [&](int i, T(&r)[J], int &on) {
-        const int64_t t = t0 + min(i, n - 1);
-        load_logits<J>(logits + t * a.ldl, E, lane, a.vec, r);
-        on = a.mask ? a.mask[t] : 1;
-    };
-    load(wave, raw, routed);
-    clear(s, E);
     float psum[J];
 #pragma unroll
     for (int j = 0; j < J; ++j)
         psum[j] = 0.0f;
-    for (int i = wave; i < n; i += kWaves) {
-        load(i + kWaves, next, next_routed);   // in flight while this token is worked on
-        const int64_t t = t0 + i;
+    for (int i0 = 0; i0 < n; i0 += kWaves * kTokens) {
+        const bool any = i0 + wave * kTokens < n;   // uniform over the wave
+        const int i = i0 + own;
+        const int64_t t = t0 + min(i, n - 1);   // past the end: the last token, unrouted
+        T raw[J];
+        int routed = 0;
+        if (any) {
+            load_logits<J>(logits + t * a.ldl, E, l, a.vec, raw);
+            routed = a.mask ? a.mask[t] : 1;
+        }
+        if (i0 == 0)
+            clear(s, E);   // behind the first loads
+        if (!any)
+            break;
         float x[J], p[J];
-        open_logits<J>(raw, E, lane, routed != 0, x);
+        open_logits<J>(raw, E, l, routed != 0 && i < n, x);
         float top, inv;
-        const bool live = softmax<J>(x, p, top, inv);
+        const bool live = softmax<L, J>(x, p, top, inv);
 #pragma unroll
         for (int j = 0; j < J; ++j)
             psum[j] += p[j];
         int my_idx;
         float my_value;
-        choose<J, T>(raw, x, lane, k, my_idx, my_value);
+        choose<L, J, T>(raw, x, l, k, my_idx, my_value);
         float my_w = my_idx >= 0 ? exp_of(my_value - top) * inv : 0.0f;
         if (a.renormalize) {
-            const float total = wave_sum(my_w);
+            const float total = sum_of<L>(my_w);
             my_w = my_idx >= 0 && total != 0.0f ? my_w / total : 0.0f;
         }
-        if (lane < k) {
-            a.idx[t * k + lane] = my_idx;
-            a.weight[t * k + lane] = my_w;
+        if (l < k && i < n) {
+            a.idx[t * k + l] = my_idx;
+            a.weight[t * k + l] = my_w;
+            mark(s, i, my_idx);
         }
-        mark(s, i, lane, k, my_idx);
-        if (lane == 0 && live)
+        if (l == 0 && live)
             atomicAdd(&s.live, 1);
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-            raw[j] = next[j];
-        routed = next_routed;
     }
+    // the sums over a wave's tokens
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-        if (lane * J + j < E)
+    for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int d = L; d < 64; d *= 2)
+            psum[j] += __shfl_xor(psum[j], d);
+        if (lane < L && lane * J + j < E)
             s.sums[wave][lane * J + j] = psum[j];
+    }
     __syncthreads();
 }
 
@@ -399,7 +427,7 @@ __device__ __forceinline__ void place_slots(const RouteArgs &a, const Lds &s, co
     }
 }
 
-template <int J, typename T>
+template <int L, int J, typename T>
 __global__ __launch_bounds__(kThreads) void route_one_kernel(Route r)
 {
     __shared__ Lds s;
@@ -407,7 +435,7 @@ __global__ __launch_bounds__(kThreads) void route_one_kernel(Route r)
     __shared__ double scratch[kWaves];
     __shared__ int32_t counts[kBins + 1];
     const RouteArgs &a = r.a;
-    route_tokens<J, T>(a, 0, (int)a.T, s);
+    route_tokens<L, J, T>(a, 0, (int)a.T, s);
     for (int e = threadIdx.x; e < a.E + 2; e += kThreads)
         counts[e] = count_of(s, e, a.E);
     __syncthreads();   // idx is read back below by other threads of this workgroup
@@ -416,13 +444,13 @@ __global__ __launch_bounds__(kThreads) void route_one_kernel(Route r)
     place_slots(a, s, base, 0, (int)a.T);
 }
 
-template <int J, typename T>
+template <int L, int J, typename T>
 __global__ __launch_bounds__(kThreads) void route_tokens_kernel(Route r)
 {
     __shared__ Lds s;
     const RouteArgs &a = r.a;
     const int64_t t0 = (int64_t)blockIdx.x * kChunkTokens;
-    route_tokens<J, T>(a, t0, (int)min((int64_t)kChunkTokens, a.T - t0), s);
+    route_tokens<L, J, T>(a, t0, (int)min((int64_t)kChunkTokens, a.T - t0), s);
     for (int e = threadIdx.x; e < a.E + 2; e += kThreads)
         r.chunk_counts[(int64_t)blockIdx.x * (a.E + 2) + e] = count_of(s, e, a.E);
     for (int e = threadIdx.x; e < a.E; e += kThreads)
@@ -482,14 +510,14 @@ __global__ __launch_bounds__(kThreads) void route_slots_kernel(Route r)
     __shared__ Lds s;
     __shared__ double scratch[kWaves];
     const RouteArgs &a = r.a;
-    const int E = a.E, lane = threadIdx.x & 63;
+    const int E = a.E;
     const int64_t t0 = (int64_t)blockIdx.x * kChunkTokens;
     const int n = (int)min((int64_t)kChunkTokens, a.T - t0);
     for (int e = threadIdx.x; e < E + 2; e += kThreads)
         counts[e] = r.totals[e];
     clear(s, E);
-    for (int i = threadIdx.x >> 6; i < n; i += kWaves)
-        mark(s, i, lane, a.k, lane < a.k ? a.idx[(t0 + i) * a.k + lane] : -1);
+    for (int i = threadIdx.x; i < n * a.k; i += kThreads)
+        mark(s, i / a.k, a.idx[t0 * a.k + i]);
     __syncthreads();
     bases(counts, E, base);
     if (blockIdx.x == 0) {
@@ -506,25 +534,28 @@ __global__ __launch_bounds__(kThreads) void route_slots_kernel(Route r)
 // (k n^2), and for the chosen experts the gradient through the weights: with
 // renormalized weights w_j (g_j - sum_i g_i w_i); without, p_j g_j enters the
 // sum and the product with p like dp.
-template <int J, typename T>
+template <int L, int J, typename T>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a)
 {
-    const int lane = threadIdx.x & 63;
+    constexpr int kTokens = 64 / L;   // of a wave
+    const int l = threadIdx.x % L;
     const int E = a.E, k = a.k;
     const double n = a.counts[E];
     const float unit = a.grad_loss && n > 0 ? (float)((double)*a.grad_loss * E / (n * n * k)) : 0.0f;
     float dp0[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        const int e = lane * J + j;
+        const int e = l * J + j;
         dp0[j] = e < E && a.grad_loss ? unit * (float)a.counts[e] : 0.0f;
     }
-    __shared__ float given[4][64 * J];
+    __shared__ float given[256 / L][L * J];   // a row a token
+    float *const mine = given[threadIdx.x / L];
 #pragma unroll
     for (int j = 0; j < J; ++j)
-        given[threadIdx.x >> 6][lane * J + j] = 0.0f;
+        mine[l * J + j] = 0.0f;
     const T *const logits = static_cast<const T *>(a.logits);
-    const int64_t first = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), stride = (int64_t)gridDim.x * 4;
+    const int64_t first = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), stride = (int64_t)gridDim.x * 4;   // of waves
+    const int own = (threadIdx.x & 63) / L;
     struct Row {
         T raw[J];
         int routed, idx;
@@ -532,42 +563,43 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a)
     };
     auto load = [&](int64_t t, Row &r) {
         t = min(t, a.T - 1);
-        load_logits<J>(logits + t * a.ldl, E, lane, a.vec, r.raw);
+        load_logits<J>(logits + t * a.ldl, E, l, a.vec, r.raw);
         r.routed = a.mask ? a.mask[t] : 1;
         r.idx = -1, r.w = r.g = 0.0f;
-        if (lane < k && a.grad_weight) {
-            const int e = a.idx[t * k + lane];
+        if (l < k && a.grad_weight) {
+            const int e = a.idx[t * k + l];
             r.idx = (uint32_t)e < (uint32_t)E ? e : -1;
-            r.w = a.weight[t * k + lane];
-            r.g = a.grad_weight[t * k + lane];
+            r.w = a.weight[t * k + l];
+            r.g = a.grad_weight[t * k + l];
         }
     };
     Row row, next;
-    load(first, row);
-    for (int64_t t = first; t < a.T; t += stride) {
-        load(t + stride, next);   // in flight while this token is worked on
+    load(first * kTokens + own, row);
+    for (int64_t at = first; at * kTokens < a.T; at += stride) {
+        const int64_t t = at * kTokens + own;
+        if ((at + stride) * kTokens < a.T)
+            load(t + stride * kTokens, next);   // in flight while these tokens are worked on
         float x[J], p[J], dp[J], own[J];
-        open_logits<J>(row.raw, E, lane, row.routed != 0, x);
+        open_logits<J>(row.raw, E, l, row.routed != 0, x);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             dp[j] = dp0[j];
             own[j] = 0.0f;
         }
         float top, inv;
-        const bool live = softmax<J>(x, p, top, inv);
+        const bool live = softmax<L, J>(x, p, top, inv);
         if (a.grad_weight) {
             const float w = row.idx >= 0 ? row.w : 0.0f, g = row.idx >= 0 ? row.g : 0.0f;
-            const float c = a.renormalize ? wave_sum(w * g) : 0.0f;
+            const float c = a.renormalize ? sum_of<L>(w * g) : 0.0f;
             const float d = a.renormalize ? w * (g - c) : g;
             // from the lanes of the k choices to the lanes of their experts,
-            // through this wave's row in LDS (zeros but for the choices)
-            float *mine = &given[threadIdx.x >> 6][0];
+            // through the token's row in LDS (zeros but for the choices)
             if (row.idx >= 0)
                 mine[row.idx] = d;
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-                const float v = mine[lane * J + j];
+                const float v = mine[l * J + j];
                 own[j] = a.renormalize ? v : 0.0f;
                 dp[j] += a.renormalize ? 0.0f : v;
             }
@@ -580,20 +612,22 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradArgs a)
 #pragma unroll
         for (int j = 0; j < J; ++j)
             s += p[j] * dp[j];
-        s = wave_sum(s);
+        s = sum_of<L>(s);
         T *out = static_cast<T *>(a.dlogits) + t * E;
         T res[J];
 #pragma unroll
         for (int j = 0; j < J; ++j)
             res[j] = from_f32<T>(live && x[j] > -__builtin_inff() ? own[j] + p[j] * (dp[j] - s) : 0.0f);
-        if (a.vec_out) {
-            if (lane * J < E)
-                __builtin_memcpy(__builtin_assume_aligned(out + lane * J, sizeof(res) < 16 ? sizeof(res) : 16), res, sizeof(res));
+        if (t >= a.T) {
+            // past the end: nothing to store
+        } else if (a.vec_out) {
+            if (l * J < E)
+                __builtin_memcpy(__builtin_assume_aligned(out + l * J, sizeof(res) < 16 ? sizeof(res) : 16), res, sizeof(res));
         } else {
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                if (lane * J + j < E)
-                    out[lane * J + j] = res[j];
+                if (l * J + j < E)
+                    out[l * J + j] = res[j];
         }
         row = next;
     }
@@ -605,38 +639,36 @@ hipError_t go(void (*fn)(P), dim3 grid, dim3 block, const P &a, hipStream_t stre
     return launch_kernel(reinterpret_cast<const void *>(fn), grid, block, 0, stream, a);
 }
 
-// fn<J, T> for the experts per lane and the logits' type.
-template <typename F>
+// L lanes hold a token, J = 2^n experts each.
+template <int L_, int J_>
+struct Form {
+    static constexpr int L = L_, J = J_;
+};
+
+// f for the form and the logits' type; a form each for up to 64, 128, 256 and
+// 512 experts.
+template <typename F64, typename F128, typename F256, typename F512, typename F>
 hipError_t with_types(int E, int type, F f)
 {
-    const int J = (E + 63) / 64;
-    auto by_type = [&](auto j) {
-        return type == QG_F32   ? f(j, float{})
-               : type == QG_F16 ? f(j, Fp16{})
-                                : f(j, Bf16{});
+    static_assert(F64::L * F64::J == 64 && F128::L * F128::J == 128 && F256::L * F256::J == 256 &&
+                      F512::L * F512::J == 512,
+                  "");
+    auto by_type = [&](auto form) {
+        return type == QG_F32   ? f(form, float{})
+               : type == QG_F16 ? f(form, Fp16{})
+                                : f(form, Bf16{});
     };
-    if (J <= 1)
-        return by_type(std::integral_constant<int, 1>{});
-    if (J <= 2)
-        return by_type(std::integral_constant<int, 2>{});
-    if (J <= 4)
-        return by_type(std::integral_constant<int, 4>{});
-    return by_type(std::integral_constant<int, 8>{});
+    return E <= 64 ? by_type(F64{}) : E <= 128 ? by_type(F128{}) : E <= 256 ? by_type(F256{}) : by_type(F512{});
 }
 
-inline int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
-
-}  // namespace
-
-namespace {
-
-// Whether a lane's elements of every row are one aligned vector.
-bool whole_vectors(const void *p, int64_t ld, int E, int type)
+// Whether a lane's J elements of every row are one aligned vector.
+inline bool whole_vectors(const void *p, int64_t ld, int E, int J, int type)
 {
-    const int J = E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : 8;
     const uintptr_t bytes = (uintptr_t)J * type_bytes(type);
     return E % J == 0 && ld % J == 0 && (reinterpret_cast<uintptr_t>(p) & (std::min<uintptr_t>(bytes, 16) - 1)) == 0;
 }
+
+inline int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
 }  // namespace
 
@@ -652,10 +684,11 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream)
 {
     Route r{};
     r.a = a;
-    r.a.vec = whole_vectors(a.logits, a.ldl, a.E, a.type);
     if (a.T <= kChunkTokens) {
-        return with_types(a.E, a.type, [&](auto j, auto t) {
-            return go(&route_one_kernel<decltype(j)::value, decltype(t)>, dim3(1), dim3(kThreads), r, stream);
+        return with_types<Form<32, 2>, Form<32, 4>, Form<32, 8>, Form<32, 16>>(a.E, a.type, [&](auto form, auto t) {
+            using O = decltype(form);
+            r.a.vec = whole_vectors(a.logits, a.ldl, a.E, O::J, a.type);
+            return go(&route_one_kernel<O::L, O::J, decltype(t)>, dim3(1), dim3(kThreads), r, stream);
         });
     }
     const int64_t E = a.E;
@@ -668,8 +701,10 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream)
     r.chunk_counts = reinterpret_cast<int32_t *>(w);
     w += round16((int64_t)r.chunks * (E + 2) * 4);
     r.chunk_sums = reinterpret_cast<float *>(w);
-    hipError_t e = with_types(a.E, a.type, [&](auto j, auto t) {
-        return go(&route_tokens_kernel<decltype(j)::value, decltype(t)>, dim3(r.chunks), dim3(kThreads), r, stream);
+    hipError_t e = with_types<Form<16, 4>, Form<16, 8>, Form<16, 16>, Form<32, 16>>(a.E, a.type, [&](auto form, auto t) {
+        using O = decltype(form);
+        r.a.vec = whole_vectors(a.logits, a.ldl, a.E, O::J, a.type);
+        return go(&route_tokens_kernel<O::L, O::J, decltype(t)>, dim3(r.chunks), dim3(kThreads), r, stream);
     });
     if (e == hipSuccess)
         e = go(&route_experts_kernel, dim3((a.E + 2 + 3) / 4), dim3(256), r, stream);
@@ -681,11 +716,12 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream)
 hipError_t launch_route_backward(const RouteGradArgs &args, int cus, hipStream_t stream)
 {
     RouteGradArgs a = args;
-    a.vec = whole_vectors(a.logits, a.ldl, a.E, a.type);
-    a.vec_out = whole_vectors(a.dlogits, a.E, a.E, a.type);
-    const unsigned wgs = (unsigned)std::min<int64_t>(ceil_div(a.T, 4), 8LL * cus);
-    return with_types(a.E, a.type, [&](auto j, auto t) {
-        return go(&route_backward_kernel<decltype(j)::value, decltype(t)>, dim3(wgs), dim3(256), a, stream);
+    return with_types<Form<32, 2>, Form<32, 4>, Form<64, 4>, Form<64, 8>>(a.E, a.type, [&](auto form, auto t) {
+        using O = decltype(form);
+        a.vec = whole_vectors(a.logits, a.ldl, a.E, O::J, a.type);
+        a.vec_out = whole_vectors(a.dlogits, a.E, a.E, O::J, a.type);
+        const unsigned wgs = (unsigned)std::min<int64_t>(ceil_div(a.T, 256 / O::L), 8LL * cus);
+        return go(&route_backward_kernel<O::L, O::J, decltype(t)>, dim3(wgs), dim3(256), a, stream);
     });
 }
 
