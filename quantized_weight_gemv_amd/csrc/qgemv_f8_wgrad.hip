@@ -100,9 +100,11 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
     }
     const int n0 = (tile % p.tiles_n) * BN, k0 = (tile / p.tiles_n) * BK;
 
-    // Rows are numbered from r0 on, 0 .. count - 1.  Rows past the end, and
-    // slots that name no row, become zeros: dY's are read from g_zero, X's
-    // codes are masked.  No branch: the loads of a step stay in one sequence,
+    // Rows are numbered from r0 on, 0 .. count - 1.  Rows past the end become
+    // zeros: they lie outside of the buffers that loads are made from.  Rows
+    // of an expert are gathered with whole addresses instead; there dY's are
+    // read from g_zero and X's codes masked, past the end as well as where a
+    // slot names no row.  No branch: the loads of a step stay in one sequence,
     // which the waits below count.
     const int count = (int)(r1 - r0);
     const uint8_t *const dY = reinterpret_cast<const uint8_t *>(p.dY);
@@ -129,6 +131,27 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
         x_at[i] = p.xq + (GROUPED ? 0 : r0 + x_r[i]) * x_bytes + 128LL * blk + (col & 127);
         s_at[i] = p.xq + p.x_scales + (GROUPED ? 0 : r0 + x_r[i]) * (int64_t)p.x_ls + blk;
     }
+    // dense: the rows m .. m + 31 of `row_bytes` each from `base` (row r0) as a
+    // buffer, and this thread's places in it; what it never reads lies beyond
+    auto step_rows = [&](const uint8_t *base, int64_t row_bytes, int m) {
+        const int left = __builtin_amdgcn_readfirstlane(min(max(count - m, 0), kStep));
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base + (left ? m : 0) * row_bytes), (short)0,
+                                                 (int)(left * row_bytes), kRsrcWord3);
+    };
+    const uint8_t *const y_base = dY + r0 * y_bytes, *const x_base = p.xq + r0 * x_bytes,
+                         *const s_base = p.xq + p.x_scales + r0 * (int64_t)p.x_ls;
+    uint32_t y_off[NY], x_off[NX], s_off[NX];
+    if constexpr (!GROUPED) {
+#pragma unroll
+        for (int i = 0; i < NY; ++i)
+            y_off[i] = y_n[i] < p.N ? (uint32_t)(y_r[i] * y_bytes) + 2u * y_n[i] : 0x7FFFFF00u;
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int col = k0 + 16 * ((threadIdx.x + kThreads * i) % XC), blk = min(col >> 7, p.cb - 1);
+            x_off[i] = (uint32_t)(x_r[i] * x_bytes) + 128u * blk + (col & 127);
+            s_off[i] = (uint32_t)(x_r[i] * p.x_ls) + blk;
+        }
+    }
     int y_slot[NY], x_slot[NX];   // grouped: slots of the step whose loads come next
     auto load_y_slots = [&](int m) {
         if constexpr (GROUPED) {
@@ -154,9 +177,10 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
         return y_at[i] + m * y_bytes;
     };
     // dY straight into LDS: thread -> (row, 16-byte position)
-    auto copy_y = [&](uint4 *Y, int m) {
-#pragma unroll
-        for (int i = 0; i < NY; ++i) {
+    auto copy_y = [&](uint4 *Y, int m, int i) {
+        if constexpr (!GROUPED) {
+            copy16(step_rows(y_base, y_bytes, m), &Y[kThreads * i + 64 * wave], y_off[i], 0);
+        } else {
             bool ok;
             const uint8_t *at = y_from(i, m, ok);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)pick(ok, at, zero),
@@ -202,6 +226,16 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
         uint32_t sbyte[NX], keep[NX];
     };
     auto load_x = [&](Codes &c, int m) {
+        if constexpr (!GROUPED) {
+            const auto from = step_rows(x_base, x_bytes, m), scales = step_rows(s_base, p.x_ls, m);
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                c.code[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(from, x_off[i], 0, 0));
+                c.sbyte[i] = __builtin_amdgcn_raw_buffer_load_b8(scales, s_off[i], 0, 0);
+                c.keep[i] = ~0u;
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
             bool ok = m + x_r[i] < count;
@@ -215,19 +249,16 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
             c.keep[i] = ok ? ~0u : 0u;
         }
     };
-    auto store_x = [&](Codes &c, uint4 *X) {
-#pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const int at = x_r[i] * XC * 2 + 2 * seg_at(x_r[i], (threadIdx.x + kThreads * i) % XC);
-            // what was loaded two steps ago is first touched here: without the
-            // pin its users move up behind the load and wait for it there
-            asm volatile("" : "+v"(c.sbyte[i]), "+v"(c.code[i].x), "+v"(c.code[i].y), "+v"(c.code[i].z),
-                         "+v"(c.code[i].w));
-            const uint32_t k = c.keep[i];   // a masked row's byte is any byte: not the scale of its zeros
-            const float s = f8_exponent(c.sbyte[i] & k);
-            X[at] = __builtin_bit_cast(uint4, f8_widen(c.code[i].x & k, c.code[i].y & k, s));
-            X[at + 1] = __builtin_bit_cast(uint4, f8_widen(c.code[i].z & k, c.code[i].w & k, s));
-        }
+    auto store_x = [&](Codes &c, uint4 *X, int i) {
+        const int at = x_r[i] * XC * 2 + 2 * seg_at(x_r[i], (threadIdx.x + kThreads * i) % XC);
+        // what was loaded two steps ago is first touched here: without the
+        // pin its users move up behind the load and wait for it there
+        asm volatile("" : "+v"(c.sbyte[i]), "+v"(c.code[i].x), "+v"(c.code[i].y), "+v"(c.code[i].z),
+                     "+v"(c.code[i].w));
+        const uint32_t k = c.keep[i];   // a masked row's byte is any byte: not the scale of its zeros
+        const float s = f8_exponent(c.sbyte[i] & k);
+        X[at] = __builtin_bit_cast(uint4, f8_widen(c.code[i].x & k, c.code[i].y & k, s));
+        X[at + 1] = __builtin_bit_cast(uint4, f8_widen(c.code[i].z & k, c.code[i].w & k, s));
     };
     // eight consecutive rows 16 h + 8 (lane / 32) .. of column 32 t + lane % 32
     auto operand = [&](const uint4 *S, int row_bytes, int h, int t) -> bf8_t {
@@ -247,13 +278,13 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
     struct Operands {
         bf8_t x[TM], y[TN];
     };
-    auto read = [&](Operands &o, const uint4 *X, const uint4 *Y, int h) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-            o.x[i] = operand(X, XC * 32, h, wk * TM + i);
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            o.y[j] = operand(Y, YC * 16, h, wn * TN + j);
+    // the o-th operand of a half, dY's first: every product of the next half's
+    // first row takes them all
+    auto read = [&](Operands &to, const uint4 *X, const uint4 *Y, int h, int o) {
+        if (o < TN)
+            to.y[o] = operand(Y, YC * 16, h, wn * TN + o);
+        else
+            to.x[o - TN] = operand(X, XC * 32, h, wk * TM + o - TN);
     };
 
     f16v_t acc[TM][TN];
@@ -264,12 +295,21 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 acc[i][j][e] = 0.0f;
-    auto multiply = [&](const Operands &o) {
+    // The products of half a step, a row of them at a time, with the reads of
+    // the next half's operands and a share of the other work in front of each:
+    // left to itself the compiler gathers the reads at the end and waits there
+    auto half = [&](const Operands &now, Operands &next, const uint4 *X, const uint4 *Y, int h, auto work) {
+        static_assert(TM == TN && NY == TM && NX <= TM, "");
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i) {
+            read(next, X, Y, h, 2 * i);
+            read(next, X, Y, h, 2 * i + 1);
+            work(i);
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.x[i], o.y[j], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now.x[i], now.y[j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
 
     if (r0 < r1) {
@@ -280,15 +320,19 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
         auto fill = [&](int q) {   // before the loop: buffer q
             load_y_slots(q * kStep);
             load_x_slots(q * kStep);
-            if constexpr (ALIGNED)
-                copy_y(ybuf(q), q * kStep);
-            else
+            if constexpr (!ALIGNED)
                 load_y(q * kStep);
             Codes c;
             load_x(c, q * kStep);
             if constexpr (!ALIGNED)
                 store_y(ybuf(q));
-            store_x(c, xbuf(q));
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                if constexpr (ALIGNED)
+                    copy_y(ybuf(q), q * kStep, i);
+                if (i < NX)
+                    store_x(c, xbuf(q), i);
+            }
         };
         fill(0);
         fill(1);
@@ -310,50 +354,33 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
         Operands first, second;
         wait_vm_lds<0>();
         bare_barrier();
-        read(first, X0, Y0, 0);
+#pragma unroll
+        for (int o = 0; o < TM + TN; ++o)
+            read(first, X0, Y0, 0, o);
         auto step = [&](int m, auto number) {
             constexpr int q = decltype(number)::value;
             wait_vm_lds<kOps>();   // and this wave's LDS writes are done
             bare_barrier();
             // buffer (q + 3) % 4 was last read in the step before
-            if constexpr (ALIGNED) {
-                copy_y(ybuf((q + 3) & 3), m + 3 * kStep);
-                load_y_slots(m + 4 * kStep);
-            } else {
-                store_y(ybuf((q + 3) & 3));
-                load_y(m + 4 * kStep);
-                load_y_slots(m + 5 * kStep);
-            }
-            store_x(q & 1 ? c1 : c0, xbuf((q + 3) & 3));
-            // one half's products hide the other half's reads; the copies and
-            // the writes go with the first half, the loads with the second
-            constexpr int kProducts = TM * TN, kReads = 2 * (TM + TN);
-            constexpr int kReadsPer = (kReads + kProducts - 1) / kProducts;
-            read(second, xbuf(q), ybuf(q), 1);
-            multiply(first);
-#pragma unroll
-            for (int i = 0; i < kProducts; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
-                if (i * kReadsPer < kReads)
-                    __builtin_amdgcn_sched_group_barrier(0x100, kReadsPer, 0);   // LDS reads
-                if (ALIGNED && i < NY)
-                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // a copy
-                if (i >= kProducts / 2 && i < kProducts / 2 + 2 * NX)
-                    __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);   // an LDS write
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            load_x(q & 1 ? c1 : c0, m + 5 * kStep);
-            load_x_slots(m + 6 * kStep);
-            read(first, xbuf((q + 1) & 3), ybuf((q + 1) & 3), 0);
-            multiply(second);
-#pragma unroll
-            for (int i = 0; i < kProducts; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                if (i * kReadsPer < kReads)
-                    __builtin_amdgcn_sched_group_barrier(0x100, kReadsPer, 0);
-                if (i < 2 * NX)
-                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // a load
-            }
+            half(first, second, xbuf(q), ybuf(q), 1, [&](int i) {
+                if constexpr (ALIGNED) {
+                    copy_y(ybuf((q + 3) & 3), m + 3 * kStep, i);
+                    if (i == TM - 1)
+                        load_y_slots(m + 4 * kStep);
+                } else if (i == 0) {
+                    store_y(ybuf((q + 3) & 3));
+                    load_y(m + 4 * kStep);
+                    load_y_slots(m + 5 * kStep);
+                }
+                if (i >= TM - NX)
+                    store_x(q & 1 ? c1 : c0, xbuf((q + 3) & 3), i - (TM - NX));
+            });
+            half(second, first, xbuf((q + 1) & 3), ybuf((q + 1) & 3), 0, [&](int i) {
+                if (i == 0) {
+                    load_x(q & 1 ? c1 : c0, m + 5 * kStep);
+                    load_x_slots(m + 6 * kStep);
+                }
+            });
         };
         // whole rounds of four steps: rows past the end are zeros
         for (int m = 0; m < count; m += 4 * kStep) {
