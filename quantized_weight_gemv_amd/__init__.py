@@ -1,5 +1,7 @@
 """Python binding of libqgemv.so (gfx950): fused dequantize-and-multiply of
-block-quantized weights (Q4_0, Q8_0 and plain 2-bit q2w).
+block-quantized weights (Q4_0, Q8_0, plain 2-bit q2w and 8-bit floating f8),
+8-bit activation checkpoints with the products of the backward pass, and
+expert routing.
 
 This module only marshals arguments: it checks tensor devices, dtypes, shapes
 and sizes (the C ABI cannot see buffer sizes), passes raw pointers and the
@@ -7,7 +9,7 @@ current HIP stream, and turns a non-zero status into an exception.  Every step
 of the computation runs in the library's HIP kernels; there is no fallback.
 If the library is missing the import of any entry point fails loudly.
 
-Names follow the C ABI in include/qgemv.h.
+Names follow the C ABI in include/qgemv.h and include/qgemv_f8.h.
 """
 from __future__ import annotations
 

@@ -2,7 +2,10 @@
 // packed weights to fp32 / fp16 and to the packed transposed matrix.
 //
 // All of them are bound by memory: each input byte is read once, each output
-// byte written once, sixteen values (one 16-byte word of codes) per lane.
+// byte written once, sixteen values (one 16-byte word of codes) per lane, which
+// is one store of the codes and two or four loads.  8192 x 4096 in bf16: 17 us
+// to quantize, 17 back, 101 MB each, 5.9 TB/s (a copy of a gigabyte runs at
+// 5.2; part of the data is still in the last-level cache).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -27,6 +27,10 @@
 // the largest of a few neighbouring products.
 // W is the first operand, so a lane holds four consecutive n of a row of Y;
 // the sums are turned through LDS for stores of whole lines.
+// Bound by the matrix cores on large products: 8192 x 14336 x 4096 in bf16
+// 390 to 415 us, 2.3 to 2.5 PFLOP/s (the instruction alone, on registers,
+// 4.2; the clock drops under it); 2048 x 8192 x 4096 54 us, 2.55 PFLOP/s.  With
+// fp32 outputs 108 us, 1.27 PFLOP/s (the bf16 instruction alone 2.4).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -433,6 +437,18 @@ hipError_t launch(GemmParams &p, hipStream_t stream)
                          dim3((unsigned)(ceil_div(items, kXcds) * kXcds)), dim3(T::NT), 0, stream, p);
 }
 
+// Tiles.  Large ones need fewer bytes from the caches, small ones fill the card.
+// Measured (us, K 4096, bf16 out; 256 x 256 / 128 x 128 with two blocks in
+// flight, two workgroups a unit / with four, one a unit / 64 x 128 with four):
+//   2048 x 8192   54 / 66 / 69 / 92     256 tiles of 256 x 256
+//   1024 x 8192   45 / 36 / 35 / 45     512 of 128 x 128
+//   1024 x 4096   43 / 26 / 20 / 23     256 of 128 x 128
+//   512 x 4096    42 / 23 / 16 / 13     128 of 128 x 128
+// and fp32 out: 110 / 118 / 144 / 228, 94 / 64 / 75 / 116, 93 / 45 / 41 / 59,
+// 92 / 41 / 36 / 29.
+// Experts: 128 x 128.  64 of 2048 x 2048 with 24006 slots: 191 us, with 256 x
+// 256 181, 128 x 256 184, 64 x 128 248; the large tiles lose on experts with
+// fewer slots (16 each: they read the same W and multiply four times the rows).
 template <typename OUT, bool GROUPED>
 hipError_t choose(GemmParams &p, int cus, hipStream_t stream)
 {

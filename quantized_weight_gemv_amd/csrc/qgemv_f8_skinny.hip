@@ -2,10 +2,17 @@
 // tokens each.  y[m][n] = sum_k X[m][k] W[n][k].
 //
 // Bound by the bytes of W, each read once: a workgroup of eight waves owns 16
-// R rows of W, its waves take the column blocks of 128 in turn (so the
+// rows of W, its waves take the column blocks of 128 in turn (so the
 // workgroup reads 16 KiB of consecutive memory a round) and add their sums
 // through LDS at the end: no atomics, no second launch, and 16 rows a
 // workgroup fill the card from 4096 rows up.
+// One and eight tokens (us): 4096 x 4096 6.2 and 7.7 in a row of launches (a
+// launch and the latency of the first loads; 16.8 MB), 28672 x 4096 20.7 and
+// 22 (5.3 to 5.7 TB/s, a copy's rate), 4096 x 14336 12.5 and 19.5 (every
+// workgroup quantizes the tokens: 4.7 and 3.0 TB/s).  With four waves 6.8 and
+// 9.3, 20.4 and 24, 14.8 and 24.9; with one block in flight instead of two
+// 6.7 and 7.8, 20.8 and 23.2, 13.1 and 19.9; with 2, 3 or 4 workgroups a unit
+// the same within 2 % (up to 6 % once).
 // A tile of W is in operand order in memory: a wave's lane l loads 16 codes of
 // row l % 16 with each of two loads of a whole kilobyte, nothing goes through
 // LDS.  The codes are widened to bf16 with their scale (exact: four
@@ -44,14 +51,11 @@ struct SkinnyParams {
     bool vec;             // rows of Y take whole vectors of four
 };
 
-// One column block of this wave's operands: W's R row tiles, packed X's G
-// token groups (GX = 0: X is read from LDS when it is multiplied).
-template <int R, int GX>
+// One column block of this wave's operands (X's only where it is packed, else
+// it is read from LDS when it is multiplied).
 struct Block {
-    uint4 w[R][2];
-    uint32_t ws[R];
-    uint4 x[GX ? GX : 1][2];
-    uint32_t xs[GX ? GX : 1];
+    uint4 w[2], x[2];
+    uint32_t ws, xs;
 };
 
 template <typename T>
@@ -72,17 +76,15 @@ __device__ __forceinline__ void store4(void *Y, int64_t at, const f4_t &v, int l
     }
 }
 
-// SRC: Packed, or the type of x; R row tiles of W and G token groups a
-// workgroup; NW waves share K; U column blocks in flight (and U more while
-// those are multiplied).
-template <typename SRC, int R, int G, int NW, int U, bool GROUPED>
-__global__ __launch_bounds__(64 * NW, R * G <= 1 ? 4 : 2) void skinny_kernel(SkinnyParams p)
+// SRC: Packed, or the type of x; NW waves share K; U column blocks in flight
+// (and U more while those are multiplied).
+template <typename SRC, int NW, int U, bool GROUPED>
+__global__ __launch_bounds__(64 * NW, 4) void skinny_kernel(SkinnyParams p)
 {
     constexpr bool kPacked = sizeof(SRC) == 1;
-    constexpr int GX = kPacked ? G : 0;
     extern __shared__ uint4 lds[];
-    f4_t *part = reinterpret_cast<f4_t *>(lds);                      // [2][wave][R][G][64]
-    uint4 *codes = lds + 2 * NW * R * G * 64;                        // [cb][2][32], quantizing
+    f4_t *part = reinterpret_cast<f4_t *>(lds);                      // [2][wave][64]
+    uint4 *codes = lds + 2 * NW * 64;                               // [cb][2][32], quantizing
     uint8_t *scales = reinterpret_cast<uint8_t *>(codes + p.cb * 64);   // [cb][8]
 
     const int lane = threadIdx.x & 63;
@@ -96,148 +98,110 @@ __global__ __launch_bounds__(64 * NW, R * G <= 1 ? 4 : 2) void skinny_kernel(Ski
     if (item >= total)
         return;
     F8Unit u{0, 0, p.rows.rows, 0, 1, 0, 0};
-    int64_t y_row[G], x_row[G];   // this lane's rows of Y (-1: none) and of X
+    int64_t y_row, x_row;   // this lane's rows of Y (-1: none) and of X
     const uint8_t *W = p.W;
     auto begin_unit = [&](int64_t unit) {
         if constexpr (GROUPED) {
-            u = f8_unit(p.rows.offsets, p.rows.P, p.rows.rows, 16 * G, unit);
+            u = f8_unit(p.rows.offsets, p.rows.P, p.rows.rows, 16, unit);
             if (u.r0 >= u.r1)
                 return;
             W = p.W + min(u.e, p.rows.P - 1) * p.rows.stride;
         }
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int64_t at = u.r0 + 16 * g + r16;
-            y_row[g] = at < u.r1 ? at : -1;
-            x_row[g] = min(at, u.r1 - 1);
-            if constexpr (GROUPED) {
-                const int64_t s = p.rows.order[x_row[g]];
-                const bool ok = s >= 0 && s < p.rows.rows;
-                y_row[g] = at < u.r1 && ok ? s : -1;
-                x_row[g] = ok ? min((int64_t)((uint32_t)s / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1) : 0;
-            }
+        const int64_t at = u.r0 + r16;
+        y_row = at < u.r1 ? at : -1;
+        x_row = min(at, u.r1 - 1);
+        if constexpr (GROUPED) {
+            const int64_t s = p.rows.order[x_row];
+            const bool ok = s >= 0 && s < p.rows.rows;
+            y_row = at < u.r1 && ok ? s : -1;
+            x_row = ok ? min((int64_t)((uint32_t)s / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1) : 0;
         }
     };
     begin_unit(GROUPED ? item / p.row_groups : 0);
     if (GROUPED && u.r0 >= u.r1)
         return;   // past the last unit (uniform over the workgroup)
 
-    using B = Block<R, GX>;
-    auto load_w = [&](B(&b)[U], int rg, int j0) {
-        const int t0 = rg * R;
-        const auto rw = make_rsrc(W + (int64_t)t0 * p.cb * 2048, (int64_t)min(R, p.rt - t0) * p.cb * 2048);
+    auto load_w = [&](Block(&b)[U], int rg, int j0) {
+        const auto rw = make_rsrc(W + (int64_t)rg * p.cb * 2048, (int64_t)p.cb * 2048);
 #pragma unroll
         for (int q = 0; q < U; ++q) {
-            const int cb = wave + NW * max(0, min(j0 + q, mine - 1));   // past the wave's last: that one again, unused
+            // past the wave's last block: that one again, unused; a wave
+            // without blocks reads outside the descriptor
+            const int cb = wave + NW * max(0, min(j0 + q, mine - 1));
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                // a row tile past the matrix lies outside the descriptor: zeros
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    b[q].w[i][h] = stream_load16(rw, (uint32_t)((i * p.cb + cb) * 2048 + 1024 * h + 16 * lane));
-                b[q].ws[i] = W[p.w_scales + (int64_t)(min(t0 + i, p.rt - 1) >> 3) * p.ls + min(cb, p.cb - 1)];
-            }
+            for (int h = 0; h < 2; ++h)
+                b[q].w[h] = stream_load16(rw, (uint32_t)(cb * 2048 + 1024 * h + 16 * lane));
+            b[q].ws = W[p.w_scales + (int64_t)(rg >> 3) * p.ls + min(cb, p.cb - 1)];
         }
     };
-    auto load_x = [&](B(&b)[U], int j0) {
+    auto load_x = [&](Block(&b)[U], int j0) {
         if constexpr (kPacked) {
 #pragma unroll
             for (int q = 0; q < U; ++q) {
                 const int cb = min(wave + NW * max(0, min(j0 + q, mine - 1)), p.cb - 1);
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint8_t *x = p.xq + (x_row[g] * p.cb + cb) * 128 + 16 * c;
-                    b[q].x[g][0] = *reinterpret_cast<const uint4 *>(x);
-                    b[q].x[g][1] = *reinterpret_cast<const uint4 *>(x + 64);
-                    b[q].xs[g] = p.xq[p.x_scales + x_row[g] * p.ls + cb];
-                }
+                const uint8_t *x = p.xq + (x_row * p.cb + cb) * 128 + 16 * c;
+                b[q].x[0] = *reinterpret_cast<const uint4 *>(x);
+                b[q].x[1] = *reinterpret_cast<const uint4 *>(x + 64);
+                b[q].xs = p.xq[p.x_scales + x_row * p.ls + cb];
             }
         }
     };
 
-    f4_t acc[R][G];
-    auto clear = [&] {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                acc[i][g] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    };
-    auto multiply = [&](const B(&b)[U], int j0) {
+    f4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](const Block(&b)[U], int j0) {
 #pragma unroll
         for (int q = 0; q < U; ++q) {
             if (j0 + q >= mine)
                 break;   // uniform over the wave
             const int cb = wave + NW * (j0 + q);
-            uint4 xv[G][2];
-            float xs[G];
+            uint4 xv[2];
+            uint32_t xb;
+            if constexpr (kPacked) {
+                xv[0] = b[q].x[0], xv[1] = b[q].x[1];
+                xb = b[q].xs;
+            } else {
+                // tokens from M on hold what is in LDS: their sums are never stored
+                xv[0] = codes[cb * 64 + c * 8 + (r16 & 7)];
+                xv[1] = codes[cb * 64 + 32 + c * 8 + (r16 & 7)];
+                xb = scales[cb * 8 + (r16 & 7)];
+            }
+            const float ws = f8_exponent(b[q].ws), xs = f8_exponent(xb);
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                if constexpr (kPacked) {
-                    xv[g][0] = b[q].x[g][0], xv[g][1] = b[q].x[g][1];
-                    xs[g] = f8_exponent(b[q].xs[g]);
-                } else {
-                    // tokens from M on hold what is in LDS: their sums are never stored
-                    xv[g][0] = codes[cb * 64 + c * 8 + (r16 & 7)];
-                    xv[g][1] = codes[cb * 64 + 32 + c * 8 + (r16 & 7)];
-                    xs[g] = f8_exponent(scales[cb * 8 + (r16 & 7)]);
-                }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    bf8_t w[R], x[G];
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-                        w[i] = o ? f8_widen(b[q].w[i][h].z, b[q].w[i][h].w, f8_exponent(b[q].ws[i]))
-                                 : f8_widen(b[q].w[i][h].x, b[q].w[i][h].y, f8_exponent(b[q].ws[i]));
-#pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        x[g] = o ? f8_widen(xv[g][h].z, xv[g][h].w, xs[g]) : f8_widen(xv[g][h].x, xv[g][h].y, xs[g]);
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-#pragma unroll
-                        for (int g = 0; g < G; ++g)
-                            acc[i][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x[g], acc[i][g], 0, 0, 0);
-                }
+            for (int h = 0; h < 2; ++h) {
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen(b[q].w[h].x, b[q].w[h].y, ws),
+                                                              f8_widen(xv[h].x, xv[h].y, xs), acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen(b[q].w[h].z, b[q].w[h].w, ws),
+                                                              f8_widen(xv[h].z, xv[h].w, xs), acc, 0, 0, 0);
+            }
         }
     };
     // D of a 16 x 16 product: lane (c, r) holds rows 4 c .. 4 c + 3 (of W) of
-    // column r (token r).  The R G 64 vectors of four are summed over the
-    // waves through LDS, pair (i, g) by wave (i G + g) % NW.  Two buffers in
-    // turn: one barrier an item.
+    // column r (token r).  The first wave adds the waves' vectors of four from
+    // LDS.  Two buffers in turn: one barrier an item.
     int turn = 0;
     auto finish = [&](int rg) {
-        f4_t *buf = part + turn * NW * R * G * 64;
+        f4_t *buf = part + turn * NW * 64;
         turn ^= 1;
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                buf[((wave * R + i) * G + g) * 64 + lane] = acc[i][g];
+        buf[wave * 64 + lane] = acc;
         wait_lds();
         bare_barrier();   // the next row group's loads stay in flight
+        if (wave == 0) {
+            f4_t v = buf[lane];
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if ((i * G + g) % NW == wave) {
-                    f4_t v = buf[(i * G + g) * 64 + lane];
-#pragma unroll
-                    for (int w = 1; w < NW; ++w)
-                        v += buf[((w * R + i) * G + g) * 64 + lane];
-                    const int n = (rg * R + i) * 16 + 4 * c;
-                    if (y_row[g] >= 0 && n < p.N) {
-                        const int64_t at = y_row[g] * p.N + n;
-                        if (p.y_type == QG_F32)
-                            store4<float>(p.Y, at, v, p.N - n, p.vec);
-                        else if (p.y_type == QG_F16)
-                            store4<Fp16>(p.Y, at, v, p.N - n, p.vec);
-                        else
-                            store4<Bf16>(p.Y, at, v, p.N - n, p.vec);
-                    }
-                }
-        clear();
+            for (int w = 1; w < NW; ++w)
+                v += buf[w * 64 + lane];
+            const int n = rg * 16 + 4 * c;
+            if (y_row >= 0 && n < p.N) {
+                const int64_t at = y_row * p.N + n;
+                if (p.y_type == QG_F32)
+                    store4<float>(p.Y, at, v, p.N - n, p.vec);
+                else if (p.y_type == QG_F16)
+                    store4<Fp16>(p.Y, at, v, p.N - n, p.vec);
+                else
+                    store4<Bf16>(p.Y, at, v, p.N - n, p.vec);
+            }
+        }
+        acc = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
     };
 
     // The batches of `items` row groups from rg on, gridDim.x apart, as one
@@ -245,10 +209,10 @@ __global__ __launch_bounds__(64 * NW, R * G <= 1 ? 4 : 2) void skinny_kernel(Ski
     // across row groups as well.  b0 holds the first batch.  The loads of a
     // pair of batches stand on one path without branches, so that a wait for
     // a batch leaves the next one's loads in flight.
-    B b0[U], b1[U];
+    Block b0[U], b1[U];
     auto run = [&](int rg, int items) {
         int t = 0;
-        auto turn = [&](B(&cur)[U], B(&nxt)[U], bool more) {
+        auto turn = [&](Block(&cur)[U], Block(&nxt)[U], bool more) {
             const bool last = t + 1 == batches;
             const int nt = last ? 0 : t + 1, nrg = last ? rg + (int)gridDim.x : rg;
             if (more) {   // known where it is called
@@ -273,7 +237,6 @@ __global__ __launch_bounds__(64 * NW, R * G <= 1 ? 4 : 2) void skinny_kernel(Ski
             turn(b0, b1, false);
         }
     };
-    clear();
     if constexpr (GROUPED) {
         // one item after the other: its expert and its tokens have to be found
         for (;;) {
@@ -352,14 +315,18 @@ __global__ __launch_bounds__(64 * NW, R * G <= 1 ? 4 : 2) void skinny_kernel(Ski
     }
 }
 
-// 17 to 64 tokens of one matrix (G groups of 16): the same streaming of W, with
+// 17 to 64 tokens of one matrix (G groups of 16; where N is large the tiled
+// kernels take over): the same streaming of W, with
 // X's blocks copied into LDS a block ahead (buffer loads that write LDS), by
 // each wave for itself.  An operand read straight from memory takes 16 rows x
 // 64 bytes, and the caches deliver 9.5 TB/s to such loads against 30 to the 8
 // rows x 128 bytes of a copy; X, read by every workgroup, is most of what is
 // read here.  Rows are 128 bytes, 16-byte chunk c of row r at position
 // c ^ ((r / 2) % 8): the 16 rows of a quarter of an operand read touch all 64
-// banks.
+// banks.  Every unit needs all of X: 64 x 4096 x 14336 takes 28 us, of which
+// W alone is 14, the copies of X 11 (235 MB at 20 TB/s) and the products,
+// behind them, 3; 17 tokens take 15, 32 19.  Four waves with four buffers each
+// take as long (29, 15, 19).
 template <int G>
 __global__ __launch_bounds__(512, 2) void skinny_lds_kernel(SkinnyParams p)
 {
@@ -507,13 +474,13 @@ hipError_t launch_lds(SkinnyParams &p, int cus, hipStream_t stream)
                          dim3((unsigned)std::min(p.rt, cus * (G == 2 ? 2 : 1))), dim3(512), 0, stream, p);
 }
 
-template <typename SRC, int R, int G, int NW, int U, bool GROUPED>
+template <typename SRC, int NW, int U, bool GROUPED>
 hipError_t launch(SkinnyParams &p, int cus, hipStream_t stream)
 {
-    p.row_groups = (p.rt + R - 1) / R;
-    p.units = GROUPED ? f8_units(p.rows.rows, p.rows.P, 16 * G) : 1;
-    const size_t lds = (size_t)2 * NW * R * G * 1024 + (sizeof(SRC) == 1 ? 0 : (size_t)p.cb * (1024 + 8));
-    const void *fn = reinterpret_cast<const void *>(&skinny_kernel<SRC, R, G, NW, U, GROUPED>);
+    p.row_groups = p.rt;
+    p.units = GROUPED ? f8_units(p.rows.rows, p.rows.P, 16) : 1;
+    const size_t lds = (size_t)2 * NW * 1024 + (sizeof(SRC) == 1 ? 0 : (size_t)p.cb * (1024 + 8));
+    const void *fn = reinterpret_cast<const void *>(&skinny_kernel<SRC, NW, U, GROUPED>);
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess)
@@ -533,13 +500,13 @@ hipError_t launch_f8_skinny(const uint8_t *W, const uint8_t *xq, const void *x, 
     const F8Acts a = f8_acts(r.x_rows, K);
     SkinnyParams p{W, xq, x, Y, r, f.scales, a.scales, 1, (int)N, (int)K, f.cb, f.ls, a.ls, f.rt, 0, y_type, N % 4 == 0 && (reinterpret_cast<uintptr_t>(Y) & (4 * type_bytes(y_type) - 1)) == 0};
     if (x)
-        return x_type == QG_F32   ? launch<float, 1, 1, 8, 2, false>(p, cus, stream)
-               : x_type == QG_F16 ? launch<Fp16, 1, 1, 8, 2, false>(p, cus, stream)
-                                  : launch<Bf16, 1, 1, 8, 2, false>(p, cus, stream);
+        return x_type == QG_F32   ? launch<float, 8, 2, false>(p, cus, stream)
+               : x_type == QG_F16 ? launch<Fp16, 8, 2, false>(p, cus, stream)
+                                  : launch<Bf16, 8, 2, false>(p, cus, stream);
     if (r.order)
-        return launch<Packed, 1, 1, 4, 1, true>(p, cus, stream);
+        return launch<Packed, 4, 1, true>(p, cus, stream);
     if (r.rows <= 16)
-        return launch<Packed, 1, 1, 8, 2, false>(p, cus, stream);
+        return launch<Packed, 8, 2, false>(p, cus, stream);
     if (r.rows <= 32)
         return launch_lds<2>(p, cus, stream);
     return launch_lds<4>(p, cus, stream);

@@ -22,6 +22,12 @@
 // Tiles beyond whole rounds of the card's compute units are split along the
 // rows among the units that would be idle; their parts go to the workspace
 // and a second kernel adds them in a fixed order (no atomics).
+// 8192 x 4096 x 4096, one round of tiles: 224 us, 1.23 PFLOP/s (a library
+// product of bf16 operands 1.4, the instruction alone 2.4).  With nothing
+// loaded it takes 153, without the widening as well 131, with the products
+// alone 127: what is left is the wait for operands, which are copied two steps
+// before they are read (four buffers of 32 KB are what LDS holds).
+// 8192 x 6144 x 4096: 381 us and 18 for the second kernel.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
