@@ -437,15 +437,19 @@ hipError_t launch(GemmParams &p, hipStream_t stream)
                          dim3((unsigned)(ceil_div(items, kXcds) * kXcds)), dim3(T::NT), 0, stream, p);
 }
 
-// Tiles.  Large ones need fewer bytes from the caches, small ones fill the card.
-// Measured (us, K 4096, bf16 out; 256 x 256 / 128 x 128 with two blocks in
-// flight, two workgroups a unit / with four, one a unit / 64 x 128 with four):
-//   2048 x 8192   54 / 66 / 69 / 92     256 tiles of 256 x 256
-//   1024 x 8192   45 / 36 / 35 / 45     512 of 128 x 128
-//   1024 x 4096   43 / 26 / 20 / 23     256 of 128 x 128
-//   512 x 4096    42 / 23 / 16 / 13     128 of 128 x 128
-// and fp32 out: 110 / 118 / 144 / 228, 94 / 64 / 75 / 116, 93 / 45 / 41 / 59,
-// 92 / 41 / 36 / 29.
+// Tiles.  Large ones need fewer bytes from the caches, small ones fill the card;
+// with few tiles it is rounds of them over the compute units that count.  Time
+// of a round at K 4096 (us, bf16 out, fp32 about twice that everywhere):
+//   256 x 256, two blocks in flight, one a unit        47
+//   128 x 128, two blocks, two a unit                  34, or 24 if half is empty
+//   128 x 128, four blocks, one a unit                 18.5
+//   64 x 128, four blocks, one a unit                  12.5
+// The shape whose rounds add up to the least is taken (below: twice these, in
+// whole numbers).  Measured (us, in that
+// order): 2048 x 8192 54 / 66 / 69 / 92; 1536 x 6144 45 / 55 / 52 / 57; 2304 x
+// 8192 92 / 86 / 89 / 104; 1024 x 6144 44 / 31 / 35 / 35; 1024 x 4096 43 / 26 /
+// 20 / 23; 640 x 4096 42 / 25 / 18 / 23; 512 x 4096 42 / 23 / 16 / 13; fp32:
+// 2304 x 8192 193 / 146 / 177 / 256, 640 x 4096 94 / 43 / 39 / 57.
 // Experts: 128 x 128.  64 of 2048 x 2048 with 24006 slots: 191 us, with 256 x
 // 256 181, 128 x 256 184, 64 x 128 248; the large tiles lose on experts with
 // fewer slots (16 each: they read the same W and multiply four times the rows).
@@ -454,11 +458,16 @@ hipError_t choose(GemmParams &p, int cus, hipStream_t stream)
 {
     if constexpr (!GROUPED) {
         auto tiles = [&](int bm, int bn) { return ceil_div(p.rows.rows, bm) * ceil_div(p.N, bn); };
-        if (tiles(256, 256) >= cus)
-            return launch<4, 4, 2, OUT, GROUPED>(p, stream);
-        if (tiles(128, 128) >= 2 * cus)
+        const int64_t middle = tiles(128, 128), last = middle % (2 * cus);
+        const int64_t t256 = ceil_div(tiles(256, 256), cus) * 94,
+                      t128 = middle / (2 * cus) * 68 + (last == 0 ? 0 : last <= cus ? 48 : 68),
+                      t128d = ceil_div(middle, cus) * 37, t64 = ceil_div(tiles(64, 128), cus) * 25;
+        const int64_t least = std::min(std::min(t256, t128), std::min(t128d, t64));
+        if (least == t128)
             return launch<2, 2, 2, OUT, GROUPED>(p, stream);
-        if (tiles(128, 128) >= cus)
+        if (least == t256)
+            return launch<4, 4, 2, OUT, GROUPED>(p, stream);
+        if (least == t128d)
             return launch<2, 2, 4, OUT, GROUPED>(p, stream);
         return launch<1, 2, 4, OUT, GROUPED>(p, stream);
     } else {
