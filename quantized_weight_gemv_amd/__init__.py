@@ -403,15 +403,20 @@ class _Call:
     """One call's device: every tensor has to be on it, and the call is made
     with it as the current device, on its current stream."""
 
-    __slots__ = ("device", "torch")
+    __slots__ = ("device", "index", "torch")
 
     def __init__(self, first, name: str):
         self.torch = torch = _torch()
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError(f"{name} must be a device tensor")
         self.device = first.device
+        self.index = first.get_device()
 
     def ptr(self, t, dtype, name: str, numel: int):
+        # one pass over what has to hold; the reasons are looked up only for a refusal
+        if isinstance(t, self.torch.Tensor) and t.get_device() == self.index and t.dtype is dtype and \
+                t.numel() >= numel and t.is_contiguous():
+            return t.data_ptr()
         if not isinstance(t, self.torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a device tensor")
         if t.device != self.device:
@@ -420,9 +425,7 @@ class _Call:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.numel() < numel:
-            raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
-        return t.data_ptr()
+        raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
 
     def opt(self, t, dtype, name: str, numel: int):
         return None if t is None else self.ptr(t, dtype, name, numel)
@@ -441,7 +444,7 @@ class _Call:
 
     def __call__(self, fn: str, *args):
         f = getattr(lib(), fn)
-        index = self.device.index
+        index = self.index
         # the stream's handle as it is: torch.cuda.current_stream() makes an
         # object around it first (2.7 us of the 9.7 that a small call took)
         stream = self.torch._C._cuda_getCurrentRawStream(index)
