@@ -342,3 +342,67 @@ def test_far_outputs():
         assert torch.equal(y[at:at + 300], part), at
     del y
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------- every choice of tiles
+@pytest.mark.parametrize("M,N,K", [(1500, 1490, 300), (2210, 2100, 129), (3600, 3399, 257), (40, 8210, 200), (20, 12400, 384),
+                                   (50, 20700, 130), (64, 300, 5000), (31, 4100, 1100)])
+@pytest.mark.parametrize("dtype", fu.TYPES)
+def test_gemm_shapes_of_tiles(M, N, K, dtype):
+    """Sizes on both sides of each choice: 64 x 128, 128 x 128 (both depths), 256 x 256, streaming; ragged edges."""
+    q, torch = qg(), torch_cuda()
+    W, xq = to_dev(q.qquantize_f8(fu.weights(N, K, seed=31))), q.qact_quantize_f8(to_dev(fu.acts(M, K, seed=32)))
+    wv, xv = q.qdequant_f8(W, N, K).double(), q.qact_dequant_f8(xq, M, K).double()
+    ref, size = (xv @ wv.t().contiguous()).cpu().numpy(), (xv.abs() @ wv.abs().t().contiguous()).cpu().numpy()
+    kind = getattr(torch, dtype)
+    buf = torch.full((M * N + 8,), 5.0, dtype=kind, device="cuda")
+    y = q.qgemm_f8(W, xq, M, N, K, Y=buf[:M * N].view(M, N))
+    fu.assert_close(_np(y), ref, fu.product_bound(ref, size, K, dtype), f"{M}x{N}x{K} {dtype}")
+    assert (buf[M * N:] == 5.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(70, 3601, 3500), (600, 3608, 3399), (2200, 3592, 3585), (33, 2055, 2050)])
+def test_wgrad_large_tiles(M, N, K):
+    q, torch = qg(), torch_cuda()
+    xq = q.qact_quantize_f8(to_dev(fu.acts(M, K, seed=34)))
+    dy = to_dev(fu.acts(M, N, seed=35)).to(torch.bfloat16)
+    xv, dv = q.qact_dequant_f8(xq, M, K).double(), dy.double()
+    ref, size = (dv.t().contiguous() @ xv).cpu().numpy(), (dv.abs().t().contiguous() @ xv.abs()).cpu().numpy()
+    b = fu.sum_bound(size, M)
+    dw = q.qgemm_f8_wgrad(dy, xq, M, N, K)
+    fu.assert_close(_np(dw), ref, b, "dW")
+    q.qgemm_f8_wgrad(dy, xq, M, N, K, dW=dw, accumulate=True)
+    fu.assert_close(_np(dw), 2 * ref, 2 * b + 2.0 ** -23 * (2 * np.abs(ref) + b), "on top of itself")
+
+
+@pytest.mark.parametrize("P,T,N,K", [(3, 400, 2055, 2050), (40, 700, 520, 1030)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_experts_with_uneven_slots(P, T, N, K, dtype):
+    """One expert with most of the slots, some with none: products and weight gradients of wide matrices."""
+    q, torch = qg(), torch_cuda()
+    pool = to_dev(_pool(P, N, K, seed=41))
+    g = np.random.default_rng(T)
+    flat = np.where(g.random(T) < 0.6, 1, g.integers(0, P, T))
+    flat[flat == 0] = -1
+    key = np.where(flat >= 0, flat, P)
+    order = np.argsort(key, kind="stable").astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(np.bincount(key, minlength=P + 1)[:P])]).astype(np.int32)
+    xq = q.qact_quantize_f8(to_dev(fu.acts(T, K, seed=42)))
+    xv = q.qact_dequant_f8(xq, T, K).double()
+    dy = to_dev(fu.acts(T, N, seed=43)).to(torch.bfloat16)
+    y = q.qmoe_gemm_f8(pool, P, xq, T, to_dev(order), to_dev(off), N, K, dtype=getattr(torch, dtype))
+    dw = q.qmoe_gemm_f8_wgrad(dy, xq, T, to_dev(order), to_dev(off), P, N, K)
+    yv, nb = _np(y), q.qpacked_bytes_f8(N, K)
+    for e in range(P):
+        at = np.flatnonzero(flat == e)
+        if len(at) == 0:
+            assert (dw[e] == 0).all()
+            continue
+        rows = xv[torch.from_numpy(at).cuda()]
+        wv = q.qdequant_f8(pool[e * nb:(e + 1) * nb], N, K).double()
+        ref, size = (rows @ wv.t().contiguous()).cpu().numpy(), (rows.abs() @ wv.abs().t().contiguous()).cpu().numpy()
+        fu.assert_close(yv[at], ref, fu.product_bound(ref, size, K, dtype), f"expert {e}")
+        d = dy[torch.from_numpy(at).cuda()].double()
+        ref, size = (d.t().contiguous() @ rows).cpu().numpy(), (d.abs().t().contiguous() @ rows.abs()).cpu().numpy()
+        fu.assert_close(_np(dw[e]), ref, fu.sum_bound(size, len(at)), f"gradient of expert {e}")
+    assert (yv[flat < 0] == 0).all()

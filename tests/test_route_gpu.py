@@ -186,3 +186,10 @@ def test_route_checks():
             call()
     with pytest.raises(TypeError):
         q.qmoe_route(x.double(), 2)
+
+
+@pytest.mark.parametrize("dtype", fu.TYPES)
+@pytest.mark.parametrize("T,E,k", [(70, 200, 8), (33, 512, 16), (100, 257, 5), (2100, 64, 6)])
+def test_route_gradient_of_many_experts(T, E, k, dtype):
+    for renorm in (True, False):
+        test_route_gradient(T, E, k, renorm, dtype)
