@@ -256,6 +256,21 @@ __device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t from, uint4 *to, u
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, at, off, 0, 0);
 }
 
+// Sums of v over the lanes up to this one, the whole wave active, with
+// data-parallel-primitive moves: one to eight lanes on inside rows of 16, then
+// the rows' and the halves' totals (a step of a shuffle through LDS takes over
+// a hundred cycles).
+__device__ __forceinline__ int prefix_sum(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // lane 15 of a row into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // lane 31 into rows 2 and 3
+    return v;
+}
+
 // Where a group's rows are: rows r0 .. r1 - 1 of `order` (or of Y and X, dense),
 // at most `tile` of them, of expert e; e = P: slots without an expert.
 struct F8Unit {
@@ -291,12 +306,7 @@ __device__ __forceinline__ F8Unit f8_unit_of(const int32_t *offsets, int P, int6
         const int end = e < P ? max(at[j], min(max(at[j + 1], 0), n)) : n;
         mine += j < per && e <= P ? (end - at[j] + tile - 1) / tile : 0;
     }
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(incl, d);
-        incl += lane >= d ? o : 0;
-    }
+    const int incl = prefix_sum(mine);
     const unsigned long long holds = __ballot((int64_t)incl > unit);
     if (holds == 0)
         return F8Unit{P, 0, 0, 0, 1, 0, 0};

@@ -356,12 +356,7 @@ __device__ __forceinline__ void bases(const int32_t *counts, int E, int32_t *bas
             const int e = lane * per + j;
             mine += e <= E ? counts[e] : 0;
         }
-        int incl = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(incl, d);
-            incl += lane >= d ? o : 0;
-        }
+        const int incl = prefix_sum(mine);
         int at = incl - mine;
         for (int j = 0; j < per; ++j) {
             const int e = lane * per + j;
@@ -481,12 +476,9 @@ __global__ __launch_bounds__(256) void route_experts_kernel(Route r)
 #pragma unroll
         for (int q = 0; q < kAt; ++q) {
             const int c = c0 + 64 * q + lane;
-            int incl = v[q];
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const int o = __shfl_up(incl, d);
-                incl += lane >= d ? o : 0;
-            }
+            if (c0 + 64 * q >= r.chunks)
+                break;
+            const int incl = prefix_sum(v[q]);
             if (c < r.chunks)
                 r.chunk_counts[(int64_t)c * (E + 2) + e] = before + incl - v[q];
             sum += (double)f[q];
