@@ -9,7 +9,8 @@
 // 64): 16384 tokens of 256 experts, 8 each: 23 + 15 / 24 + 15 / 28 + 11; of
 // 512, 10 each: 46 + 31 / 34 + 25 / 37 + 21; of 64, 6 each: 16 + 5 / 18 + 5 /
 // 21 + 6; 4 tokens of 128, 10 each (one workgroup): 7 / 6 / 6 forward; 64
-// tokens: 9 / 11 / 15.  So many tokens take L = 16, with 512 experts 32, the
+// tokens: 9 / 11 / 15 (all forms of the forward pass are 1 to 2 us faster
+// since, by what they share).  So many tokens take L = 16, with 512 experts 32, the
 // one workgroup of a decode step 32, the backward pass, which has no rounds
 // and many values in registers, 32 and from 256 experts on 64.
 // The forward pass reads each logit once.  Beyond one workgroup's tokens it is
@@ -19,8 +20,8 @@
 //      counts and its sums of p per expert;
 //   2. experts: the counts of the chunks before each chunk, the totals;
 //   3. slots: offsets from the totals, every slot to its place, the loss.
-// 16384 x 256: 14, 6 and 5 us (the launches' own latencies in the last two),
-// the backward pass 11; 8.4 MB of logits, read twice, and their gradient would
+// 16384 x 256: 13, 4 and 5 us (the launches' own latencies in the last two),
+// the backward pass 12; 8.4 MB of logits, read twice, and their gradient would
 // take 5 us at the copy rate.  Up to kChunkTokens tokens one workgroup does all
 // of it in one launch.
 // All sums run in a fixed order (a lane's tokens, the wave's, the waves, the
@@ -146,13 +147,14 @@ __device__ __forceinline__ float exp_of(float x)
 template <int L, int J>
 __device__ __forceinline__ bool softmax(const float (&x)[J], float (&p)[J], float &top, float &inv)
 {
-    uint32_t best = 0;
+    top = x[0];   // the maximum passes over NaNs by itself
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-        best = max(best, key_of(x[j]));
-    best = max_of<L>(best);
-    const bool live = best != 0;
-    top = value_of(best);
+    for (int j = 1; j < J; ++j)
+        top = fmaxf(top, x[j]);
+    top = __uint_as_float(reduce<L>(__float_as_uint(top), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+    const bool live = top > -__builtin_inff();
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
