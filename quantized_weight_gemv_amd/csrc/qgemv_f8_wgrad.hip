@@ -121,7 +121,8 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
     };
     // this thread's chunks: row inside a step, column
     int y_r[NY], y_n[NY], x_r[NX];
-    const uint8_t *y_at[NY], *x_at[NX], *s_at[NX];   // dense: row r0 + r; grouped: row 0
+    const uint8_t *y_at[NY];                // dense: row r0 + r; grouped: row 0
+    const uint8_t *x_at[NX], *s_at[NX];     // grouped: row 0
 #pragma unroll
     for (int i = 0; i < NY; ++i) {
         const int idx = threadIdx.x + kThreads * i, pos = idx % YC;
@@ -134,8 +135,8 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
         const int idx = threadIdx.x + kThreads * i;
         x_r[i] = idx / XC;
         const int col = k0 + 16 * (idx % XC), blk = min(col >> 7, p.cb - 1);
-        x_at[i] = p.xq + (GROUPED ? 0 : r0 + x_r[i]) * x_bytes + 128LL * blk + (col & 127);
-        s_at[i] = p.xq + p.x_scales + (GROUPED ? 0 : r0 + x_r[i]) * (int64_t)p.x_ls + blk;
+        x_at[i] = p.xq + 128 * blk + (col & 127);
+        s_at[i] = p.xq + p.x_scales + blk;
     }
     // dense: the rows m .. m + 31 of `row_bytes` each from `base` (row r0) as a
     // buffer, and this thread's places in it; what it never reads lies beyond
@@ -240,19 +241,16 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
                 c.sbyte[i] = __builtin_amdgcn_raw_buffer_load_b8(scales, s_off[i], 0, 0);
                 c.keep[i] = ~0u;
             }
-            return;
-        }
+        } else {
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            bool ok = m + x_r[i] < count;
-            int64_t row = m;
-            if constexpr (GROUPED) {
-                ok &= is_slot(x_slot[i]);
-                row = min((int64_t)((uint32_t)(ok ? x_slot[i] : 0) / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1);
+            for (int i = 0; i < NX; ++i) {
+                const bool ok = (m + x_r[i] < count) & is_slot(x_slot[i]);
+                const int64_t row =
+                    min((int64_t)((uint32_t)(ok ? x_slot[i] : 0) / (uint32_t)p.rows.k_slots), p.rows.x_rows - 1);
+                c.code[i] = *reinterpret_cast<const uint4 *>(pick(ok, x_at[i] + row * x_bytes, p.xq));
+                c.sbyte[i] = *pick(ok, s_at[i] + row * p.x_ls, p.xq);
+                c.keep[i] = ok ? ~0u : 0u;
             }
-            c.code[i] = *reinterpret_cast<const uint4 *>(pick(ok, x_at[i] + row * x_bytes, p.xq));
-            c.sbyte[i] = *pick(ok, s_at[i] + row * p.x_ls, p.xq);
-            c.keep[i] = ok ? ~0u : 0u;
         }
     };
     auto store_x = [&](Codes &c, uint4 *X, int i) {
