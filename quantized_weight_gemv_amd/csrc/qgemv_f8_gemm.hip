@@ -450,9 +450,14 @@ hipError_t launch(GemmParams &p, hipStream_t stream)
 // 8192 92 / 86 / 89 / 104; 1024 x 6144 44 / 31 / 35 / 35; 1024 x 4096 43 / 26 /
 // 20 / 23; 640 x 4096 42 / 25 / 18 / 23; 512 x 4096 42 / 23 / 16 / 13; fp32:
 // 2304 x 8192 193 / 146 / 177 / 256, 640 x 4096 94 / 43 / 39 / 57.
-// Experts: 128 x 128.  64 of 2048 x 2048 with 24006 slots: 191 us, with 256 x
-// 256 181, 128 x 256 184, 64 x 128 248; the large tiles lose on experts with
-// fewer slots (16 each: they read the same W and multiply four times the rows).
+// Experts: 128 x 128, and 256 x 256 where they have 1024 slots each on average
+// (fp32 out: 2048).  128 x 128 / 256 x 256, uneven experts (us), bf16 out: 64
+// of 2048 x 2048 with 256 slots each 143 / 157, 512 233 / 221, 1024 420 / 373,
+// 2048 811 / 671; 128 of 640 x 2560: 512 194 / 210, 1024 342 / 341, 2048 732 /
+// 623; 16 of 4096 x 4096: 512 203 / 206, 1024 377 / 329, 2048 718 / 552; fp32:
+// 1024 698 / 686, 542 / 630, 623 / 670, 2048 1317 / 1199, 1090 / 1138, 1196 /
+// 1085.  (64 of 2048 x 2048 with 375 each: 128 x 256 184, 64 x 128 248 beside
+// 188 / 181.)
 template <typename OUT, bool GROUPED>
 hipError_t choose(GemmParams &p, int cus, hipStream_t stream)
 {
@@ -471,6 +476,8 @@ hipError_t choose(GemmParams &p, int cus, hipStream_t stream)
             return launch<2, 2, 4, OUT, GROUPED>(p, stream);
         return launch<1, 2, 4, OUT, GROUPED>(p, stream);
     } else {
+        if (p.rows.rows >= (sizeof(OUT) == 4 ? 2048LL : 1024LL) * p.rows.P)
+            return launch<4, 4, 2, OUT, GROUPED>(p, stream);
         return launch<2, 2, 2, OUT, GROUPED>(p, stream);
     }
 }

@@ -375,8 +375,8 @@ def test_wgrad_large_tiles(M, N, K):
     fu.assert_close(_np(dw), 2 * ref, 2 * b + 2.0 ** -23 * (2 * np.abs(ref) + b), "on top of itself")
 
 
-@pytest.mark.parametrize("P,T,N,K", [(3, 400, 2055, 2050), (40, 700, 520, 1030)])
-@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("P,T,N,K", [(3, 400, 2055, 2050), (40, 700, 520, 1030), (2, 4300, 300, 260)])
+@pytest.mark.parametrize("dtype", fu.TYPES)
 def test_experts_with_uneven_slots(P, T, N, K, dtype):
     """One expert with most of the slots, some with none: products and weight gradients of wide matrices."""
     q, torch = qg(), torch_cuda()
