@@ -14,11 +14,12 @@
 //     at a time; an operand read is 256 consecutive bytes a quarter wave.
 // X has D buffers (blocks), W 2 D (steps).  During step t the matrix cores
 // multiply operands that were read from LDS during step t - 1, the operands of
-// t + 1 are read, W's copies of step t + 2 D - 1 are issued and, in a block's
-// second step, X's copies of the block D further on, both into buffers whose
-// last reads fed products of step t - 1.  One barrier a step; before it a wave
-// waits for those of its own copies that step t reads.  K takes whole rounds
-// of D blocks; blocks past it are read as zeros.
+// t + 1 are read, W's copies of step t + 2 D - 1 are issued into the buffer
+// that step t - 2 read and, in a block's second step, X's copies of the block D
+// further on into the one that step t - 1 read last.  One barrier a step;
+// before it a wave waits for those of its own copies that step t reads and for
+// its LDS reads, so that behind it every buffer's readers are done.  K takes
+// whole rounds of D blocks; blocks past it are read as zeros.
 // 16-bit outputs: v_mfma_scale_f32_32x32x64_f8f6f4 with the two block scales
 // as its scale operands, so the fp32 sums need no further instruction.  fp32
 // outputs: the codes are widened to bf16 with their scale (exact) and
@@ -358,7 +359,7 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
     // step q of a round of D blocks, the first of which is b
     auto step = [&](int b, auto number) {
         constexpr int q = decltype(number)::value;
-        wait_vm<q & 1 ? kOdd : kEven>();
+        wait_vm_lds<q & 1 ? kOdd : kEven>();   // the reads of step t - 1 as well: an odd step copies over them
         bare_barrier();
         if constexpr (q == 0) {
             // the scales of a round are loaded a round ahead
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
             step(b, std::integral_constant<int, 7>{});
         }
     }
-    wait_vm<0>();   // no copy is in flight when X0 is used for staging
+    wait_vm_lds<0>();   // no copy and no read is in flight when X0 is used for staging
     bare_barrier();
     write();
 }
