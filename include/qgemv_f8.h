@@ -33,15 +33,10 @@
  *
  * Element types of inputs and outputs: QG_F32, QG_F16, QG_BF16.
  *
- * Accuracy of the products.  With fp32 outputs both sides are widened to
- * bf16, exactly, and multiplied with fp32 sums, whose roundings are all that
- * is lost: at most (K / 8 + 16) 2^-24 sum |w x|, about 1e-7 of the result on
- * ordinary data.  16-bit outputs are rounded once from fp32 sums; beyond 16
- * rows, or 8 slots an expert on average, those sums may come from the 8-bit
- * matrix instructions, which align the products of a few neighbouring k to
- * their largest and keep about 13 bits below it (measured: 1.3e-5 relative to
- * the result on normal data, at most 1.7e-4 sum |w x|): within 1e-3 sum |w x|
- * before the rounding.
+ * Accuracy of the products.  Both sides are widened to bf16, exactly, and
+ * multiplied with fp32 sums, whose roundings are all that is lost: at most
+ * (K / 8 + 16) 2^-24 sum |w x|, about 1e-7 of the result on ordinary data.
+ * 16-bit outputs are rounded once from these sums.
  * Results are bitwise reproducible: no atomics.
  */
 #ifndef QGEMV_F8_H

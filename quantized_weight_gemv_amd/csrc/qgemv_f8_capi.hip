@@ -49,22 +49,17 @@ qg_status check_route(const void *logits, int type, int64_t ldl, int64_t T, int6
 
 // Few rows: the streaming kernels, bound by W's way to every compute unit, or
 // the tiled ones, whose time is one tile's as long as tiles are few.  Measured
-// (us, streaming / tiled; K 4096), M 64, bf16 out: N 4096 11 / 15, 8192 20 /
-// 15, 28672 63 / 20; fp32: 12288 29 / 30, 16384 38 / 42, 22016 54 / 42.
-// M 32, bf16: N 8192 12.6 / 13.4, 12288 17 / 12; fp32: 22016 30 / 42.
-bool few_rows(int64_t M, int64_t N, int y_type, int cus)
+// (us, streaming / tiled, fp32 out; K 4096): M 64: N 12288 29 / 30, 16384 38 /
+// 42, 22016 54 / 42; M 32: 22016 30 / 42.
+bool few_rows(int64_t M, int64_t N, int cus)
 {
-    const int64_t tiles = ceil_div(N, 128);
-    if (y_type == QG_F32)
-        return M <= 32 || (M <= 64 && tiles < 5 * cus / 8);
-    return M <= 16 || (M <= 32 && tiles < 3 * cus / 8) || (M <= 64 && tiles < cus / 4);
+    return M <= 32 || (M <= 64 && ceil_div(N, 128) < 5 * cus / 8);
 }
 
 // The same for experts, by their average slots.  Measured (us, streaming /
-// tiled), 64 experts of 2048 x 2048, bf16 out: 8 slots each 57 / 58, 16 82 /
-// 60; fp32: 8 59 / 80, 16 82 / 88, 24 111 / 91.  128 experts of 640 x 2560,
-// bf16: 8 46 / 44; fp32: 8 47 / 60, 16 68 / 61.
-bool few_slots(int64_t slots, int64_t P, int y_type) { return slots <= (y_type == QG_F32 ? 16 : 8) * P; }
+// tiled, fp32 out): 64 experts of 2048 x 2048: 8 slots each 59 / 80, 16 82 / 88,
+// 24 111 / 91; 128 experts of 640 x 2560: 8 47 / 60, 16 68 / 61.
+bool few_slots(int64_t slots, int64_t P) { return slots <= 16 * P; }
 
 }  // namespace
 }  // namespace qg
@@ -148,7 +143,7 @@ qg_status qgemm_f8(const void *Wp, const void *xq, void *Y, int y_type, int64_t 
     const F8Rows r{M, M, nullptr, nullptr, 0, 1, 0};
     const auto *W = static_cast<const uint8_t *>(Wp);
     const auto *X = static_cast<const uint8_t *>(xq);
-    if (few_rows(M, N, y_type, cus))
+    if (few_rows(M, N, cus))
         return status(launch_f8_skinny(W, X, nullptr, 0, Y, y_type, r, N, K, cus, on(stream)));
     return status(launch_f8_gemm(W, X, Y, y_type, r, N, K, cus, on(stream)));
 }
@@ -233,7 +228,7 @@ qg_status qmoe_gemm_f8(const void *pool, int64_t P, const void *xq, int64_t T, i
     const F8Rows r{T * k_slots, T, order, offsets, (int)P, k_slots, f8_weights(N, K).bytes};
     const auto *W = static_cast<const uint8_t *>(pool);
     const auto *X = static_cast<const uint8_t *>(xq);
-    if (few_slots(r.rows, P, y_type))
+    if (few_slots(r.rows, P))
         return status(launch_f8_skinny(W, X, nullptr, 0, Y, y_type, r, N, K, cus, on(stream)));
     return status(launch_f8_gemm(W, X, Y, y_type, r, N, K, cus, on(stream)));
 }

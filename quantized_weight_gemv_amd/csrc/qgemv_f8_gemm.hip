@@ -20,18 +20,16 @@
 // before it a wave waits for those of its own copies that step t reads and for
 // its LDS reads, so that behind it every buffer's readers are done.  K takes
 // whole rounds of D blocks; blocks past it are read as zeros.
-// 16-bit outputs: v_mfma_scale_f32_32x32x64_f8f6f4 with the two block scales
-// as its scale operands, so the fp32 sums need no further instruction.  fp32
-// outputs: the codes are widened to bf16 with their scale (exact) and
-// multiplied with v_mfma_f32_32x32x16_bf16: half the rate, but products and
-// sums exact to fp32, where the 8-bit instructions keep about 13 bits below
-// the largest of a few neighbouring products.
+// The codes are widened to bf16 with their scale (exact) and multiplied with
+// v_mfma_f32_32x32x16_bf16, whatever the type of the outputs: products are
+// exact and sums are fp32 sums.  The 8-bit instruction with the block scales as
+// operands runs twice as fast, but it aligns neighbouring products to the
+// largest of them and keeps about 13 bits below it: where products of 2^16
+// cancel, it loses up to a tenth of the sum of 200 others of 1 to 6.
 // W is the first operand, so a lane holds four consecutive n of a row of Y;
 // the sums are turned through LDS for stores of whole lines.
-// Bound by the matrix cores on large products: 8192 x 14336 x 4096 in bf16
-// 390 to 415 us, 2.3 to 2.5 PFLOP/s (the instruction alone, on registers,
-// 4.2; the clock drops under it); 2048 x 8192 x 4096 54 us, 2.55 PFLOP/s.  With
-// fp32 outputs 108 us, 1.27 PFLOP/s (the bf16 instruction alone 2.4).
+// Bound by the matrix cores and by waits for copies: 2048 x 8192 x 4096 108 us,
+// 1.27 PFLOP/s (the instruction alone, on registers, 2.4).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -99,7 +97,6 @@ template <int TM, int TN, int D, typename OUT, bool GROUPED>
 __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_kernel(GemmParams p)
 {
     using T = Tile<TM, TN>;
-    constexpr bool kWide = sizeof(OUT) == 4;
     // one variable a buffer: the compiler then knows which copies an operand
     // read has to wait for (none: the waits are the kernel's own)
     static_assert(D == 2 || D == 4, "");
@@ -107,7 +104,7 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
     __shared__ uint4 X0[kX], X1[kX], X2[D > 2 ? kX : 1], X3[D > 2 ? kX : 1];
     __shared__ uint4 W0[kW], W1[kW], W2[kW], W3[kW];
     __shared__ uint4 W4[D > 2 ? kW : 1], W5[D > 2 ? kW : 1], W6[D > 2 ? kW : 1], W7[D > 2 ? kW : 1];
-    constexpr int JN = kWide ? TN / 2 : TN;   // column tiles that are staged at a time
+    constexpr int JN = sizeof(OUT) == 4 ? TN / 2 : TN;   // column tiles that are staged at a time
     constexpr bool kOwnStage = 4 * 32 * 32 * JN * (int)sizeof(OUT) > T::BM * 128;
     __shared__ uint4 stages[kOwnStage ? 4 * 2 * 32 * JN * (int)sizeof(OUT) : 1];
     __shared__ int out_row[GROUPED ? T::BM : 1];
@@ -212,7 +209,7 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
                     const int at = (32 * j + 8 * g + 4 * half) * (int)sizeof(OUT);
                     char *to = bytes + r32 * kRow + (((at >> 4) ^ (r32 & (kChunks - 1))) << 4) + (at & 15);
                     const f16v_t &a = acc[i][j0 + j];
-                    if constexpr (kWide)
+                    if constexpr (sizeof(OUT) == 4)
                         *reinterpret_cast<f4_t *>(to) = f4_t{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
                     else
                         *reinterpret_cast<uint2 *>(to) =
@@ -254,7 +251,7 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
 #pragma unroll
                 for (int e = 0; e < kPer; ++e)
                     if (n + e < p.N) {
-                        if constexpr (kWide)
+                        if constexpr (sizeof(OUT) == 4)
                             to[e] = __uint_as_float(w[e]);
                         else
                             to[e] = OUT{(uint16_t)(w[e / 2] >> (16 * (e & 1)))};
@@ -315,39 +312,25 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
         }
     };
     auto multiply = [&](const Operands &o) {
-        if constexpr (!kWide) {
+        const float wf = f8_exponent(ws & 255u);
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    const i8_t a = {(int)o.w[j][0].x, (int)o.w[j][0].y, (int)o.w[j][0].z, (int)o.w[j][0].w,
-                                    (int)o.w[j][1].x, (int)o.w[j][1].y, (int)o.w[j][1].z, (int)o.w[j][1].w};
-                    const i8_t b = {(int)o.x[i][0].x, (int)o.x[i][0].y, (int)o.x[i][0].z, (int)o.x[i][0].w,
-                                    (int)o.x[i][1].x, (int)o.x[i][1].y, (int)o.x[i][1].z, (int)o.x[i][1].w};
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc[i][j], 0, 0, 0, (int)ws, 0,
-                                                                               (int)xs[i]);
-                }
-        } else {
-            const float wf = f8_exponent(ws & 255u);
+            for (int h = 0; h < 2; ++h) {
+                bf8_t w[TN];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+                for (int j = 0; j < TN; ++j)
+                    w[j] = h ? f8_widen(o.w[j][q].z, o.w[j][q].w, wf) : f8_widen(o.w[j][q].x, o.w[j][q].y, wf);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    bf8_t w[TN];
+                for (int i = 0; i < TM; ++i) {
+                    const float xf = f8_exponent(xs[i] & 255u);
+                    const bf8_t x =
+                        h ? f8_widen(o.x[i][q].z, o.x[i][q].w, xf) : f8_widen(o.x[i][q].x, o.x[i][q].y, xf);
 #pragma unroll
                     for (int j = 0; j < TN; ++j)
-                        w[j] = h ? f8_widen(o.w[j][q].z, o.w[j][q].w, wf) : f8_widen(o.w[j][q].x, o.w[j][q].y, wf);
-#pragma unroll
-                    for (int i = 0; i < TM; ++i) {
-                        const float xf = f8_exponent(xs[i] & 255u);
-                        const bf8_t x =
-                            h ? f8_widen(o.x[i][q].z, o.x[i][q].w, xf) : f8_widen(o.x[i][q].x, o.x[i][q].y, xf);
-#pragma unroll
-                        for (int j = 0; j < TN; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x, acc[i][j], 0, 0, 0);
-                    }
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x, acc[i][j], 0, 0, 0);
                 }
-        }
+            }
     };
 
     // Copies that may be in flight behind what a step waits for: those of the
@@ -381,21 +364,6 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
         copy_w(wbuf((q + 2 * D - 1) % (2 * D)));
         read(q & 1 ? even : odd, xbuf((q + 1) % (2 * D) >> 1), (q + 1) & 1, wbuf((q + 1) % (2 * D)));
         multiply(q & 1 ? odd : even);
-        // reads and copies behind the first products: left alone they gather
-        // at the end of the step
-        if constexpr (!kWide) {
-            constexpr int kProducts = TM * TN, kReads = 2 * (TM + TN), kCopies = T::WC + (q & 1 ? T::XC : 0);
-            constexpr int kCopiesPer = (kCopies + kProducts - 1) / kProducts;
-            constexpr int kReadsPer = (kReads + kProducts - 1) / kProducts > 2 ? (kReads + kProducts - 1) / kProducts : 2;
-#pragma unroll
-            for (int m = 0; m < kProducts; ++m) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
-                if (kReadsPer * m < kReads)
-                    __builtin_amdgcn_sched_group_barrier(0x100, kReadsPer, 0);   // LDS reads
-                if (kCopiesPer * m < kCopies)
-                    __builtin_amdgcn_sched_group_barrier(0x020, kCopiesPer, 0);   // copies
-            }
-        }
     };
     // what the 2 D - 1 steps before the first one would have copied
     load_scales(0);
@@ -440,7 +408,8 @@ hipError_t launch(GemmParams &p, hipStream_t stream)
 
 // Tiles.  Large ones need fewer bytes from the caches, small ones fill the card;
 // with few tiles it is rounds of them over the compute units that count.  Time
-// of a round at K 4096 (us, bf16 out, fp32 about twice that everywhere):
+// of a round at K 4096 (us, of products of 8-bit operands; of the widened ones
+// about twice that everywhere):
 //   256 x 256, two blocks in flight, one a unit        47
 //   128 x 128, two blocks, two a unit                  34, or 24 if half is empty
 //   128 x 128, four blocks, one a unit                 18.5
@@ -477,7 +446,7 @@ hipError_t choose(GemmParams &p, int cus, hipStream_t stream)
             return launch<2, 2, 4, OUT, GROUPED>(p, stream);
         return launch<1, 2, 4, OUT, GROUPED>(p, stream);
     } else {
-        if (p.rows.rows >= (sizeof(OUT) == 4 ? 2048LL : 1024LL) * p.rows.P)
+        if (p.rows.rows >= 2048LL * p.rows.P)
             return launch<4, 4, 2, OUT, GROUPED>(p, stream);
         return launch<2, 2, 2, OUT, GROUPED>(p, stream);
     }

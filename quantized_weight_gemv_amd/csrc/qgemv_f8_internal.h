@@ -65,7 +65,6 @@ typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 typedef float f16v_t __attribute__((ext_vector_type(16)));
-typedef int i8_t __attribute__((ext_vector_type(8)));
 
 // Element types as C++ types, for templates.
 struct Bf16 {
