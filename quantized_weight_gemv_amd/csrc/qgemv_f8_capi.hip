@@ -49,17 +49,24 @@ qg_status check_route(const void *logits, int type, int64_t ldl, int64_t T, int6
 
 // Few rows: the streaming kernels, bound by W's way to every compute unit, or
 // the tiled ones, whose time is one tile's as long as tiles are few.  Measured
-// (us, streaming / tiled, fp32 out; K 4096): M 64: N 12288 29 / 30, 16384 38 /
-// 42, 22016 54 / 42; M 32: 22016 30 / 42.
-bool few_rows(int64_t M, int64_t N, int cus)
+// (us, streaming / tiled, bf16 out; fp32 out the same within a microsecond),
+// K 4096: M 32: N 8192 11 / 20, 12288 16 / 20, 22016 29 / 21, 28672 35 / 23;
+// M 64: 4096 9 / 18, 8192 19 / 20, 12288 28 / 20, 28672 62 / 24.  K 1024: M 32:
+// 12288 5.2 / 7.7, 22016 8.1 / 7.9, 28672 9.6 / 7.9; M 64: 8192 6.8 / 7.5, 12288
+// 8.9 / 7.7.  M 16: 28672 x 4096 28 / 23, the largest difference of up to 16
+// rows.  fp32 outputs of up to 32 rows always stream: their bits are then the
+// same in any split of the rows of W.
+bool few_rows(int64_t M, int64_t N, int y_type, int cus)
 {
-    return M <= 32 || (M <= 64 && ceil_div(N, 128) < 5 * cus / 8);
+    const int64_t tiles = ceil_div(N, 128);
+    return M <= 16 || (M <= 32 && (y_type == QG_F32 || tiles < cus / 2)) || (M <= 64 && tiles < cus / 4);
 }
 
 // The same for experts, by their average slots.  Measured (us, streaming /
-// tiled, fp32 out): 64 experts of 2048 x 2048: 8 slots each 59 / 80, 16 82 / 88,
-// 24 111 / 91; 128 experts of 640 x 2560: 8 47 / 60, 16 68 / 61.
-bool few_slots(int64_t slots, int64_t P) { return slots <= 16 * P; }
+// tiled), 64 experts of 2048 x 2048, bf16 out: 8 slots each 60 / 66, 16 86 /
+// 64, 24 108 / 67; fp32: 58 / 67, 83 / 69, 107 / 70.  128 experts of 640 x 2560,
+// bf16: 8 47 / 49, 16 66 / 50; fp32: 45 / 50, 65 / 51.
+bool few_slots(int64_t slots, int64_t P) { return slots <= 8 * P; }
 
 }  // namespace
 }  // namespace qg
@@ -143,7 +150,7 @@ qg_status qgemm_f8(const void *Wp, const void *xq, void *Y, int y_type, int64_t 
     const F8Rows r{M, M, nullptr, nullptr, 0, 1, 0};
     const auto *W = static_cast<const uint8_t *>(Wp);
     const auto *X = static_cast<const uint8_t *>(xq);
-    if (few_rows(M, N, cus))
+    if (few_rows(M, N, y_type, cus))
         return status(launch_f8_skinny(W, X, nullptr, 0, Y, y_type, r, N, K, cus, on(stream)));
     return status(launch_f8_gemm(W, X, Y, y_type, r, N, K, cus, on(stream)));
 }

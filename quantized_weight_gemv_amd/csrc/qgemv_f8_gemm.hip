@@ -28,8 +28,10 @@
 // cancel, it loses up to a tenth of the sum of 200 others of 1 to 6.
 // W is the first operand, so a lane holds four consecutive n of a row of Y;
 // the sums are turned through LDS for stores of whole lines.
-// Bound by the matrix cores and by waits for copies: 2048 x 8192 x 4096 108 us,
-// 1.27 PFLOP/s (the instruction alone, on registers, 2.4).
+// Bound by the matrix cores on large products: 8192 x 14336 x 4096 takes 671 us
+// with bf16 outputs, 1.43 PFLOP/s, and 720 with fp32 (a library product of bf16
+// operands 1.41 PFLOP/s, the instruction alone, on registers, 2.4; the clock
+// drops under it); 2048 x 8192 x 4096 104 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -81,6 +83,8 @@ __device__ __forceinline__ void dense_tile(uint32_t lin, uint32_t units, int til
     tn = (int)(in / rows);
     unit = band * kBand + (in - (uint32_t)tn * rows);
 }
+
+typedef uint32_t Words __attribute__((ext_vector_type(4)));
 
 // Buffers that loads are made from: base and size of what they may read.
 struct Source {
@@ -146,8 +150,10 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
     const int rt0 = n0 / 16;
     const Source w_src{Wm + (int64_t)rt0 * p.cb * 2048, (uint32_t)(min(T::BN / 16, p.rt - rt0) * p.cb * 2048)};
     static_assert(128 % (32 * TN) == 0, "a wave's rows of W lie in one block");
-    const uint8_t *const ws_src =
-        Wm + p.w_scales + (int64_t)min((n0 + wn * TN * 32) >> 7, (p.N - 1) >> 7) * p.w_ls;
+    const Source ws_src{Wm + p.w_scales + (int64_t)min((n0 + wn * TN * 32) >> 7, (p.N - 1) >> 7) * p.w_ls,
+                        (uint32_t)p.w_ls};
+    uint32_t ws_at = 0;
+    asm("" : "+v"(ws_at));   // a lane's own: a word known to be the wave's would go to a scalar register, behind a wait
     // this thread's places in them
     uint32_t x_at[T::XC], w_at[T::WC], xs_at[TM];
     auto row_at = [&](int r) -> uint32_t {   // grouped: the row of X of a row of the tile; past its end: none
@@ -290,10 +296,12 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
 #pragma unroll
         for (int i = 0; i < TM; ++i)
             xs_next[i] = __builtin_amdgcn_raw_buffer_load_b32(r, xs_at[i], 4 * word, 0);
-        ws_next = *reinterpret_cast<const uint32_t *>(ws_src + 4 * word);
+        ws_next = __builtin_amdgcn_raw_buffer_load_b32(rsrc_of(ws_src), ws_at, 4 * word, 0);
     };
+    // (one load of 16 bytes: taken word by word, the compiler loses track of the
+    // buffer that some of them are from and waits for every copy)
     struct Operands {
-        uint4 x[TM][2], w[TN][2];
+        Words x[TM][2], w[TN][2];
     };
     auto read = [&](Operands &o, const uint4 *X, int h, const uint4 *Wb) {   // h: half of X's block
 #pragma unroll
@@ -302,12 +310,12 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const int r = (wm * TM + i) * 32 + r32;
-                o.x[i][q] = X[r * 8 + ((4 * h + ch) ^ ((r >> 1) & 7))];
+                o.x[i][q] = *reinterpret_cast<const Words *>(&X[r * 8 + ((4 * h + ch) ^ ((r >> 1) & 7))]);
             }
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int t = (wn * TN + j) * 2 + (r32 >> 4);
-                o.w[j][q] = Wb[t * 64 + ch * 16 + (r32 & 15)];
+                o.w[j][q] = *reinterpret_cast<const Words *>(&Wb[t * 64 + ch * 16 + (r32 & 15)]);
             }
         }
     };
@@ -335,7 +343,8 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
 
     // Copies that may be in flight behind what a step waits for: those of the
     // 2 D - 3 steps before it, of which an even step has D - 1 with X's among
-    // them, an odd one D - 2.
+    // them, an odd one D - 2.  (The loads of a round's scales are not counted,
+    // so the second step of a round waits for up to TM + 1 operations more.)
     constexpr int kEven = (2 * D - 3) * T::WC + (D - 1) * T::XC, kOdd = (2 * D - 3) * T::WC + (D - 2) * T::XC;
     constexpr int kFirst = (2 * D - 2) * T::WC + (D - 1) * T::XC;
     Operands even, odd;
@@ -359,11 +368,22 @@ __global__ __launch_bounds__(256, TM *TN *D > 16 || D == 4 ? 1 : 2) void gemm_ke
                 xs[i] = at < p.cb ? xword[i] >> (8 * (at & 3)) : 127u;
             ws = at < p.cb ? wword >> (8 * (at & 3)) : 127u;
         }
+        read(q & 1 ? even : odd, xbuf((q + 1) % (2 * D) >> 1), (q + 1) & 1, wbuf((q + 1) % (2 * D)));
         if constexpr (q & 1)
             copy_x(xbuf(q >> 1));
         copy_w(wbuf((q + 2 * D - 1) % (2 * D)));
-        read(q & 1 ? even : odd, xbuf((q + 1) % (2 * D) >> 1), (q + 1) & 1, wbuf((q + 1) % (2 * D)));
         multiply(q & 1 ? odd : even);
+        // both behind the first products: left alone they gather at the end of
+        // the step
+        constexpr int kProducts = 4 * TM * TN, kReads = 2 * (TM + TN), kCopies = T::WC + (q & 1 ? T::XC : 0);
+#pragma unroll
+        for (int m = 0; m < kProducts; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+            if (m < kReads)
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // an LDS read
+            else if (m < kReads + kCopies)
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // a copy
+        }
     };
     // what the 2 D - 1 steps before the first one would have copied
     load_scales(0);
@@ -408,35 +428,34 @@ hipError_t launch(GemmParams &p, hipStream_t stream)
 
 // Tiles.  Large ones need fewer bytes from the caches, small ones fill the card;
 // with few tiles it is rounds of them over the compute units that count.  Time
-// of a round at K 4096 (us, of products of 8-bit operands; of the widened ones
-// about twice that everywhere):
-//   256 x 256, two blocks in flight, one a unit        47
-//   128 x 128, two blocks, two a unit                  34, or 24 if half is empty
-//   128 x 128, four blocks, one a unit                 18.5
-//   64 x 128, four blocks, one a unit                  12.5
-// The shape whose rounds add up to the least is taken (below: twice these, in
-// whole numbers).  Measured (us, in that
-// order): 2048 x 8192 54 / 66 / 69 / 92; 1536 x 6144 45 / 55 / 52 / 57; 2304 x
-// 8192 92 / 86 / 89 / 104; 1024 x 6144 44 / 31 / 35 / 35; 1024 x 4096 43 / 26 /
-// 20 / 23; 640 x 4096 42 / 25 / 18 / 23; 512 x 4096 42 / 23 / 16 / 13; fp32:
-// 2304 x 8192 193 / 146 / 177 / 256, 640 x 4096 94 / 43 / 39 / 57.
-// Experts: 128 x 128, and 256 x 256 where they have 1024 slots each on average
-// (fp32 out: 2048).  128 x 128 / 256 x 256, uneven experts (us), bf16 out: 64
-// of 2048 x 2048 with 256 slots each 143 / 157, 512 233 / 221, 1024 420 / 373,
-// 2048 811 / 671; 128 of 640 x 2560: 512 194 / 210, 1024 342 / 341, 2048 732 /
-// 623; 16 of 4096 x 4096: 512 203 / 206, 1024 377 / 329, 2048 718 / 552; fp32:
-// 1024 698 / 686, 542 / 630, 623 / 670, 2048 1317 / 1199, 1090 / 1138, 1196 /
-// 1085.  (64 of 2048 x 2048 with 375 each: 128 x 256 184, 64 x 128 248 beside
-// 188 / 181.)
+// of a round at K 4096 (us, any output type):
+//   256 x 256, two blocks in flight, one a unit        103
+//   128 x 128, two blocks, two a unit                  55, or 35 if half is empty
+//   128 x 128, four blocks, one a unit                 30
+//   64 x 128, four blocks, one a unit                  20
+// The shape whose rounds add up to the least is taken.  Measured (us, in that
+// order, bf16 out): 8192 x 14336 671 / 739 / 788 / 1073; 2048 x 8192 104 / 110 /
+// 114 / 154; 1536 x 6144 78 / 78 / 79 / 94; 2304 x 8192 170 / 131 / 134 / 172;
+// 1024 x 6144 76 / 50 / 52 / 60; 1024 x 4096 76 / 35 / 31 / 43; 640 x 4096 78 / 32
+// / 26 / 39; 512 x 4096 75 / 30 / 26 / 23; fp32: 8192 x 14336 720 / 780 / 842 /
+// 1053, 2304 x 8192 184 / 137 / 138 / 172, 640 x 4096 83 / 33 / 27 / 38.  At K 512
+// rounds cost 21, 10 or 8, 7 and 4.5; the rule takes the best there or one up to
+// 8 % slower (8192 x 4096: 41 / 38 / 52 / 67; 1024 x 4096: 16 / 8.2 / 8.7 / 11).
+// Experts: 128 x 128, and 256 x 256 where they have 2048 slots each on average.
+// 128 x 128 / 256 x 256, uneven experts (us), bf16 out: 64 of 2048 x 2048 with
+// 128 slots each 130 / 149, 375 237 / 261, 1024 536 / 538, 2048 1061 / 955; 128
+// of 640 x 2560: 375 191 / 243, 1024 427 / 501, 2048 811 / 886; 16 of 4096 x
+// 4096: 512 280 / 296, 1024 498 / 489, 2048 944 / 869; fp32, 2048 slots: 1127 /
+// 1021, 859 / 936, 1003 / 898.
 template <typename OUT, bool GROUPED>
 hipError_t choose(GemmParams &p, int cus, hipStream_t stream)
 {
     if constexpr (!GROUPED) {
         auto tiles = [&](int bm, int bn) { return ceil_div(p.rows.rows, bm) * ceil_div(p.N, bn); };
         const int64_t middle = tiles(128, 128), last = middle % (2 * cus);
-        const int64_t t256 = ceil_div(tiles(256, 256), cus) * 94,
-                      t128 = middle / (2 * cus) * 68 + (last == 0 ? 0 : last <= cus ? 48 : 68),
-                      t128d = ceil_div(middle, cus) * 37, t64 = ceil_div(tiles(64, 128), cus) * 25;
+        const int64_t t256 = ceil_div(tiles(256, 256), cus) * 103,
+                      t128 = middle / (2 * cus) * 55 + (last == 0 ? 0 : last <= cus ? 35 : 55),
+                      t128d = ceil_div(middle, cus) * 30, t64 = ceil_div(tiles(64, 128), cus) * 20;
         const int64_t least = std::min(std::min(t256, t128), std::min(t128d, t64));
         if (least == t128)
             return launch<2, 2, 2, OUT, GROUPED>(p, stream);

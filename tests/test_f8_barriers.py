@@ -55,6 +55,32 @@ def test_no_lds_read_is_in_flight_at_a_barrier(unit, kernels, tmp_path):
     assert not bad, bad
 
 
+def _waits_in_loops(lines):
+    """{kernel: [vmcnt of each wait in the loop that multiplies]}."""
+    found, kernel, labels = {}, None, {}
+    for n, line in enumerate(lines):
+        name = re.match(r"^(_Z\S+):", line)
+        if name:
+            kernel, labels = name.group(1), {}
+        label = re.match(r"^(\.LBB\S+):", line)
+        if label:
+            labels[label.group(1)] = n
+        back = re.match(r"\s+s_c?branch\S*\s+(\.LBB\S+)", line)
+        if back and back.group(1) in labels:
+            body = lines[labels[back.group(1)]:n]
+            if any("v_mfma" in op for op in body):
+                found[kernel] = [int(w) for op in body for w in re.findall(r"s_waitcnt.*vmcnt\((\d+)\)", op)]
+    return found
+
+
+def test_gemm_loops_keep_their_copies_in_flight(tmp_path):
+    """The loop waits for the copies that a step reads, by count; a wait for all of them would empty the ring."""
+    found = _waits_in_loops(_assembly("qgemv_f8_gemm.hip", tmp_path))
+    assert len(found) >= 12
+    drained = {k: v for k, v in found.items() if 0 in v or not v}
+    assert not drained, drained
+
+
 def test_the_count_sees_a_missing_wait():
     """The counting itself, on a loop with and without the wait."""
     code = ["_Zk:", "ds_read_b128 v[0:3], v9", "s_waitcnt vmcnt(4)", "s_barrier", "s_waitcnt lgkmcnt(0)", "s_endpgm"]
