@@ -10,9 +10,13 @@
  * 0x7f / 0xff are NaN); a scale is a power of two 2^e held as the byte
  * e + 127 (0..254).  A block's scale is the smallest 2^e, e >= -127, with
  * |v| <= 448 * 2^e for every finite v of the block, and 2^0 where all of
- * them are zero; a code is v / 2^e rounded to nearest, ties to even.  A power
- * of two costs a floating code no precision, keeps every value exact in
- * bf16 and is what the matrix cores' block scales are.
+ * them are zero; a code is v / 2^e rounded to nearest, ties to even, and at
+ * most 240 under 2^120, the largest scale (256 would be 2^128), so finite
+ * values stay finite.  A power of two costs a floating code no precision and
+ * keeps values exact in bf16, down to multiples of 2^-133, bf16's smallest
+ * step: only a block whose largest magnitude is below 448 * 2^-124 holds
+ * values between those, which dequantize exactly in fp32 and enter products to
+ * within 2^-133.
  *   Weights N x K: one scale per 128 x 128 block.
  *   Activations M x K: one scale per 128 elements of a row; infinities and
  *   NaNs become the NaN code and do not enter the block's scale, so they

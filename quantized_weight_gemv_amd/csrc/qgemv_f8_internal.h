@@ -177,7 +177,8 @@ __device__ __forceinline__ float max_of_8(float v)
 // and the block's scale byte.  The maximum passes over NaNs by itself and a
 // NaN stays one through the product and the conversion; an infinity, which
 // would become the scale and the largest code, sends the wave over its values
-// once more with NaNs in the place of whatever is not finite.
+// once more with NaNs in the place of whatever is not finite.  Under the
+// largest scale, 2^120, codes stop at 240: 256 would be 2^128.
 __device__ __forceinline__ uint32_t f8_quantize16(float (&v)[16], uint32_t (&w)[4])
 {
     auto largest = [&] {
@@ -195,6 +196,12 @@ __device__ __forceinline__ uint32_t f8_quantize16(float (&v)[16], uint32_t (&w)[
         amax = largest();
     }
     const uint32_t byte = f8_scale_byte(__float_as_uint(amax));
+    if (__any(byte == 120 + 127)) {
+        const float most = byte == 120 + 127 ? 0x1.ep127f : __builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)   // (a NaN compares false)
+            v[i] = fabsf(v[i]) > most ? copysignf(most, v[i]) : v[i];
+    }
     const float inv = f8_inverse(byte);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -207,7 +214,8 @@ __device__ __forceinline__ uint32_t f8_quantize16(float (&v)[16], uint32_t (&w)[
 __device__ __forceinline__ float f8_exponent(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // Eight codes (two words) times a power of two (f8_exponent) as a bf16
-// operand: exact (four significant bits, bf16's exponent range).
+// operand: exact (four significant bits, bf16's exponent range) down to
+// multiples of 2^-133, its subnormal step.
 __device__ __forceinline__ bf8_t f8_widen(uint32_t lo, uint32_t hi, float scale)
 {
     const bf2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);

@@ -14,6 +14,11 @@ namespace {
 constexpr int64_t kMaxK = 1 << 20;
 constexpr int64_t kMaxRows = 1 << 30;
 
+// The largest scale that a finite value needs, 2^120, and the largest code's
+// value under it that fp32 still holds (the next, 256, would be 2^128).
+constexpr int kMaxExponent = 120;
+constexpr double kMaxOfLast = 240.0;
+
 // The e4m3 code of v, |v| <= 448: the grid's step is 2^(x - 3) for 2^x <= |v|
 // < 2^(x + 1) and 2^-9 below 2^-6.  nearbyint rounds ties to even (the
 // default rounding mode), and a value that rounds up to the next power of two
@@ -91,8 +96,12 @@ qg_status qquantize_f8(const float *w, int64_t N, int64_t K, void *packed, size_
             scales[b * ls + c] = static_cast<uint8_t>(e + 127);
             for (int64_t n = b * 128; n < n1; ++n) {
                 uint8_t *row = out + ((n / 16) * cb + c) * 2048 + 16 * (n % 16);
-                for (int64_t k = c * 128; k < k1; ++k)
-                    row[256 * (k % 128 / 16) + k % 16] = e4m3_code(std::ldexp(static_cast<double>(w[n * K + k]), -e));
+                for (int64_t k = c * 128; k < k1; ++k) {
+                    double v = std::ldexp(static_cast<double>(w[n * K + k]), -e);
+                    if (e == kMaxExponent && std::isfinite(v))
+                        v = std::fmin(std::fmax(v, -kMaxOfLast), kMaxOfLast);
+                    row[256 * (k % 128 / 16) + k % 16] = e4m3_code(v);
+                }
             }
         }
     }
