@@ -601,16 +601,21 @@ def qmoe_route_backward(logits, route: MoeRoute, grad_weight=None, grad_loss=Non
     c, T, E, ld, mp = _logits(logits, mask)
     k = route.idx.shape[1]
     if route.idx.shape != (T, k) or route.weight.shape != (T, k) or route.counts.shape != (E,) or \
-            route.tokens.data_ptr() != route.counts.data_ptr() + 4 * E:
+            route.tokens.shape != (1,):
         raise ValueError("route is not of these logits")
     for name, t, n in (("grad_weight", grad_weight, (T, k)), ("grad_loss", grad_loss, None)):
         if t is not None and (t.numel() != 1 if n is None else tuple(t.shape) != n):
             raise ValueError(f"{name} has shape {list(t.shape)}")
     dl, dp = c.result(out, (T, E), logits.dtype, "out", T * E)
     f32, i32 = torch.float32, torch.int32
+    counts = route.counts
+    cp, tp = c.ptr(counts, i32, "route.counts", E), c.ptr(route.tokens, i32, "route.tokens", 1)
+    if tp != cp + 4 * E:   # a copy of what qmoe_route returned: the kernel reads both from one buffer
+        counts = torch.cat((counts, route.tokens))
+        cp = counts.data_ptr()
     c("qmoe_route_backward", logits.data_ptr(), _type(logits.dtype), ld, mp, T, E, k, int(renormalize),
       c.ptr(route.idx, i32, "route.idx", T * k), c.ptr(route.weight, f32, "route.weight", T * k),
-      c.ptr(route.counts, i32, "route.counts", E), c.opt(grad_weight, f32, "grad_weight", T * k),
+      cp, c.opt(grad_weight, f32, "grad_weight", T * k),
       c.opt(grad_loss, f32, "grad_loss", 1), dp)
     return dl
 
