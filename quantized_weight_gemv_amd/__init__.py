@@ -7,6 +7,10 @@ This module only marshals arguments: it checks tensor devices, dtypes, shapes
 and sizes (the C ABI cannot see buffer sizes), passes raw pointers and the
 current HIP stream, and turns a non-zero status into an exception.  Every step
 of the computation runs in the library's HIP kernels; there is no fallback.
+Autograd records none of the calls.  The f8 and routing calls, which have
+gradients of their own to be put together, refuse tensors that require one while
+gradients are recorded; torch.autograd.Function's forward and backward run
+without.
 If the library is missing the import of any entry point fails loudly.
 
 Names follow the C ABI in include/qgemv.h and include/qgemv_f8.h.
@@ -409,13 +413,23 @@ class _Call:
         self.torch = torch = _torch()
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError(f"{name} must be a device tensor")
+        if first.requires_grad:
+            self.no_grad(name)
         self.device = first.device
         self.index = first.get_device()
+
+    def no_grad(self, name: str):
+        # the calls are not recorded: an output without a gradient would end the backward pass unseen
+        if self.torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, which this call would not pass on: make it under "
+                             "torch.no_grad() or inside a torch.autograd.Function")
 
     def ptr(self, t, dtype, name: str, numel: int):
         # one pass over what has to hold; the reasons are looked up only for a refusal
         if isinstance(t, self.torch.Tensor) and t.get_device() == self.index and t.dtype is dtype and \
                 t.numel() >= numel and t.is_contiguous():
+            if t.requires_grad:
+                self.no_grad(name)
             return t.data_ptr()
         if not isinstance(t, self.torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a device tensor")
