@@ -400,6 +400,7 @@ __global__ __launch_bounds__(512, 2) void skinny_lds_kernel(SkinnyParams p)
     // whichever the next block is not copied into, holds them
     auto finish = [&](int rg, uint4 *X) {
         f4_t *buf = reinterpret_cast<f4_t *>(X);
+        wait_lds();
         bare_barrier();   // every wave has read its last block from X
 #pragma unroll
         for (int g = 0; g < G; ++g)
