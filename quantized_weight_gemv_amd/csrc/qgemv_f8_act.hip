@@ -1,11 +1,14 @@
 // f8 conversions (formats in qgemv_f8.h): activations to packed f8 and back,
 // packed weights to fp32 / fp16 and to the packed transposed matrix.
 //
-// All of them are bound by memory: each input byte is read once, each output
-// byte written once, sixteen values (one 16-byte word of codes) per lane, which
-// is one store of the codes and two or four loads.  8192 x 4096 in bf16: 17 us
-// to quantize, 17 back, 101 MB each, 5.9 TB/s (a copy of a gigabyte runs at
-// 5.2; part of the data is still in the last-level cache).
+// All of them are bound by memory: sixteen values (one 16-byte word of codes) a
+// lane.  Activations: each byte read and written once, one store of the codes
+// and two or four loads.  8192 x 4096 in bf16: 17 us to quantize, 17 back, 101 MB
+// each, 5.9 TB/s (a copy of a gigabyte runs at 5.2; part of the data is still in
+// the last-level cache).  Transposed weights: 28672 x 4096 43 us, 5.5 TB/s; 4096
+// x 4096 9.5, 3.5 TB/s.  Weights back to fp32 or fp16 run at 2.5 to 3.4 TB/s
+// (28672 x 4096 190 and 142 us, 4096 x 4096 26 and 15): whole lines are written,
+// but read in pieces of 16 bytes, 256 apart.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -28,10 +28,13 @@
 // cancel, it loses up to a tenth of the sum of 200 others of 1 to 6.
 // W is the first operand, so a lane holds four consecutive n of a row of Y;
 // the sums are turned through LDS for stores of whole lines.
-// Bound by the matrix cores on large products: 8192 x 14336 x 4096 takes 671 us
-// with bf16 outputs, 1.43 PFLOP/s, and 720 with fp32 (a library product of bf16
-// operands 1.41 PFLOP/s, the instruction alone, on registers, 2.4; the clock
-// drops under it); 2048 x 8192 x 4096 104 us.
+// Bound by the matrix cores on large products: 8192 x 14336 x 4096 takes 671 to
+// 710 us with bf16 outputs, 1.36 to 1.43 PFLOP/s, and 720 with fp32 (a library
+// product of bf16 operands 1.41 PFLOP/s, the instruction alone, on registers,
+// 2.4): they are busy 70 % of the time, at 1.9 GHz under that load; 2048 x 8192 x
+// 4096 104 us.  Short products wait for their chain of steps: with one wave a SIMD
+// (733 x 2053 x 5011, 29 us) a step of 64 columns takes 720 cycles, of which the
+// products are 250, the widening beside them 240.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -325,7 +325,8 @@ __global__ __launch_bounds__(64 * NW, 4) void skinny_kernel(SkinnyParams p)
 // c ^ ((r / 2) % 8): the 16 rows of a quarter of an operand read touch all 64
 // banks.  Every unit needs all of X: 64 x 4096 x 14336 takes 28 us, of which
 // W alone is 14, the copies of X 11 (235 MB at 20 TB/s) and the products,
-// behind them, 3; 17 tokens take 15, 32 19.  Four waves with four buffers each
+// behind them, 3: W's loads and X's copies share the way and add up; 17 tokens
+// take 15, 32 19.  Four waves with four buffers each
 // take as long (29, 15, 19).
 template <int G>
 __global__ __launch_bounds__(512, 2) void skinny_lds_kernel(SkinnyParams p)

@@ -22,12 +22,20 @@
 // Tiles beyond whole rounds of the card's compute units are split along the
 // rows among the units that would be idle; their parts go to the workspace
 // and a second kernel adds them in a fixed order (no atomics).
-// 8192 x 4096 x 4096, one round of tiles: 224 us, 1.23 PFLOP/s (a library
+// 8192 x 4096 x 4096, one round of tiles: 226 us, 1.22 PFLOP/s (a library
 // product of bf16 operands 1.4, the instruction alone 2.4).  With nothing
 // loaded it takes 153, without the widening as well 131, with the products
-// alone 127: what is left is the wait for operands, which are copied two steps
-// before they are read (four buffers of 32 KB are what LDS holds).
-// 8192 x 6144 x 4096: 381 us and 18 for the second kernel.
+// alone 127.  8192 x 6144 x 4096: 350 us with the second kernel, of whose 18 us
+// it is the rest; the matrix cores are busy 58 % of the waves' time, waves wait
+// for loads and barriers 17 %, and a quarter of LDS cycles are conflicts.
+// The compiler waits where the kernel does not ask for it: in dense calls it
+// widens the scale bytes at the head of each four steps, behind a wait for all
+// loads; per expert the slots' numbers are the newest loads when their rows are
+// addressed, so every step waits for all of them, and unaligned rows of dY
+// branch as well.  64 experts of 2048 x 2048 with 375 slots each take 856 us
+// (writing 1.07 GB of dW would take 208), 16 of 4096 x 4096 with 1024 1250 us,
+// 0.44 PFLOP/s.  The 256 x 256 form keeps 11 registers in scratch memory,
+// outside of the loop.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -41,7 +49,10 @@ namespace {
 
 constexpr int kStep = 32;     // rows per step
 constexpr int kThreads = 256;
-constexpr int kCus = 256;     // compute units that a round of tiles fills
+// Compute units that a round of tiles fills.  Not asked from the device: the
+// size of the workspace has to be the same for the query and the call, and the
+// order of the sums the same on any device.
+constexpr int kCus = 256;
 constexpr int kPartRows = 1024;
 
 typedef short s4_t __attribute__((ext_vector_type(4)));
@@ -110,8 +121,8 @@ __global__ __launch_bounds__(kThreads, TM == 4 ? 1 : 2) void wgrad_kernel(WgradP
     // zeros: they lie outside of the buffers that loads are made from.  Rows
     // of an expert are gathered with whole addresses instead; there dY's are
     // read from g_zero and X's codes masked, past the end as well as where a
-    // slot names no row.  No branch: the loads of a step stay in one sequence,
-    // which the waits below count.
+    // slot names no row.  No branch where dY is copied: the loads of a step stay
+    // in one sequence, which the waits below count.
     const int count = (int)(r1 - r0);
     const uint8_t *const dY = reinterpret_cast<const uint8_t *>(p.dY);
     const uint8_t *const zero = reinterpret_cast<const uint8_t *>(&g_zero);
@@ -468,13 +479,15 @@ __global__ __launch_bounds__(256) void join_kernel(JoinParams p)
 }
 
 // How a dense dW is cut.  Tiles of 256 x 256 where they fill most of a round
-// of compute units (8192 x 6144 x 4096: 406 us, 1016 TFLOP/s), else of
-// 128 x 128, two to a unit.  The tiles beyond whole rounds are cut along the
-// rows in as many parts as idle units allow: 8192 x 6144 x 4096 takes 406 us
-// for 476 without, 16384 x 1024 x 1024 takes 53 for 202.  A part has at least
-// 1024 rows, since the parts' way through memory and the second launch cost
-// more than they save on fewer: 1024 x 2048 x 2048 takes 21 us whole and 34 in
-// parts of 512 rows, 519 x 1288 x 2056 takes 15 whole and 23 in two parts.
+// of compute units, else of 128 x 128, two to a unit.  The tiles beyond whole
+// rounds are cut along the rows in as many parts as idle units allow: 8192 x
+// 6144 x 4096 takes 350 us for 389 without, 16384 x 1024 x 1024 53 for 169, 4096
+// x 1024 x 1024 29 for 47.  A part has at least 1024 rows, since the parts' way
+// through memory and the second launch cost more than they save on fewer: 1024
+// x 2048 x 2048 takes 21 us whole and 35 in parts of 512 rows.  Two parts of
+// little more than that gain with few tiles (2048 x 1024 x 1024 23 us for 26)
+// and lose with many (2048 x 2048 x 2048 39 for 32, 3000 x 2048 x 2048 46 for 42;
+// from 4096 rows on they are even or gain).
 struct Cut {
     int size, tiles_n, tiles, whole, parts;
 };
