@@ -1,19 +1,20 @@
 """Python binding of libqgemv.so (gfx950): fused dequantize-and-multiply of
 block-quantized weights (Q4_0, Q8_0, plain 2-bit q2w and 8-bit floating f8),
-8-bit activation checkpoints with the products of the backward pass, and
-expert routing.
+8-bit activation checkpoints with the products of the backward pass, expert
+routing, and the attention step: head norms with the position rotation, a
+paged cache quantised as it is written, attention of new tokens over it.
 
 This module only marshals arguments: it checks tensor devices, dtypes, shapes
 and sizes (the C ABI cannot see buffer sizes), passes raw pointers and the
 current HIP stream, and turns a non-zero status into an exception.  Every step
 of the computation runs in the library's HIP kernels; there is no fallback.
-Autograd records none of the calls.  The f8 and routing calls, which have
-gradients of their own to be put together, refuse tensors that require one while
-gradients are recorded; torch.autograd.Function's forward and backward run
+Autograd records none of the calls.  The f8, routing and attention calls
+refuse tensors that require a gradient while gradients are recorded; torch.autograd.Function's forward and backward run
 without.
 If the library is missing the import of any entry point fails loudly.
 
-Names follow the C ABI in include/qgemv.h and include/qgemv_f8.h.
+Names follow the C ABI in include/qgemv.h, include/qgemv_f8.h and
+include/qgemv_attn.h.
 """
 from __future__ import annotations
 
@@ -59,7 +60,8 @@ def lib() -> ctypes.CDLL:
     except ImportError:
         pass
     L = ctypes.CDLL(LIB_PATH)
-    vp, i64, sz, c_int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    vp, i64, sz, c_int, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+    turn = [vp, vp, c_int, f32, vp, c_int, vp, vp, c_int, c_int]   # gains, eps, positions, sections, freq, rot
     sig = {
         "qg_status_str": (ctypes.c_char_p, [c_int]),
         "qpacked_bytes_q4_0": (sz, [i64, i64]),
@@ -97,6 +99,19 @@ def lib() -> ctypes.CDLL:
         "qmoe_route_backward": (c_int, [vp, c_int, i64, vp, i64, i64, c_int, c_int, vp, vp, vp, vp, vp, vp, vp]),
         "qmoe_gemm_f8": (c_int, [vp, i64, vp, i64, c_int, vp, vp, vp, c_int, i64, i64, vp]),
         "qmoe_gemm_f8_wgrad": (c_int, [vp, vp, i64, c_int, vp, vp, i64, vp, c_int, i64, i64, vp]),
+        "qkv_page_bytes": (sz, [c_int, c_int, c_int, c_int]),
+        "qhead_norm_rope": (c_int, [vp, i64, c_int, vp, i64, c_int, c_int, *turn, i64, c_int, vp, i64, vp, i64, c_int,
+                                    vp]),
+        "qhead_norm_rope_backward_workspace": (sz, [i64, c_int, c_int, c_int, c_int]),
+        "qhead_norm_rope_backward": (c_int, [vp, i64, vp, i64, c_int, vp, i64, c_int, vp, i64, c_int, c_int, *turn,
+                                             i64, c_int, vp, i64, vp, i64, vp, vp, vp]),
+        "qkv_write": (c_int, [vp, i64, vp, i64, c_int, vp, i64, vp, i64, c_int, c_int, c_int, c_int, vp]),
+        "qkv_read": (c_int, [vp, i64, c_int, c_int, c_int, c_int, vp, i64, vp, vp, c_int, vp]),
+        "qkv_norm_rope_write": (c_int, [vp, i64, c_int, vp, i64, vp, i64, c_int, *turn, i64, vp, vp, i64, c_int, vp,
+                                        i64, c_int, c_int, c_int, c_int, vp]),
+        "qattn_decode_workspace": (sz, [i64, c_int, c_int, c_int, c_int, c_int, i64]),
+        "qattn_decode": (c_int, [vp, i64, c_int, c_int, c_int, c_int, vp, c_int, i64, i64, c_int, c_int, vp, i64, vp,
+                                 f32, i64, f32, vp, vp, vp]),
         "qg_time_next_launch": (None, [vp, vp]),
         "qg_device_cus": (c_int, [c_int, ctypes.POINTER(c_int)]),
         "qg_set_gemv_shape": (None, [c_int, c_int, c_int, c_int, i64, c_int, c_int, c_int]),
@@ -120,6 +135,8 @@ def exported_symbols() -> list[str]:
             "qpacked_bytes_f8", "qact_bytes_f8", "qquantize_f8", "qdequant_f8", "qtranspose_f8", "qact_quantize_f8",
             "qact_dequant_f8", "qgemv_f8", "qgemm_f8", "qgemm_f8_wgrad_workspace", "qgemm_f8_wgrad",
             "qmoe_route_workspace", "qmoe_route", "qmoe_route_backward", "qmoe_gemm_f8", "qmoe_gemm_f8_wgrad",
+            "qkv_page_bytes", "qhead_norm_rope", "qhead_norm_rope_backward_workspace", "qhead_norm_rope_backward",
+            "qkv_write", "qkv_read", "qkv_norm_rope_write", "qattn_decode_workspace", "qattn_decode",
             "qg_time_next_launch", "qg_device_cus", "qg_set_gemv_shape", "qg_read_probe", "qg_set_prefill_shape"]
 
 
@@ -671,6 +688,251 @@ def qmoe_gemm_f8_wgrad(dY, xq, T: int, order, offsets, P: int, N: int, K: int, d
       c.ptr(order, torch.int32, "order", S), c.ptr(offsets, torch.int32, "offsets", P + 1), P,
       wp, int(accumulate), N, K)
     return dW
+
+
+# ------------------------------------------------------------ attention step
+class KVCache(NamedTuple):
+    """A paged key-value cache: uint8 pages (laid out as include/qgemv_attn.h
+    says), tokens a page, key heads, their dimension, and what it holds:
+    torch.float8_e4m3fn (with a power of two a token and head), float16 or
+    bfloat16.  qkv_cache makes a new one."""
+    data: object      # uint8 [pages][qkv_page_bytes]
+    page: int
+    heads: int
+    dim: int
+    dtype: object
+
+
+def _cache_type(dtype) -> int:
+    torch = _torch()
+    code = {torch.float8_e4m3fn: 3, torch.float16: 1, torch.bfloat16: 2}.get(dtype)
+    if code is None:
+        raise TypeError(f"a cache holds float8_e4m3fn, float16 or bfloat16, got {dtype}")
+    return code
+
+
+def qkv_page_bytes(page: int, heads: int, dim: int, dtype) -> int:
+    """Bytes of one cache page (0 where the sizes are out of range)."""
+    return int(lib().qkv_page_bytes(page, heads, dim, _cache_type(dtype)))
+
+
+def qkv_cache(pages: int, page: int, heads: int, dim: int, dtype=None, device="cuda") -> KVCache:
+    """A cache of zeros; dtype float8_e4m3fn by default."""
+    torch = _torch()
+    dtype = dtype or torch.float8_e4m3fn
+    nb = qkv_page_bytes(page, heads, dim, dtype)
+    _sizes("qkv_page_bytes", nb)
+    return KVCache(torch.zeros((pages, nb), dtype=torch.uint8, device=device), page, heads, dim, dtype)
+
+
+def _cache(c, fn: str, cache: KVCache):
+    """The cache's arguments: address, pages, page, heads, dim, type."""
+    code = _cache_type(cache.dtype)
+    nb = int(lib().qkv_page_bytes(cache.page, cache.heads, cache.dim, code))
+    _sizes(fn, nb)
+    n = cache.data.numel()
+    if n % nb or n == 0:
+        raise ValueError(f"cache.data has {n} bytes, not a multiple of {nb}")
+    return c.ptr(cache.data, c.torch.uint8, "cache.data", n), n // nb, cache.page, cache.heads, cache.dim, code
+
+
+def _rows(c, x, name: str, dtype, T: int, D: int, heads=None):
+    """Address, distance of tokens and heads of a tensor [T][heads][D]."""
+    if not isinstance(x, c.torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if x.get_device() != c.index:
+        raise ValueError(f"{name} is on {x.device}, the call's other tensors on {c.device}")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or (heads is not None and x.shape[1] != heads):
+        raise ValueError(f"{name} must be [{T}][{'heads' if heads is None else heads}][{D}], got {list(x.shape)}")
+    if x.requires_grad:
+        c.no_grad(name)
+    n = x.shape[1]
+    ld, of_head, of_element = x.stride()
+    if (D > 1 and of_element != 1) or (n > 1 and of_head != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return x.data_ptr(), ld if T > 1 else n * D, n
+
+
+def _turn(c, q, k, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, k_heads):
+    """The arguments of norm and rotation that the calls have in common."""
+    torch = c.torch
+    T, _, D = q.shape
+    if (q_gain is None) != (k_gain is None) and k_heads:
+        raise ValueError("q_gain and k_gain: both or none")
+    gains, gain_type = (None, None), 0
+    if q_gain is not None:
+        k_gain = q_gain if k_gain is None else k_gain
+        gain_type = _type(q_gain.dtype)
+        gains = tuple(c.ptr(g, q_gain.dtype, n, D) for g, n in ((q_gain, "q_gain"), (k_gain, "k_gain")))
+        if q_gain.numel() != D or k_gain.numel() != D:
+            raise ValueError(f"gains must be [{D}]")
+    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
+    if rot == 0:
+        return *gains, gain_type, eps, None, 1, None, None, 0, 0
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.shape[-1] != T or positions.dim() > 2:
+        raise ValueError(f"positions must be [{T}] or [axes][{T}], got {list(positions.shape)}")
+    if sections is not None:
+        if len(sections) != axes or sum(sections) != rot // 2:
+            raise ValueError(f"sections must be {axes} numbers with the sum {rot // 2}, got {list(sections)}")
+        sections = (ctypes.c_int32 * axes)(*sections)
+    elif axes > 1:
+        raise ValueError("positions of several axes need sections")
+    return (*gains, gain_type, eps, c.ptr(positions, torch.int32, "positions", axes * T), axes, sections,
+            c.ptr(inv_freq, torch.float32, "inv_freq", rot // 2), rot, int(interleaved))
+
+
+def _head_tensors(c, q, k):
+    if not isinstance(q, c.torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [T][heads][D]")
+    T, _, D = q.shape
+    qp, ldq, nq = _rows(c, q, "q", q.dtype, T, D)
+    kp, ldk, nk = _rows(c, k, "k", q.dtype, T, D) if k is not None else (None, 0, 0)
+    return T, D, nq, nk, (qp, ldq, nq, kp, ldk, nk, _type(q.dtype))
+
+
+def _head_outputs(c, out, name: str, T: int, D: int, nq: int, nk: int, dtype):
+    """Two head tensors of the caller's or new ones (no second one without k)."""
+    if out is None:
+        yq = c.new((T, nq, D), dtype)
+        yk = c.new((T, nk, D), dtype) if nk else None
+        return yq, yk, yq.data_ptr(), nq * D, yk.data_ptr() if nk else None, nk * D
+    yq, yk = out
+    qp, ldq, _ = _rows(c, yq, name + "[0]", dtype, T, D, nq)
+    kp, ldk, _ = _rows(c, yk, name + "[1]", dtype, T, D, nk) if nk else (None, 0, 0)
+    return yq, yk, qp, ldq, kp, ldk
+
+
+def qhead_norm_rope(q, k, positions, inv_freq, q_gain=None, k_gain=None, eps: float = 1e-6, interleaved: bool = False,
+                    sections=None, dtype=None, out=None):
+    """RMS norm of each query and key head with a gain, and the rotation of its
+    first 2 * inv_freq.numel() elements by the angles positions * inv_freq, in
+    one pass: (q', k') in `dtype` (the inputs' by default).
+
+    q, k: [T][heads][D] (fp32, fp16 or bf16; the heads of a token contiguous,
+    tokens any distance apart: parts of one projection's output); k may be
+    None.  Without gains there is no norm.  positions: int32 [T], or [axes][T]
+    with `sections`, the pairs that each axis turns; inv_freq: fp32, None: no
+    rotation.  Pairs are halves (i, i + rot / 2), interleaved (2 i, 2 i + 1).
+    out: the two results' tensors, which may be q and k themselves."""
+    c = _Call(q, "q")
+    T, D, nq, nk, heads = _head_tensors(c, q, k)
+    turn = _turn(c, q, k, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
+    dtype = dtype or (q.dtype if out is None else out[0].dtype)
+    code = _type(dtype)
+    yq, yk, *ys = _head_outputs(c, out, "out", T, D, nq, nk, dtype)
+    c("qhead_norm_rope", *heads, *turn, T, D, *ys, code)
+    return yq, yk
+
+
+def qhead_norm_rope_backward(dq, dk, q, k, positions, inv_freq, q_gain=None, k_gain=None, eps: float = 1e-6,
+                             interleaved: bool = False, sections=None, out=None):
+    """From the gradients of qhead_norm_rope's results (one type) and its
+    inputs: (q's gradient, k's, q_gain's, k_gain's), the first two in the
+    inputs' type, the gains' in fp32 (None without gains)."""
+    c = _Call(q, "q")
+    T, D, nq, nk, heads = _head_tensors(c, q, k)
+    turn = _turn(c, q, k, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
+    gqp, ldgq, _ = _rows(c, dq, "dq", dq.dtype, T, D, nq)
+    gkp, ldgk, _ = _rows(c, dk, "dk", dq.dtype, T, D, nk) if nk else (None, 0, 0)
+    gq, gk, *gs = _head_outputs(c, out, "out", T, D, nq, nk, q.dtype)
+    ws = int(lib().qhead_norm_rope_backward_workspace(T, nq, nk, D, int(q_gain is not None)))
+    g = w = None
+    if ws:
+        g, w = c.new((2, D), c.torch.float32), c.new((ws,), c.torch.uint8)
+    c("qhead_norm_rope_backward", gqp, ldgq, gkp, ldgk, _type(dq.dtype), *heads, *turn, T, D, *gs,
+      g.data_ptr() if ws else None, w.data_ptr() if ws else None)
+    return gq, gk, g[0] if ws else None, g[1] if ws and nk else None
+
+
+def qkv_write(cache: KVCache, k, v, slots):
+    """k and v[T][heads][dim] into the slots (int32 [T], page number * cache.page
+    + place in the page; -1: not written) of the cache, quantised on the way."""
+    c = _Call(cache.data, "cache.data")
+    args = _cache(c, "qkv_write", cache)
+    T = slots.numel()
+    kp, ldk, _ = _rows(c, k, "k", k.dtype, T, cache.dim, cache.heads)
+    vp, ldv, _ = _rows(c, v, "v", k.dtype, T, cache.dim, cache.heads)
+    c("qkv_write", kp, ldk, vp, ldv, _type(k.dtype), c.ptr(slots, c.torch.int32, "slots", T), T, *args)
+
+
+def qkv_read(cache: KVCache, slots, dtype=None):
+    """(k, v)[T][heads][dim] of the slots, fp32 by default; zeros for slots outside the cache."""
+    c = _Call(cache.data, "cache.data")
+    args = _cache(c, "qkv_read", cache)
+    T = slots.numel()
+    dtype = dtype or c.torch.float32
+    code = _type(dtype)
+    sp = c.ptr(slots, c.torch.int32, "slots", T)
+    k, v = c.new((T, cache.heads, cache.dim), dtype), c.new((T, cache.heads, cache.dim), dtype)
+    c("qkv_read", *args, sp, T, k.data_ptr(), v.data_ptr(), code)
+    return k, v
+
+
+def qkv_norm_rope_write(cache: KVCache, q, k, v, slots, positions, inv_freq, q_gain=None, k_gain=None,
+                        eps: float = 1e-6, interleaved: bool = False, sections=None, dtype=None, out=None):
+    """qhead_norm_rope of q and k with the keys, and v as it is, written into
+    the cache's slots, in one launch: q' in `dtype` (q's by default)."""
+    c = _Call(cache.data, "cache.data")
+    args = _cache(c, "qkv_norm_rope_write", cache)
+    T, D, nq, nk, heads = _head_tensors(c, q, k)
+    if D != cache.dim or nk != cache.heads:
+        raise ValueError(f"k must be [{T}][{cache.heads}][{cache.dim}]")
+    vp, ldv, _ = _rows(c, v, "v", q.dtype, T, D, nk)
+    if slots.numel() != T:
+        raise ValueError(f"slots must be [{T}]")
+    turn = _turn(c, q, k, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
+    dtype = dtype or (q.dtype if out is None else out.dtype)
+    code = _type(dtype)
+    if out is None:
+        out = c.new((T, nq, D), dtype)
+        yp, ldy = out.data_ptr(), nq * D
+    else:
+        yp, ldy, _ = _rows(c, out, "out", dtype, T, D, nq)
+    c("qkv_norm_rope_write", *heads[:5], vp, ldv, heads[6], *turn, T,
+      c.ptr(slots, c.torch.int32, "slots", T), yp, ldy, code, *args)
+    return out
+
+
+def qattn_decode(cache: KVCache, q, table, lens, scale: float | None = None, window: int = 0, softcap: float = 0.0,
+                 out=None):
+    """Attention of the last M tokens of each sequence over the cache:
+    softmax(scale q.k) v in q's type and shape.
+
+    q: [B][M][heads][dim] (fp16 or bf16, M up to 16) or [B][heads][dim] for one
+    token, the heads of a token contiguous; table: int32 [B][width], the pages
+    of each sequence; lens: int32 [B], its tokens, the new ones among them.
+    New token i sees the places up to its own, lens - M + i, the last `window`
+    of them if window > 0; softcap > 0 takes scores s as softcap *
+    tanh(s / softcap).  scale: dim ** -0.5 by default.  A query that sees
+    nothing gets zeros."""
+    c = _Call(q, "q")
+    torch = c.torch
+    args = _cache(c, "qattn_decode", cache)
+    if q.dim() not in (3, 4) or q.shape[-1] != cache.dim:
+        raise ValueError(f"q must be [B][M][heads][{cache.dim}] or [B][heads][{cache.dim}]")
+    B, H, D = q.shape[0], q.shape[-2], cache.dim
+    M = q.shape[1] if q.dim() == 4 else 1
+    if q.stride(-1) != 1 or (H > 1 and q.stride(-2) != D):
+        raise ValueError("q: the heads of a token must be contiguous")
+    ld = q.stride(0) if q.dim() == 3 else q.stride(1) if M > 1 else q.stride(0)
+    if M > 1 and B > 1 and q.stride(0) != M * ld:
+        raise ValueError("q: the tokens must be the same distance apart in and between the sequences")
+    if B * M == 1:
+        ld = H * D
+    if table.dim() != 2 or table.shape[0] != B or lens.numel() != B:
+        raise ValueError(f"table must be [{B}][width], lens [{B}]")
+    W = table.shape[1]
+    code = _type(q.dtype)
+    out, op = c.result(out, tuple(q.shape), q.dtype, "out", B * M * H * D)
+    ws = int(lib().qattn_decode_workspace(B, M, H, cache.heads, D, cache.page, W))
+    w = c.new((ws,), torch.uint8) if ws else None
+    c("qattn_decode", *args, q.data_ptr(), code, ld, B, M, H, c.ptr(table, torch.int32, "table", B * W), W,
+      c.ptr(lens, torch.int32, "lens", B), D ** -0.5 if scale is None else scale, window, softcap, op,
+      w.data_ptr() if ws else None)
+    return out
 
 
 # --------------------------------------------------------------- measurement

@@ -1,0 +1,688 @@
+// Norms of query and key heads with the rotation of positions, forward and
+// backward, and the paged cache written and read back (definitions in
+// qgemv_attn.h).
+//
+// L lanes hold a head vector (8, 16 or 32 for up to 64, 128 and 256 elements), a
+// wave 64 / L heads of one token.  A lane's eight elements are four pairs of the
+// rotation: halves (i and i + rot / 2, two pieces of four) or neighbours (eight
+// in a row), so nothing moves between lanes but the sum of squares.  The four
+// cosines and sines of a lane are the same for every head of a token: a wave
+// takes them once and walks over the heads.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "qgemv_attn_internal.h"
+
+namespace qg {
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kMaxBlocks = 1 << 20;
+constexpr double kInvTwoPi = 0.15915494309189533577;
+
+struct __attribute__((packed, aligned(2))) Raw8 {
+    uint32_t w[2];
+};
+struct __attribute__((packed, aligned(4))) Raw16f {
+    uint32_t w[4];
+};
+
+template <typename T>
+__device__ __forceinline__ void load4(const T *p, float *v)
+{
+    if constexpr (sizeof(T) == 4) {
+        const Raw16f r = *reinterpret_cast<const Raw16f *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __uint_as_float(r.w[i]);
+    } else {
+        const Raw8 r = *reinterpret_cast<const Raw8 *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = to_f32(T{(uint16_t)(r.w[i / 2] >> (16 * (i & 1)))});
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T *p, const float *v)
+{
+    if constexpr (sizeof(T) == 4) {
+        Raw16f r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = __float_as_uint(v[i]);
+        *reinterpret_cast<Raw16f *>(p) = r;
+    } else {
+        *reinterpret_cast<Raw8 *>(p) = Raw8{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
+    }
+}
+
+// A lane's eight elements from `lo` and `hi` of a vector; the type is the
+// launch's, so the branches are the wave's.
+__device__ __forceinline__ void load8_as(int type, const void *base, int64_t at, int lo, int hi, float (&v)[8])
+{
+    if (type == QG_F32) {
+        load4(static_cast<const float *>(base) + at + lo, v);
+        load4(static_cast<const float *>(base) + at + hi, v + 4);
+    } else if (type == QG_F16) {
+        load4(static_cast<const Fp16 *>(base) + at + lo, v);
+        load4(static_cast<const Fp16 *>(base) + at + hi, v + 4);
+    } else {
+        load4(static_cast<const Bf16 *>(base) + at + lo, v);
+        load4(static_cast<const Bf16 *>(base) + at + hi, v + 4);
+    }
+}
+__device__ __forceinline__ void store8_as(int type, void *base, int64_t at, int lo, int hi, const float (&v)[8])
+{
+    if (type == QG_F32) {
+        store4(static_cast<float *>(base) + at + lo, v);
+        store4(static_cast<float *>(base) + at + hi, v + 4);
+    } else if (type == QG_F16) {
+        store4(static_cast<Fp16 *>(base) + at + lo, v);
+        store4(static_cast<Fp16 *>(base) + at + hi, v + 4);
+    } else {
+        store4(static_cast<Bf16 *>(base) + at + lo, v);
+        store4(static_cast<Bf16 *>(base) + at + hi, v + 4);
+    }
+}
+
+template <int kCtrl>
+__device__ __forceinline__ double dpp(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, 0xF, 0xF, true);
+    const uint32_t hi =
+        (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+template <int L>
+__device__ __forceinline__ double group_sum(double v)
+{
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    if constexpr (L >= 16)
+        v += dpp<0x140>(v);
+    if constexpr (L >= 32) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const f2_t lo = pair16(__uint_as_float((uint32_t)u)), hi = pair16(__uint_as_float((uint32_t)(u >> 32)));
+        auto of = [](float h, float l) {
+            return __builtin_bit_cast(double, (uint64_t)__float_as_uint(h) << 32 | __float_as_uint(l));
+        };
+        v = of(hi[0], lo[0]) + of(hi[1], lo[1]);
+    }
+    return v;
+}
+
+// A wave's lane inside its head vector.
+struct Place {
+    int sub, l;     // head of the group, lane of the head
+    bool on;        // has elements
+    bool turned;    // its pairs are turned
+    int lo, hi;     // its elements: lo .. lo + 3, hi .. hi + 3
+};
+
+template <int L>
+__device__ __forceinline__ Place place(int D, int half, bool interleaved)
+{
+    const int lane = threadIdx.x & 63;
+    Place p;
+    p.sub = lane / L;
+    p.l = lane % L;
+    p.on = 8 * p.l < D;
+    p.turned = p.on && 4 * p.l < half;
+    const bool halves = p.turned && !interleaved;
+    p.lo = halves ? 4 * p.l : 8 * p.l;
+    p.hi = halves ? half + 4 * p.l : 8 * p.l + 4;
+    return p;
+}
+
+// Turns of the four pairs of a lane at a token's positions: position * freq /
+// 2 pi in 64 bits, whose whole turns are dropped before the sine (far positions
+// keep all 24 bits of the rest).
+template <typename F>
+__device__ __forceinline__ void turns(const HeadArgs &a, const Place &p, int64_t t, F (&c)[4], F (&s)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = 1, s[i] = 0;
+    if (!p.turned)
+        return;
+    const Raw16f f = *reinterpret_cast<const Raw16f *>(a.freq + 4 * p.l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int pair = 4 * p.l + i;
+        int axis = 0;
+        for (int j = 0; j + 1 < a.axes; ++j)
+            axis += pair >= a.sections[j] ? 1 : 0;
+        double turn = (double)a.positions[axis * a.T + t] * (double)__uint_as_float(f.w[i]) * kInvTwoPi;
+        turn -= rint(turn);
+        if constexpr (sizeof(F) == 8)
+            sincospi(2.0 * turn, &s[i], &c[i]);
+        else
+            sincospif((float)(2.0 * turn), &s[i], &c[i]);
+    }
+}
+
+template <typename F>
+__device__ __forceinline__ void turn(const Place &p, bool interleaved, const F (&c)[4], const F (&s)[4], F (&v)[8])
+{
+    if (!p.turned)
+        return;   // (what is not turned is left as it is, infinities too)
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F x = v[2 * i], y = v[2 * i + 1];
+            v[2 * i] = x * c[i] - y * s[i];
+            v[2 * i + 1] = y * c[i] + x * s[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F x = v[i], y = v[4 + i];
+            v[i] = x * c[i] - y * s[i];
+            v[4 + i] = y * c[i] + x * s[i];
+        }
+    }
+}
+
+__device__ __forceinline__ float inverse_root(float v) { return rsqrtf(v); }
+__device__ __forceinline__ double inverse_root(double v) { return 1.0 / sqrt(v); }
+
+template <int L, typename F>
+__device__ __forceinline__ F inverse_norm(const F (&v)[8], int D, float eps)
+{
+    F ss = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        ss += v[i] * v[i];
+    return inverse_root(group_sum<L>(ss) / (F)D + (F)eps);
+}
+
+// A lane's eight values of an f8 vector held by L lanes: codes and scale byte,
+// by the rule of f8_quantize16.
+template <int L>
+__device__ __forceinline__ uint32_t quantize8(float (&v)[8], uint32_t (&w)[2])
+{
+    auto largest = [&] {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = fmaxf(m, fabsf(v[i]));
+        return group_max<L>(m);
+    };
+    float amax = largest();
+    if (__any(amax == __builtin_inff())) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = fabsf(v[i]) < __builtin_inff() ? v[i] : __builtin_nanf("");
+        amax = largest();
+    }
+    const uint32_t byte = f8_scale_byte(__float_as_uint(amax));
+    if (__any(byte == 120 + 127)) {
+        const float most = byte == 120 + 127 ? 0x1.ep127f : __builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = fabsf(v[i]) > most ? copysignf(most, v[i]) : v[i];
+    }
+    const float inv = f8_inverse(byte);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = f8_pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    return byte;
+}
+
+// The fp32 value below a 64-bit one in magnitude with the last bit set if
+// anything was cut: rounding it to fewer bits gives what rounding the 64-bit
+// value gives.
+__device__ __forceinline__ float sticky(double v)
+{
+    const float f = __double2float_rz(v);
+    return (double)f != v ? __uint_as_float(__float_as_uint(f) | 1u) : f;
+}
+
+// A head's vector of a cache slot: element and scale addresses.
+struct SlotAt {
+    uint8_t *codes, *scale;
+};
+__device__ __forceinline__ SlotAt slot_at(const KvCache &c, int slot, int head, int kv)
+{
+    uint8_t *page = c.data + (int64_t)(slot >> c.log_page) * c.page_bytes;
+    const int row = (head * 2 + kv) * c.page + (slot & (c.page - 1));
+    return SlotAt{page + (int64_t)row * c.dim * (c.type == QG_F8 ? 1 : 2), page + c.scales + row};
+}
+
+// Eight values of a lane into a slot's vector.
+template <int L>
+__device__ __forceinline__ void put(const KvCache &c, int slot, int head, int kv, bool on, int l, int lo, int hi,
+                                    float (&v)[8])
+{
+    if (c.type == QG_F8) {
+        uint32_t w[2];
+        const uint32_t byte = quantize8<L>(v, w);
+        if (on) {
+            const SlotAt at = slot_at(c, slot, head, kv);
+            *reinterpret_cast<uint32_t *>(at.codes + lo) = w[0];
+            *reinterpret_cast<uint32_t *>(at.codes + hi) = w[1];
+            if (l == 0)
+                *at.scale = (uint8_t)byte;
+        }
+    } else if (on) {
+        store8_as(c.type, slot_at(c, slot, head, kv).codes, 0, lo, hi, v);
+    }
+}
+
+// Heads of one kind of a token, groups first .. last - 1 of them.
+template <typename T, int L, typename F, typename Done>
+__device__ __forceinline__ void walk(const HeadArgs &a, const Place &p, int64_t t, int kind, int first, int last,
+                                     const F (&c)[4], const F (&s)[4], Done done)
+{
+    const bool plain = kind == 2;
+    float gain[8];
+    const bool normed = !plain && a.gain[0] != nullptr;
+    if (normed && p.on)
+        load8_as(a.gain_type, a.gain[kind], 0, p.lo, p.hi, gain);
+    const T *x = static_cast<const T *>(a.x[kind]) + t * a.ldx[kind];
+#pragma unroll 2
+    for (int g = first; g < last; ++g) {
+        const int head = g * (64 / L) + p.sub;
+        const bool on = p.on && head < a.heads[kind];
+        float in[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            in[i] = 0.0f;
+        if (on) {
+            load4(x + head * a.D + p.lo, in);
+            load4(x + head * a.D + p.hi, in + 4);
+        }
+        F v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = in[i];
+        if (normed) {
+            const F r = inverse_norm<L>(v, a.D, a.eps);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = v[i] * r * (F)gain[i];
+        }
+        if (!plain)
+            turn(p, a.interleaved, c, s, v);
+        done(head, on, v);
+    }
+}
+
+// Wave `unit` of the launch takes part unit % parts of the groups of heads of
+// token unit / parts.
+template <typename T, int L, bool kWrite, bool kF8>
+__global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
+{
+    const Place p = place<L>(a.D, a.half, a.interleaved);
+    const int all = a.groups[0] + a.groups[1] + (kWrite ? a.groups[2] : 0);
+    const int64_t units = a.T * a.parts;
+    for (int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+         unit < units; unit += (int64_t)gridDim.x * (kBlock / 64)) {
+        const int64_t t = unit / a.parts;
+        const int part = (int)(unit - t * a.parts);
+        const int first = (int)((int64_t)part * all / a.parts), last = (int)((int64_t)(part + 1) * all / a.parts);
+        float c[4], s[4];
+        double cd[4], sd[4];
+        const int k0 = a.groups[0], v0 = k0 + a.groups[1];
+        if constexpr (kF8) {
+            if (first < v0 && last > k0) {
+                turns(a, p, t, cd, sd);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    c[i] = (float)cd[i], s[i] = (float)sd[i];
+            } else if (first < k0) {
+                turns(a, p, t, c, s);
+            }
+        } else if (first < v0) {
+            turns(a, p, t, c, s);
+        }
+        if (first < k0)
+            walk<T, L>(a, p, t, 0, first, min(last, k0), c, s, [&](int head, bool on, float (&v)[8]) {
+                if (on)
+                    store8_as(a.y_type, a.y[0], t * a.ldy[0] + head * a.D, p.lo, p.hi, v);
+            });
+        if (last <= k0)
+            continue;
+        if constexpr (!kWrite) {
+            walk<T, L>(a, p, t, 1, max(first - k0, 0), last - k0, c, s, [&](int head, bool on, float (&v)[8]) {
+                if (on)
+                    store8_as(a.y_type, a.y[1], t * a.ldy[1] + head * a.D, p.lo, p.hi, v);
+            });
+        } else {
+            const int slot = a.slots[t];
+            if ((uint32_t)slot >= (uint32_t)a.cache.pages << a.cache.log_page)
+                continue;
+            if (first < v0) {
+                const int from = max(first - k0, 0), to = min(last, v0) - k0;
+                if constexpr (kF8)
+                    walk<T, L>(a, p, t, 1, from, to, cd, sd, [&](int head, bool on, double (&v)[8]) {
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            f[i] = sticky(v[i]);
+                        put<L>(a.cache, slot, head, 0, on, p.l, p.lo, p.hi, f);
+                    });
+                else
+                    walk<T, L>(a, p, t, 1, from, to, c, s, [&](int head, bool on, float (&v)[8]) {
+                        put<L>(a.cache, slot, head, 0, on, p.l, p.lo, p.hi, v);
+                    });
+            }
+            if (last > v0)
+                walk<T, L>(a, p, t, 2, max(first - v0, 0), last - v0, c, s, [&](int head, bool on, float (&v)[8]) {
+                    put<L>(a.cache, slot, head, 1, on, p.l, p.lo, p.hi, v);
+                });
+        }
+    }
+}
+
+// The gradient.  With h the output's gradient turned back and n = x r the
+// normed row:  dgain += h n,  dx = r (h gain - n mean(h gain n)).  A lane keeps
+// its eight sums of each gain over all the heads and tokens of its wave; the
+// workgroup leaves one row of sums.
+template <typename T, typename TY, int L>
+__global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
+{
+    const HeadArgs &a = ga.h;
+    const Place p = place<L>(a.D, a.half, a.interleaved);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool normed = a.gain[0] != nullptr;
+    float dg[2][8], gain[2][8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            dg[k][i] = 0.0f, gain[k][i] = 1.0f;
+        if (normed && p.on)
+            load8_as(a.gain_type, a.gain[k], 0, p.lo, p.hi, gain[k]);
+    }
+    const int all = a.groups[0] + a.groups[1];
+    const int64_t units = a.T * a.parts;
+    for (int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + wave; unit < units;
+         unit += (int64_t)gridDim.x * (kBlock / 64)) {
+        const int64_t t = unit / a.parts;
+        const int part = (int)(unit - t * a.parts);
+        const int first = (int)((int64_t)part * all / a.parts), last = (int)((int64_t)(part + 1) * all / a.parts);
+        float c[4], s[4];
+        turns(a, p, t, c, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s[i] = -s[i];
+        auto heads = [&](auto kind, int from, int to) {
+            constexpr int k = decltype(kind)::value;
+            const T *x = static_cast<const T *>(a.x[k]) + t * a.ldx[k];
+            const TY *dy = static_cast<const TY *>(a.y[k]) + t * a.ldy[k];
+            T *dx = static_cast<T *>(ga.g[k]) + t * ga.ldg[k];
+#pragma unroll 2
+            for (int g = from; g < to; ++g) {
+                const int head = g * (64 / L) + p.sub;
+                const bool on = p.on && head < a.heads[k];
+                float v[8], h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = h[i] = 0.0f;
+                if (on) {
+                    load4(dy + head * a.D + p.lo, h);
+                    load4(dy + head * a.D + p.hi, h + 4);
+                    if (normed) {
+                        load4(x + head * a.D + p.lo, v);
+                        load4(x + head * a.D + p.hi, v + 4);
+                    }
+                }
+                turn(p, a.interleaved, c, s, h);
+                if (normed) {
+                    float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        ss += v[i] * v[i];
+                        dot += h[i] * gain[k][i] * v[i];
+                    }
+                    const float r = inverse_root(group_sum<L>(ss) / (float)a.D + a.eps);
+                    const float mean = group_sum<L>(dot) * r / (float)a.D;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float n = v[i] * r;
+                        dg[k][i] += on ? h[i] * n : 0.0f;
+                        h[i] = r * (h[i] * gain[k][i] - n * mean);
+                    }
+                }
+                if (on) {
+                    store4(dx + head * a.D + p.lo, h);
+                    store4(dx + head * a.D + p.hi, h + 4);
+                }
+            }
+        };
+        const int k0 = a.groups[0];
+        if (first < k0)
+            heads(std::integral_constant<int, 0>{}, first, min(last, k0));
+        if (last > k0)
+            heads(std::integral_constant<int, 1>{}, max(first - k0, 0), last - k0);
+    }
+    if (!normed)
+        return;
+    // the heads of a wave, then the waves, in their order
+    __shared__ float sums[kBlock / 64][2][64 / L][8 * L];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (p.on)
+                sums[wave][k][p.sub][(i < 4 ? p.lo : p.hi - 4) + i] = dg[k][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.D; i += kBlock) {
+        const int k = i >= a.D ? 1 : 0, at = i - k * a.D;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kBlock / 64; ++w)
+#pragma unroll
+            for (int j = 0; j < 64 / L; ++j)
+                sum += sums[w][k][j][at];
+        ga.workspace[(int64_t)blockIdx.x * 2 * a.D + i] = sum;
+    }
+}
+
+// The workgroups' rows of sums, 16 columns a workgroup, 16 threads a column.
+__global__ __launch_bounds__(kBlock) void gain_join_kernel(HeadGradArgs ga)
+{
+    __shared__ double sums[16][16];
+    const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+    const int at = blockIdx.x * 16 + col, width = 2 * ga.h.D;
+    double sum = 0.0;
+#pragma unroll 8
+    for (int r = row; r < ga.groups_of_work; r += 16)
+        sum += (double)ga.workspace[(int64_t)r * width + at];
+    sums[row][col] = sum;
+    __syncthreads();
+    if (row == 0) {
+#pragma unroll
+        for (int r = 1; r < 16; ++r)
+            sum += sums[r][col];
+        ga.g_gain[at] = (float)sum;
+    }
+}
+
+template <typename T, int L>
+__global__ __launch_bounds__(kBlock) void kv_write_kernel(KvArgs a)
+{
+    const int64_t vectors = a.T * 2 * a.cache.heads;
+    const int l = threadIdx.x % L;
+    for (int64_t v0 = (int64_t)blockIdx.x * (kBlock / L); v0 < vectors; v0 += (int64_t)gridDim.x * (kBlock / L)) {
+        const int64_t v = v0 + threadIdx.x / L;
+        const int64_t row = v / a.cache.heads, t = row >> 1;
+        const int head = (int)(v - row * a.cache.heads), kv = (int)(row & 1);
+        int slot = -1;
+        if (v < vectors)
+            slot = a.slots[t];
+        const bool on = (uint32_t)slot < (uint32_t)a.cache.pages << a.cache.log_page && 8 * l < a.cache.dim;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = 0.0f;
+        if (on) {
+            const T *from = static_cast<const T *>(kv ? a.v : a.k) + t * (kv ? a.ldv : a.ldk) + head * a.cache.dim + 8 * l;
+            load4(from, x);
+            load4(from + 4, x + 4);
+        }
+        put<L>(a.cache, slot, head, kv, on, l, 8 * l, 8 * l + 4, x);
+    }
+}
+
+template <typename TY, int L>
+__global__ __launch_bounds__(kBlock) void kv_read_kernel(KvArgs a)
+{
+    const int64_t vectors = a.T * 2 * a.cache.heads;
+    const int l = threadIdx.x % L;
+    for (int64_t v = (int64_t)blockIdx.x * (kBlock / L) + threadIdx.x / L; v < vectors;
+         v += (int64_t)gridDim.x * (kBlock / L)) {
+        const int64_t row = v / a.cache.heads, t = row >> 1;
+        const int head = (int)(v - row * a.cache.heads), kv = (int)(row & 1);
+        const int slot = a.slots[t];
+        if (8 * l >= a.cache.dim)
+            continue;
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = 0.0f;
+        if ((uint32_t)slot < (uint32_t)a.cache.pages << a.cache.log_page) {
+            const SlotAt at = slot_at(a.cache, slot, head, kv);
+            if (a.cache.type == QG_F8) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(at.codes + 8 * l);
+                const float scale = f8_scale(*at.scale);
+                float u[16];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t q = i ? w.y : w.x;
+                    u[4 * i] = __builtin_amdgcn_cvt_f32_fp8((int)q, 0);
+                    u[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8((int)q, 1);
+                    u[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8((int)q, 2);
+                    u[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8((int)q, 3);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = u[i] * scale;
+            } else {
+                load8_as(a.cache.type, at.codes, 0, 8 * l, 8 * l + 4, x);
+            }
+        }
+        TY *to = static_cast<TY *>(kv ? a.yv : a.yk) + (t * a.cache.heads + head) * a.cache.dim + 8 * l;
+        store4(to, x);
+        store4(to + 4, x + 4);
+    }
+}
+
+template <typename P>
+hipError_t go(void (*fn)(P), int64_t grid, const P &a, hipStream_t stream)
+{
+    return launch_kernel(reinterpret_cast<const void *>(fn), dim3((unsigned)std::min<int64_t>(grid, kMaxBlocks)),
+                         dim3(kBlock), 0, stream, a);
+}
+
+// fn<T, L> of the element type and of the lanes that a head takes.
+template <typename P, typename Pick>
+hipError_t by_type(int type, int D, Pick pick, int64_t grid, const P &a, hipStream_t stream)
+{
+    auto lanes = [&](auto t) {
+        return D <= 64    ? pick(t, std::integral_constant<int, 8>{})
+               : D <= 128 ? pick(t, std::integral_constant<int, 16>{})
+                          : pick(t, std::integral_constant<int, 32>{});
+    };
+    void (*fn)(P) = type == QG_F32 ? lanes(0.0f) : type == QG_F16 ? lanes(Fp16{}) : lanes(Bf16{});
+    return go(fn, grid, a, stream);
+}
+
+int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
+
+// Groups of heads, and how many waves share a token: as few as give every
+// compute unit its waves, since each takes the token's sines anew.
+void split_heads(HeadArgs &a, int kinds, int64_t waves)
+{
+    const int per = 64 / lanes_of(a.D);
+    int all = 0;
+    for (int i = 0; i < 3; ++i) {
+        a.groups[i] = i < kinds ? (a.heads[i] + per - 1) / per : 0;
+        all += a.groups[i];
+    }
+    a.parts = (int)std::min<int64_t>(all, ceil_div(waves, a.T));
+}
+
+constexpr int64_t kForwardWaves = 8192;
+constexpr int64_t kBackwardWaves = 4096;
+
+int64_t backward_groups(int64_t T, int heads, int D)
+{
+    const int64_t units = std::min<int64_t>(T * ceil_div(heads, 64 / lanes_of(D)), kBackwardWaves);
+    return ceil_div(std::max<int64_t>(units, 1), kBlock / 64);
+}
+
+}  // namespace
+
+hipError_t launch_head_norm_rope(const HeadArgs &args, int x_type, hipStream_t stream)
+{
+    HeadArgs a = args;
+    split_heads(a, 2, kForwardWaves);
+    return by_type(
+        x_type, a.D,
+        [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, false, false>; },
+        ceil_div(a.T * a.parts, kBlock / 64), a, stream);
+}
+
+hipError_t launch_head_norm_rope_write(const HeadArgs &args, int x_type, hipStream_t stream)
+{
+    HeadArgs a = args;
+    split_heads(a, 3, kForwardWaves);
+    const int64_t grid = ceil_div(a.T * a.parts, kBlock / 64);
+    if (a.cache.type == QG_F8)
+        return by_type(
+            x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, true, true>; },
+            grid, a, stream);
+    return by_type(
+        x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, true, false>; }, grid,
+        a, stream);
+}
+
+size_t head_backward_workspace(int64_t T, int heads, int D)
+{
+    return (size_t)backward_groups(T, heads, D) * 2 * D * sizeof(float);
+}
+
+hipError_t launch_head_norm_rope_backward(const HeadGradArgs &args, int x_type, hipStream_t stream)
+{
+    HeadGradArgs a = args;
+    split_heads(a.h, 2, kBackwardWaves);
+    a.groups_of_work = (int)std::min(backward_groups(a.h.T, a.h.heads[0] + a.h.heads[1], a.h.D),
+                                     ceil_div(a.h.T * a.h.parts, kBlock / 64));
+    const hipError_t e = by_type(
+        x_type, a.h.D,
+        [&](auto t, auto l) -> void (*)(HeadGradArgs) {
+            using T = decltype(t);
+            constexpr int L = decltype(l)::value;
+            return a.h.y_type == QG_F32   ? &head_backward_kernel<T, float, L>
+                   : a.h.y_type == QG_F16 ? &head_backward_kernel<T, Fp16, L>
+                                          : &head_backward_kernel<T, Bf16, L>;
+        },
+        a.groups_of_work, a, stream);
+    if (e != hipSuccess || !a.h.gain[0])
+        return e;
+    return go(&gain_join_kernel, a.h.D / 8, a, stream);
+}
+
+hipError_t launch_kv_write(const KvArgs &a, int x_type, hipStream_t stream)
+{
+    return by_type(
+        x_type, a.cache.dim, [](auto t, auto l) { return &kv_write_kernel<decltype(t), decltype(l)::value>; },
+        ceil_div(a.T * 2 * a.cache.heads, kBlock / lanes_of(a.cache.dim)), a, stream);
+}
+
+hipError_t launch_kv_read(const KvArgs &a, int y_type, hipStream_t stream)
+{
+    return by_type(
+        y_type, a.cache.dim, [](auto t, auto l) { return &kv_read_kernel<decltype(t), decltype(l)::value>; },
+        ceil_div(a.T * 2 * a.cache.heads, kBlock / lanes_of(a.cache.dim)), a, stream);
+}
+
+}  // namespace qg
