@@ -107,9 +107,11 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
  *   q: [B][M][q_heads][dim], type q_type (QG_F16 or QG_BF16; the cache's type
  *   where that has 16 bits), tokens ldq elements apart; 1 <= M <= 16,
  *   q_heads a multiple of kv_heads, at most 1024: query heads
- *   j q_heads / kv_heads .. share key head j; 1 <= B <= 65536.
- *   table: int32 [B][width], the pages of a sequence in order; lens: int32
- *   [B], its tokens, the M new ones among them (already written).
+ *   j q_heads / kv_heads .. share key head j; 1 <= B <= 65536, B M q_heads <=
+ *   2^23.
+ *   table: int32 [B][width], the pages of a sequence in order, width * page <=
+ *   2^30; lens: int32 [B], its tokens, the M new ones among them (already
+ *   written).
  * Token i of the M new ones stands at place p = lens[b] - M + i and sees the
  * places max(0, p - window + 1) .. p (window 0: all up to p):
  *   s = scale * q.k,  softcap > 0: s = softcap * tanh(s / softcap),

@@ -17,6 +17,8 @@ constexpr int kAttnMaxHeads = 1024;
 constexpr int kAttnMaxNew = 16;
 constexpr int kAttnMaxBatch = 1 << 16;
 constexpr int kMaxAxes = 4;
+constexpr int64_t kAttnMaxPlaces = 1 << 30;   // of a sequence: a place, a few steps on, fits 31 bits
+constexpr int64_t kAttnMaxRows = 1 << 23;     // query heads of all new tokens: workgroups of a launch
 
 inline bool cache_type_ok(int t) { return t == QG_F8 || t == QG_F16 || t == QG_BF16; }
 inline bool page_ok(int page) { return page >= 16 && page <= 1024 && (page & (page - 1)) == 0; }
@@ -47,6 +49,11 @@ inline KvCache kv_cache(void *data, int64_t pages, int page, int heads, int dim,
     c.type = type;
     return c;
 }
+
+// 8 bytes at any element's alignment.
+struct __attribute__((packed, aligned(2))) Raw8 {
+    uint32_t w[2];
+};
 
 typedef float f2_t __attribute__((ext_vector_type(2)));
 

@@ -22,9 +22,6 @@ constexpr int kBlock = 256;
 constexpr int kMaxBlocks = 1 << 20;
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
-struct __attribute__((packed, aligned(2))) Raw8 {
-    uint32_t w[2];
-};
 struct __attribute__((packed, aligned(4))) Raw16f {
     uint32_t w[4];
 };
