@@ -110,7 +110,7 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
  *   j q_heads / kv_heads .. share key head j; 1 <= B <= 65536, B M q_heads <=
  *   2^23.
  *   table: int32 [B][width], the pages of a sequence in order, width * page <=
- *   2^30; lens: int32 [B], its tokens, the M new ones among them (already
+ *   2^30 and B times that <= 2^36; lens: int32 [B], its tokens, the M new ones among them (already
  *   written).
  * Token i of the M new ones stands at place p = lens[b] - M + i and sees the
  * places max(0, p - window + 1) .. p (window 0: all up to p):
@@ -123,7 +123,8 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
  * 16-bit parts (2^-16 of a weight is lost); one rounding to q_type.
  * workspace: qattn_decode_workspace bytes (0: may be NULL), 16-byte aligned,
  * used by this call only. */
-size_t qattn_decode_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int page, int64_t width);
+size_t qattn_decode_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int cache_type, int page,
+                              int64_t width);
 qg_status qattn_decode(const void *cache, int64_t pages, int page, int kv_heads, int dim, int cache_type,
                        const void *q, int q_type, int64_t ldq, int64_t B, int M, int q_heads, const int32_t *table,
                        int64_t width, const int32_t *lens, float scale, int64_t window, float softcap, void *out,

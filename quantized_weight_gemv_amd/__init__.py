@@ -109,7 +109,7 @@ def lib() -> ctypes.CDLL:
         "qkv_read": (c_int, [vp, i64, c_int, c_int, c_int, c_int, vp, i64, vp, vp, c_int, vp]),
         "qkv_norm_rope_write": (c_int, [vp, i64, c_int, vp, i64, vp, i64, c_int, *turn, i64, vp, vp, i64, c_int, vp,
                                         i64, c_int, c_int, c_int, c_int, vp]),
-        "qattn_decode_workspace": (sz, [i64, c_int, c_int, c_int, c_int, c_int, i64]),
+        "qattn_decode_workspace": (sz, [i64, c_int, c_int, c_int, c_int, c_int, c_int, i64]),
         "qattn_decode": (c_int, [vp, i64, c_int, c_int, c_int, c_int, vp, c_int, i64, i64, c_int, c_int, vp, i64, vp,
                                  f32, i64, f32, vp, vp, vp]),
         "qg_time_next_launch": (None, [vp, vp]),
@@ -927,7 +927,7 @@ def qattn_decode(cache: KVCache, q, table, lens, scale: float | None = None, win
     W = table.shape[1]
     code = _type(q.dtype)
     out, op = c.result(out, tuple(q.shape), q.dtype, "out", B * M * H * D)
-    ws = int(lib().qattn_decode_workspace(B, M, H, cache.heads, D, cache.page, W))
+    ws = int(lib().qattn_decode_workspace(B, M, H, cache.heads, D, args[5], cache.page, W))
     w = c.new((ws,), torch.uint8) if ws else None
     c("qattn_decode", *args, q.data_ptr(), code, ld, B, M, H, c.ptr(table, torch.int32, "table", B * W), W,
       c.ptr(lens, torch.int32, "lens", B), D ** -0.5 if scale is None else scale, window, softcap, op,

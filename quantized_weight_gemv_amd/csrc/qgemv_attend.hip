@@ -2,7 +2,7 @@
 //
 // Rows are the queries that share a key head: row i share + j is new token i of
 // query head j of the group.  One workgroup takes up to 16 kTiles rows of a
-// sequence and key head over a part of the cache ("chunk"), its four waves 32
+// sequence and key head over a part of its cache, its four waves 32
 // tokens each in turn, independently: running maximum, sum and accumulators in
 // registers, joined through LDS at the end, chunks by a second launch.
 //
@@ -20,8 +20,8 @@
 // 8-bit codes are widened as they are (exact); a key's scale multiplies its
 // score, a value's scale its weight.  A weight (fp32) enters the second product
 // as two 16-bit parts, hi = round(p), lo = round(p - hi): 2^-16 of it is lost.
-// bf16 for f8 and bf16 values; with fp16 values fp16, taken times 2^14 so that
-// small weights stay normal.
+// bf16 for f8 and bf16 values; with fp16 values fp16, taken times 2^11 (they
+// reach 2^4) so that small weights stay normal.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -37,9 +37,11 @@ constexpr int kWaves = kBlock / 64;
 constexpr int kStep = 32;                 // tokens of a wave's step
 constexpr int kTile = kStep * kWaves;     // tokens of a workgroup's step
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kSlack = 4.0f;            // weights reach 2^kSlack before they are scaled anew
 
-// Workgroups that the work is cut for, over all sequences and key heads.
-constexpr int kTargetGroups = 1024;
+// Rounds of workgroups over the compute units (256) that the work is cut for.
+constexpr int kUnits = 256;
+constexpr int kRounds = 1;
 
 typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
@@ -55,98 +57,69 @@ __device__ __forceinline__ int scalar_int(const int32_t *p, int64_t i)
     return ((ScalarInts)(uintptr_t)p)[i];
 }
 
-// How the work is cut.  A sequence has `tiles` of kTile tokens from `first`
-// on; chunks hold up to `chunk` of them.
+// How the work is cut.  A sequence has `tiles` of kTile tokens, at least one
+// (its rows are written in any case).  The tiles of all sequences, one after the
+// other, are dealt out in runs of `run` to the workgroups of a key head, so each
+// has the same work whatever the lengths are; a run may end inside a sequence
+// and begin the next one.  Run w's part of sequence b is number w + b of all
+// parts (both only grow along the runs).
 struct Plan {
+    int run, total;
     int b;              // sequence
-    int part, parts;    // chunk of it, of how many
-    int tiles;          // its tiles
-    int first;          // its first token that anybody sees, down to a multiple of 16
-    int len;
-    int base;           // number of its first chunk among all
+    int base;           // its first tile among all
 };
 
-__device__ __forceinline__ int held_length(const AttendArgs &a, int b)
+struct Sequence {
+    int len;
+    int first;          // its first token that anybody sees, down to a multiple of 16
+    int tiles;
+};
+
+__device__ __forceinline__ Sequence sequence(const AttendArgs &a, int b)
 {
     const int64_t most = (int64_t)a.width << a.cache.log_page;
-    return (int)min((int64_t)max(a.lens[b], 0), most);
+    Sequence s;
+    s.len = (int)min((int64_t)max(a.lens[b], 0), most);
+    s.first = a.window ? max(0, s.len - a.M + 1 - a.window) & ~15 : 0;
+    s.tiles = max(1, (s.len - s.first + kTile - 1) / kTile);
+    return s;
 }
 
-__device__ __forceinline__ int first_seen(const AttendArgs &a, int len)
-{
-    return a.window ? max(0, len - a.M + 1 - a.window) & ~15 : 0;
-}
-
-__device__ __forceinline__ int tiles_of(const AttendArgs &a, int len)
-{
-    return (len - first_seen(a, len) + kTile - 1) / kTile;
-}
-
-// Sum over the wave.
-__device__ __forceinline__ int wave_total(int v) { return __builtin_amdgcn_readlane(prefix_sum(v), 63); }
-
-// Tiles a chunk: as many as give the target number of workgroups; every wave
-// finds it by itself from the lengths.
-__device__ __forceinline__ int chunk_tiles(const AttendArgs &a, int target)
+// The length of the runs, from the lengths, by every wave itself, and either
+// the sequence that holds the first tile of run `w` or sequence `w`.
+template <bool kOfRun>
+__device__ __forceinline__ Plan plan(const AttendArgs &a, int target, int w)
 {
     const int lane = threadIdx.x & 63;
-    int64_t total = 0;
+    Plan p{};
+    int mine = 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
-        const int b = b0 + lane;
-        total += wave_total(b < a.B ? tiles_of(a, held_length(a, b)) : 0);
+        mine = b0 + lane < a.B ? sequence(a, b0 + lane).tiles : 0;
+        p.total += __builtin_amdgcn_readlane(prefix_sum(mine), 63);
     }
-    return (int)max((int64_t)1, (total + target - 1) / target);
-}
-
-// A sequence without tokens is one chunk without tiles, so that its rows are
-// written.
-__device__ __forceinline__ int parts_of(int tiles, int chunk) { return max(1, (tiles + chunk - 1) / chunk); }
-
-__device__ __forceinline__ Plan plan_of(const AttendArgs &a, int b, int part, int base, int chunk)
-{
-    Plan p;
-    p.b = b;
-    p.len = held_length(a, b);
-    p.first = first_seen(a, p.len);
-    p.tiles = tiles_of(a, p.len);
-    p.parts = parts_of(p.tiles, chunk);
-    p.part = part;
-    p.base = base;
-    return p;
-}
-
-// The unit-th chunk of all sequences; b = -1 past the last one.
-__device__ __forceinline__ Plan find_chunk(const AttendArgs &a, int unit, int chunk)
-{
-    const int lane = threadIdx.x & 63;
-    int base = 0;
+    p.run = (p.total + target - 1) / target;
+    const int64_t tile = kOfRun ? (int64_t)w * p.run : 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
-        const int b = b0 + lane;
-        const int mine = b < a.B ? parts_of(tiles_of(a, held_length(a, b)), chunk) : 0;
-        const int incl = prefix_sum(mine);
-        const unsigned long long holds = __ballot(base + incl > unit);
-        if (holds) {
-            const int src = __ffsll(holds) - 1;
-            const int before = base + __builtin_amdgcn_readlane(incl - mine, src);
-            return plan_of(a, b0 + src, unit - before, before, chunk);
+        if (a.B > 64)
+            mine = b0 + lane < a.B ? sequence(a, b0 + lane).tiles : 0;
+        const int upto = prefix_sum(mine);
+        if (kOfRun) {
+            const unsigned long long holds = __ballot(p.base + (int64_t)upto > tile);
+            if (holds) {
+                const int at = __ffsll(holds) - 1;
+                p.b = b0 + at;
+                p.base += __builtin_amdgcn_readlane(upto - mine, at);
+                return p;
+            }
+        } else if (w < b0 + 64) {
+            p.b = w;
+            p.base += __builtin_amdgcn_readlane(upto - mine, w - b0);
+            return p;
         }
-        base += __builtin_amdgcn_readlane(incl, 63);
+        p.base += __builtin_amdgcn_readlane(upto, 63);
     }
-    Plan none{};
-    none.b = -1;
-    return none;
-}
-
-// The chunks in front of sequence b.
-__device__ __forceinline__ Plan find_sequence(const AttendArgs &a, int b, int chunk)
-{
-    const int lane = threadIdx.x & 63;
-    int base = 0;
-    for (int b0 = 0; b0 < b; b0 += 64) {
-        const int i = b0 + lane;
-        base += wave_total(i < b ? parts_of(tiles_of(a, held_length(a, i)), chunk) : 0);
-    }
-    return plan_of(a, b, 0, base, chunk);
+    p.b = -1;
+    return p;
 }
 
 // 16-bit arithmetic of a launch: operands of the products and conversions.
@@ -169,24 +142,45 @@ struct Half<Fp16> {
     }
 };
 
-// Four codes of a word as 16-bit values, two words.
+// Four codes of a word times a power of two as 16-bit values, two words.
 template <typename T>
-__device__ __forceinline__ u2_t widen4(uint32_t w)
+__device__ __forceinline__ u2_t widen4(uint32_t w, float scale)
 {
     if constexpr (std::is_same_v<T, Bf16>) {
-        return u2_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))};
+        return u2_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, false)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, true))};
     } else {
-        return u2_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true))};
+        return u2_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, false)),
+                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, true))};
     }
 }
 
 template <typename T>
-__device__ __forceinline__ typename Half<T>::v8 widen8(uint32_t lo, uint32_t hi)
+__device__ __forceinline__ typename Half<T>::v8 widen8(uint32_t lo, uint32_t hi, float scale = 1.0f)
 {
-    const u2_t a = widen4<T>(lo), b = widen4<T>(hi);
+    const u2_t a = widen4<T>(lo, scale), b = widen4<T>(hi, scale);
     return __builtin_bit_cast(typename Half<T>::v8, u4_t{a[0], a[1], b[0], b[1]});
+}
+
+// e of the i-th of four scale bytes.
+__device__ __forceinline__ int exponent_of(uint32_t bytes, int i) { return (int)((bytes >> (8 * i)) & 255u) - 127; }
+
+// Words of the cache, each read once by one workgroup: loads that leave nothing
+// behind in the caches stream at 6.8 TB/s where ordinary ones reach 5.9 (541 MB
+// in pages of 64 tokens, loads alone).  They have to take whole lines, or the
+// other half is read again.
+template <int kWords>
+__device__ __forceinline__ void load_once(const uint8_t *from, uint32_t *to)
+{
+    constexpr int kN = kWords % 4 == 0 ? 4 : kWords % 3 == 0 ? 3 : kWords % 2 == 0 ? 2 : 1;
+    typedef uint32_t piece __attribute__((ext_vector_type(kN), aligned(4 * (kN == 3 ? 1 : kN))));
+#pragma unroll
+    for (int i = 0; i < kWords; i += kN) {
+        const piece p = __builtin_nontemporal_load(reinterpret_cast<const piece *>(from + 4 * i));
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+            to[i + j] = p[j];
+    }
 }
 
 // 4 x 4 bytes turned: word i of the result has byte i of the four words.
@@ -225,8 +219,21 @@ __device__ __forceinline__ float sum_over_groups(float v)
     return p[0] + p[1];
 }
 
-// Where a chunk's sums go if its sequence has others: accumulators [chunk][key
-// head][row][D], then (maximum, sum) [chunk][key head][row].
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = group_max<32>(v);
+    const f2_t p = pair32(v);
+    return fmaxf(p[0], p[1]);
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v = group_sum<32>(v);
+    const f2_t p = pair32(v);
+    return p[0] + p[1];
+}
+
+// Where the sums of a part go if its sequence has others: accumulators
+// [part][key head][row][D], then (maximum, sum) [part][key head][row].
 struct Parts {
     float *o;
     float *ml;
@@ -239,17 +246,27 @@ __host__ __device__ inline Parts parts_at(void *workspace, int64_t units, int he
     return p;
 }
 
+// Workgroups that a compute unit holds at once (a wave of each on every SIMD).
+constexpr int resident(int D, bool f8, int tiles)
+{
+    if (tiles == 1)
+        return D == 64 ? 4 : D == 128 ? (f8 ? 3 : 2) : D == 192 ? 2 : f8 ? 2 : 1;
+    if (tiles == 2)
+        return D == 64 ? 3 : D == 128 ? 2 : 1;
+    return 1;
+}
+
 struct AttendLaunch {
     AttendArgs a;
-    int target;     // chunks to cut for, per key head and row group
-    int units;      // chunks at most
+    int target;     // runs, at most, for each key head and row group
+    int units;      // parts, at most
     int rows;       // M share
     int row_groups;
 };
 
 // TQ: type of q, of the output and of 16-bit caches; kF8: an 8-bit cache.
 template <typename TQ, bool kF8, int D, int kTiles>
-__global__ __launch_bounds__(kBlock) void attend_kernel(AttendLaunch la)
+__global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kernel(AttendLaunch la)
 {
     using TV = std::conditional_t<kF8, Bf16, TQ>;   // of the second product
     using Q = Half<TQ>;
@@ -260,7 +277,10 @@ __global__ __launch_bounds__(kBlock) void attend_kernel(AttendLaunch la)
     constexpr int kOut = D / 16;            // accumulator tiles, consecutive dimensions of a lane
     constexpr int kKeyLoads = kRow / 64;    // 16-byte loads of a tile of 16 tokens
     constexpr int kValWords = kOut * kItem / 4;
-    constexpr float kWeight = std::is_same_v<TV, Fp16> ? 16384.0f : 1.0f;
+    constexpr bool kWholeLines = kRow % 128 == 0;
+    // a key's scale: bf16 takes it with the widening, exactly; fp16 has not the range, the score takes it there
+    constexpr bool kScaledKeys = kF8 && std::is_same_v<TQ, Bf16>;
+    constexpr float kWeight = std::is_same_v<TV, Fp16> ? 2048.0f : 1.0f;
 
     const AttendArgs &a = la.a;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -268,358 +288,394 @@ __global__ __launch_bounds__(kBlock) void attend_kernel(AttendLaunch la)
     const int heads = a.cache.heads;
     const int head = blockIdx.x % heads;
     const int group = (blockIdx.x / heads) % la.row_groups;
-    const int unit = blockIdx.x / (heads * la.row_groups);
-    const int chunk = chunk_tiles(a, la.target);
-    const Plan p = find_chunk(a, unit, chunk);
+    const int run = blockIdx.x / (heads * la.row_groups);
+    Plan p = plan<true>(a, la.target, run);
     if (p.b < 0)
         return;
-    // the tiles of this chunk, even among the chunks of the sequence
-    const int t0 = (int)((int64_t)p.part * p.tiles / p.parts), t1 = (int)((int64_t)(p.part + 1) * p.tiles / p.parts);
-
-    // queries: row r is column r of the first product
-    typename Q::v8 q[kTiles][kSteps];
-    int mine[kTiles];                       // the row's new token
+    const int run_end = min((run + 1) * p.run, p.total);
     const int row0 = group * 16 * kTiles;
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-        const int row = row0 + 16 * n + r16;
-        const int i = min(row / a.share, a.M - 1);
-        mine[n] = i;
-        const TQ *from = static_cast<const TQ *>(a.q) + ((int64_t)p.b * a.M + i) * a.ldq +
-                         ((int64_t)head * a.share + row % a.share) * D;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int d = kF8 ? 64 * (s / 2) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
-            Raw16 w{};
-            if (row < la.rows)
-                w = *reinterpret_cast<const Raw16 *>(from + d);
-            q[n][s] = __builtin_bit_cast(typename Q::v8, w);
-        }
-    }
+    __shared__ float o[kWaves][16][D + 4];
+    __shared__ float ml[kWaves][16][2];
 
-    const int64_t head_at = (int64_t)head * 2 * a.cache.page * kRow;
-    const int64_t scale_at = a.cache.scales + (int64_t)head * 2 * a.cache.page;
-    const int last_page = a.width - 1;
-    auto page_of = [&](int token) {
-        return scalar_int(a.table, (int64_t)p.b * a.width + min(token >> a.cache.log_page, last_page));
-    };
-    // a tile's page, and whether there is one
-    struct Where {
-        const uint8_t *keys, *scales;
-        bool there;
-    };
-    auto where = [&](int page, int token) {
-        Where w;
-        w.there = (uint32_t)page < (uint32_t)a.cache.pages;
-        const uint8_t *base = a.cache.data + (int64_t)(w.there ? page : 0) * a.cache.page_bytes;
-        const int in = token & (a.cache.page - 1);
-        w.keys = base + head_at + (int64_t)in * kRow;
-        w.scales = base + scale_at + in;
-        return w;
-    };
-    const int64_t values = (int64_t)a.cache.page * kRow;
+    // one sequence's part of the run after the other
+    for (int tile = run * p.run;;) {
+        const Sequence seq = sequence(a, p.b);
+        const int t0 = tile - p.base, t1 = min(seq.tiles, run_end - p.base);
 
-    u4_t kw[2][kKeyLoads];
-    uint32_t vw[8][kValWords];
-    uint32_t ks[2], vs[2];
-    auto load_keys = [&](const Where (&w)[2]) {
+        // queries: row r is column r of the first product
+        typename Q::v8 q[kTiles][kSteps];
+        int mine[kTiles];                       // the row's new token
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int n = 0; n < kTiles; ++n) {
+            const int row = row0 + 16 * n + r16;
+            const int i = min(row / a.share, a.M - 1);
+            mine[n] = i;
+            const TQ *from = static_cast<const TQ *>(a.q) + ((int64_t)p.b * a.M + i) * a.ldq +
+                             ((int64_t)head * a.share + row % a.share) * D;
 #pragma unroll
-            for (int c = 0; c < kKeyLoads; ++c)
-                kw[h][c] = *reinterpret_cast<const u4_t *>(w[h].keys + (r16 * kRow + 64 * c + 16 * g));
-            if constexpr (kF8)
-                ks[h] = *reinterpret_cast<const uint32_t *>(w[h].scales + 4 * g);
-        }
-    };
-    auto load_values = [&](const Where (&w)[2]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t *from = reinterpret_cast<const uint32_t *>(
-                    w[h].keys + values + ((4 * g + j) * kRow + r16 * (4 * kValWords)));
-                __builtin_memcpy(vw[4 * h + j], __builtin_assume_aligned(from, kValWords % 4 == 0 ? 16 : kValWords % 2 == 0 ? 8 : 4),
-                                 4 * kValWords);
+            for (int s = 0; s < kSteps; ++s) {
+                const int d = kF8 ? 64 * (s / 2) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g;
+                Raw16 w{};
+                if (row < la.rows)
+                    w = *reinterpret_cast<const Raw16 *>(from + d);
+                q[n][s] = __builtin_bit_cast(typename Q::v8, w);
             }
-            if constexpr (kF8)
-                vs[h] = *reinterpret_cast<const uint32_t *>(w[h].scales + a.cache.page + 4 * g);
         }
-    };
 
-    f4_t acc[kTiles][kOut];
-    float top[kTiles], sum[kTiles];
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-        top[n] = -__builtin_inff();
-        sum[n] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < kOut; ++d)
-            acc[n][d] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+        const int64_t head_at = (int64_t)head * 2 * a.cache.page * kRow;
+        const int64_t scale_at = a.cache.scales + (int64_t)head * 2 * a.cache.page;
+        const int last_page = a.width - 1;
+        auto page_of = [&](int token) {
+            return scalar_int(a.table, (int64_t)p.b * a.width + min(token >> a.cache.log_page, last_page));
+        };
+        // a tile's page, and whether there is one
+        struct Where {
+            const uint8_t *keys, *scales;
+            bool there;
+        };
+        auto where = [&](int page, int token) {
+            Where w;
+            w.there = (uint32_t)page < (uint32_t)a.cache.pages;
+            const uint8_t *base = a.cache.data + (int64_t)(w.there ? page : 0) * a.cache.page_bytes;
+            const int in = token & (a.cache.page - 1);
+            w.keys = base + head_at + (int64_t)in * kRow;
+            w.scales = base + scale_at + in;
+            return w;
+        };
+        const int64_t values = (int64_t)a.cache.page * kRow;
 
-    auto add = [&](const typename V::v8 &v, const typename V::v8 (&hi)[kTiles], const typename V::v8 (&lo)[kTiles], int d) {
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-            acc[n][d] = V::mfma(v, lo[n], V::mfma(v, hi[n], acc[n][d]));
-    };
-
-    // places that every row sees: from all_from on, below all_end
-    const int all_end = p.len - a.M + 1;
-    const int all_from = a.window ? max(0, p.len - a.window) : 0;
-    const int any_from = a.window ? max(0, all_end - a.window) : 0;
-    const float scale = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
-    const float cap = a.softcap * kLog2e;
-
-    auto edge = [&](int at) { return at + kStep > all_end || at < all_from; };
-    bool left_out = false;   // values that are not finite, of places that some rows do not see
-
-    const int first = p.first + t0 * kTile + wave * kStep;
-    int token = first;
-    const int end = min(p.first + t1 * kTile, p.len);
-    if (token < end) {
-        // pages a step ahead of the loads, loads a half step ahead of their products
-        int page[2] = {page_of(token), page_of(token + 16)};
-        Where now[2] = {where(page[0], token), where(page[1], token + 16)};
-        load_keys(now);
-        load_values(now);
-        int ahead = token + kTile < end ? token + kTile : token;
-        page[0] = page_of(ahead), page[1] = page_of(ahead + 16);
-        for (;;) {
-            const bool there[2] = {now[0].there, now[1].there};
-            // scores
-            float s[kTiles][8];
+        uint32_t kw[2][kKeyLoads][4];
+        uint32_t vw[8][kValWords];
+        uint32_t ks[2], vs[2];
+        // Loads stay where they are written: one moved behind the values' loads would be waited for with all of them.
+        auto keep_order = [] {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto load_keys = [&](const Where (&w)[2]) {
+            keep_order();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                f4_t c[kTiles];
-#pragma unroll
-                for (int n = 0; n < kTiles; ++n)
-                    c[n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int st = 0; st < kSteps; ++st) {
-                    typename Q::v8 k;
-                    if constexpr (kF8) {
-                        const u4_t w = kw[h][st / 2];
-                        k = (st & 1) ? widen8<TQ>(w[2], w[3]) : widen8<TQ>(w[0], w[1]);
-                    } else {
-                        k = __builtin_bit_cast(typename Q::v8, kw[h][st]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < kTiles; ++n)
-                        c[n] = Q::mfma(k, q[n][st], c[n]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f = scale;
-                    if constexpr (kF8)
-                        f *= f8_scale((ks[h] >> (8 * i)) & 255u);
-#pragma unroll
-                    for (int n = 0; n < kTiles; ++n)
-                        s[n][4 * h + i] = c[n][i] * f;
-                }
+                if constexpr (kScaledKeys)
+                    ks[h] = w[h].scales[r16];
+                else if constexpr (kF8)
+                    ks[h] = *reinterpret_cast<const uint32_t *>(w[h].scales + 4 * g);
             }
-            // the next step's keys
-            now[0] = where(page[0], ahead), now[1] = where(page[1], ahead + 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int c = 0; c < kKeyLoads; ++c) {
+                    const int at = kWholeLines ? ((r16 & 7) + 8 * (c & 1)) * kRow + 128 * (c / 2) + 64 * (r16 >> 3) + 16 * g
+                                               : r16 * kRow + 64 * c + 16 * g;
+                    load_once<4>(w[h].keys + at, kw[h][c]);
+                }
+            keep_order();
+        };
+        // Lines to rows: lane r16 has half r16 / 8 of tokens r16 % 8 and 8 + r16 % 8, and wants both halves of token r16.
+        auto key_rows = [&](int h) {
+            if constexpr (kWholeLines) {
+#pragma unroll
+                for (int c = 0; c < kKeyLoads; c += 2)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int low = (int)kw[h][c][i], high = (int)kw[h][c + 1][i];
+                        kw[h][c][i] = (uint32_t)__builtin_amdgcn_update_dpp(low, high, 0x128, 0xF, 0xC, false);
+                        kw[h][c + 1][i] = (uint32_t)__builtin_amdgcn_update_dpp(high, low, 0x128, 0xF, 0x3, false);
+                    }
+            }
+        };
+        auto load_values = [&](const Where (&w)[2]) {
+            keep_order();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if constexpr (kF8)
+                    vs[h] = *reinterpret_cast<const uint32_t *>(w[h].scales + a.cache.page + 4 * g);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    load_once<kValWords>(w[h].keys + values + ((4 * g + j) * kRow + r16 * (4 * kValWords)), vw[4 * h + j]);
+            keep_order();
+        };
+
+        f4_t acc[kTiles][kOut];
+        float top[kTiles], sum[kTiles];
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            top[n] = -__builtin_inff();
+            sum[n] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < kOut; ++d)
+                acc[n][d] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+
+        auto add = [&](const typename V::v8 &v, const typename V::v8 (&hi)[kTiles], const typename V::v8 (&lo)[kTiles], int d) {
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n)
+                acc[n][d] = V::mfma(v, lo[n], V::mfma(v, hi[n], acc[n][d]));
+        };
+
+        // places that every row sees: from all_from on, below all_end
+        const int all_end = seq.len - a.M + 1;
+        const int all_from = a.window ? max(0, seq.len - a.window) : 0;
+        const int any_from = a.window ? max(0, all_end - a.window) : 0;
+        const float scale = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
+        const float cap = a.softcap * kLog2e;
+
+        auto edge = [&](int at) { return at + kStep > all_end || at < all_from; };
+        bool left_out = false;   // values that are not finite, of places that some rows do not see
+
+        const int first = seq.first + t0 * kTile + wave * kStep;
+        int token = first;
+        const int end = min(seq.first + t1 * kTile, seq.len);
+        if (token < end) {
+            // pages a step ahead of the loads, loads a half step ahead of their products
+            int page[2] = {page_of(token), page_of(token + 16)};
+            Where now[2] = {where(page[0], token), where(page[1], token + 16)};
             load_keys(now);
-            if (a.softcap > 0.0f) {
+            load_values(now);
+            int ahead = token + kTile < end ? token + kTile : token;
+            page[0] = page_of(ahead), page[1] = page_of(ahead + 16);
+            for (;;) {
+                const bool there[2] = {now[0].there, now[1].there};
+                // scores
+                float s[kTiles][8];
 #pragma unroll
-                for (int n = 0; n < kTiles; ++n)
+                for (int h = 0; h < 2; ++h) {
+                    key_rows(h);
+                    f4_t c[kTiles];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)   // cap tanh(x) log2 e, from e^2x
-                        s[n][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[n][i] * (2.0f * kLog2e)));
-            }
-            if (edge(token) || !there[0] || !there[1]) {
+                    for (int n = 0; n < kTiles; ++n)
+                        c[n] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int at = token + 16 * (i / 4) + 4 * g + (i & 3);
-                    const bool is = there[i / 4];
+                    for (int st = 0; st < kSteps; ++st) {
+                        typename Q::v8 k;
+                        if constexpr (kF8) {
+                            const uint32_t (&w)[4] = kw[h][st / 2];
+                            const float to = kScaledKeys ? f8_exponent(ks[h]) : 1.0f;
+                            k = (st & 1) ? widen8<TQ>(w[2], w[3], to) : widen8<TQ>(w[0], w[1], to);
+                        } else {
+                            k = __builtin_bit_cast(typename Q::v8, kw[h][st]);
+                        }
 #pragma unroll
-                    for (int n = 0; n < kTiles; ++n) {
-                        const int stop = p.len - a.M + 1 + mine[n], start = a.window ? stop - a.window : 0;
-                        if (!is || at >= stop || at < start)
-                            s[n][i] = -__builtin_inff();
+                        for (int n = 0; n < kTiles; ++n)
+                            c[n] = Q::mfma(k, q[n][st], c[n]);
                     }
-                    const bool seen = is && at < p.len && at >= any_from;
 #pragma unroll
-                    for (int c = 0; c < kValWords; ++c) {
-                        if (!seen)
-                            vw[i][c] = 0;
-                        // 0 times what is not finite is not 0: what some rows see and others do not comes afterwards
-                        const uint32_t odd = not_finite<TQ, kF8>(vw[i][c]);
-                        if (a.M > 1 && odd) {
-                            vw[i][c] &= ~odd;
-                            left_out = true;
+                    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                        for (int n = 0; n < kTiles; ++n) {
+                            s[n][4 * h + i] = c[n][i] * scale;
+                            if constexpr (kF8 && !kScaledKeys)
+                                s[n][4 * h + i] = ldexpf(s[n][4 * h + i], exponent_of(ks[h], i));
                         }
                     }
                 }
-            }
-            // softmax
-            typename V::v8 hi[kTiles], lo[kTiles];
+                // the next step's keys
+                now[0] = where(page[0], ahead), now[1] = where(page[1], ahead + 16);
+                load_keys(now);
+                if (a.softcap > 0.0f) {
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n) {
-                float m = top[n];
+                    for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    m = fmaxf(m, s[n][i]);
-                m = max_over_groups(m);
-                if (__any(m > top[n])) {
-                    const float old = __builtin_amdgcn_exp2f(top[n] - (m == -__builtin_inff() ? 0.0f : m));
-                    sum[n] *= old;
-#pragma unroll
-                    for (int d = 0; d < kOut; ++d)
-                        acc[n][d] *= old;
-                    top[n] = m;
+                        for (int i = 0; i < 8; ++i)   // cap tanh(x) log2 e, from e^2x
+                            s[n][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[n][i] * (2.0f * kLog2e)));
                 }
-                const float from = m == -__builtin_inff() ? 0.0f : m;
-                float w[8];
+                if (edge(token) || !there[0] || !there[1]) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(s[n][i] - from);
-                    sum[n] += e;
-                    w[i] = e * kWeight;
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = token + 16 * (i / 4) + 4 * g + (i & 3);
+                        const bool is = there[i / 4];
+#pragma unroll
+                        for (int n = 0; n < kTiles; ++n) {
+                            const int stop = seq.len - a.M + 1 + mine[n], start = a.window ? stop - a.window : 0;
+                            if (!is || at >= stop || at < start)
+                                s[n][i] = -__builtin_inff();
+                        }
+                        const bool seen = is && at < seq.len && at >= any_from;
+#pragma unroll
+                        for (int c = 0; c < kValWords; ++c) {
+                            if (!seen)
+                                vw[i][c] = 0;
+                            // 0 times what is not finite is not 0: what some rows see and others do not comes afterwards
+                            const uint32_t odd = not_finite<TQ, kF8>(vw[i][c]);
+                            if (a.M > 1 && odd) {
+                                vw[i][c] &= ~odd;
+                                left_out = true;
+                            }
+                        }
+                    }
+                }
+                // softmax
+                typename V::v8 hi[kTiles], lo[kTiles];
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n) {
+                    float m = top[n];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        m = fmaxf(m, s[n][i]);
+                    m = max_over_groups(m);
+                    // weights up to 2^kSlack are as good as up to 1: the sums are scaled anew only beyond
+                    if (__any(m > top[n] + kSlack)) {
+                        const float old = __builtin_amdgcn_exp2f(top[n] - (m == -__builtin_inff() ? 0.0f : m));
+                        sum[n] *= old;
+#pragma unroll
+                        for (int d = 0; d < kOut; ++d)
+                            acc[n][d] *= old;
+                        top[n] = m;
+                    }
+                    const float from = top[n] == -__builtin_inff() ? 0.0f : top[n];
+                    float w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float e = __builtin_amdgcn_exp2f(s[n][i] - from);
+                        sum[n] += e;
+                        w[i] = e * kWeight;
+                        if constexpr (kF8)   // (of 0 too: the scale of a place without a token may be anything)
+                            w[i] = ldexpf(e, exponent_of(vs[i / 4], i & 3));
+                    }
+                    u4_t h4, l4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h4[i] = pack2<TV>(w[2 * i], w[2 * i + 1]);
+                        const float a0 = to_f32(TV{(uint16_t)h4[i]}), a1 = to_f32(TV{(uint16_t)(h4[i] >> 16)});
+                        l4[i] = pack2<TV>(w[2 * i] - a0, w[2 * i + 1] - a1);
+                    }
+                    hi[n] = __builtin_bit_cast(typename V::v8, h4);
+                    lo[n] = __builtin_bit_cast(typename V::v8, l4);
+                }
+#pragma unroll
+                for (int c = 0; c < kValWords; ++c) {
                     if constexpr (kF8) {
-                        const float f = f8_scale((vs[i / 4] >> (8 * (i & 3))) & 255u);
-                        w[i] = e == 0.0f ? 0.0f : e * f;   // (the scale of a place without a token may be anything)
+                        const u4_t x = turn4(vw[0][c], vw[1][c], vw[2][c], vw[3][c]);
+                        const u4_t y = turn4(vw[4][c], vw[5][c], vw[6][c], vw[7][c]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            add(widen8<TV>(x[i], y[i]), hi, lo, 4 * c + i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t half = i ? 0x07060302 : 0x05040100;
+                            add(__builtin_bit_cast(typename V::v8, u4_t{__builtin_amdgcn_perm(vw[1][c], vw[0][c], half),
+                                                                        __builtin_amdgcn_perm(vw[3][c], vw[2][c], half),
+                                                                        __builtin_amdgcn_perm(vw[5][c], vw[4][c], half),
+                                                                        __builtin_amdgcn_perm(vw[7][c], vw[6][c], half)}),
+                                hi, lo, 2 * c + i);
+                        }
                     }
                 }
-                u4_t h4, l4;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h4[i] = pack2<TV>(w[2 * i], w[2 * i + 1]);
-                    const float a0 = to_f32(TV{(uint16_t)h4[i]}), a1 = to_f32(TV{(uint16_t)(h4[i] >> 16)});
-                    l4[i] = pack2<TV>(w[2 * i] - a0, w[2 * i + 1] - a1);
-                }
-                hi[n] = __builtin_bit_cast(typename V::v8, h4);
-                lo[n] = __builtin_bit_cast(typename V::v8, l4);
+                load_values(now);
+                token += kTile;
+                if (token >= end)
+                    break;
+                ahead = token + kTile < end ? token + kTile : token;
+                page[0] = page_of(ahead), page[1] = page_of(ahead + 16);
             }
-#pragma unroll
-            for (int c = 0; c < kValWords; ++c) {
-                if constexpr (kF8) {
-                    const u4_t x = turn4(vw[0][c], vw[1][c], vw[2][c], vw[3][c]);
-                    const u4_t y = turn4(vw[4][c], vw[5][c], vw[6][c], vw[7][c]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        add(widen8<TV>(x[i], y[i]), hi, lo, 4 * c + i);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t half = i ? 0x07060302 : 0x05040100;
-                        add(__builtin_bit_cast(typename V::v8, u4_t{__builtin_amdgcn_perm(vw[1][c], vw[0][c], half),
-                                                                    __builtin_amdgcn_perm(vw[3][c], vw[2][c], half),
-                                                                    __builtin_amdgcn_perm(vw[5][c], vw[4][c], half),
-                                                                    __builtin_amdgcn_perm(vw[7][c], vw[6][c], half)}),
-                            hi, lo, 2 * c + i);
-                    }
-                }
-            }
-            load_values(now);
-            token += kTile;
-            if (token >= end)
-                break;
-            ahead = token + kTile < end ? token + kTile : token;
-            page[0] = page_of(ahead), page[1] = page_of(ahead + 16);
         }
-    }
 
-    // What was left out reaches the rows that see its place: infinities and NaNs of the values themselves (weights
-    // are positive).
-    if (__any(left_out)) {
+        // What was left out reaches the rows that see its place: infinities and NaNs of the values themselves (weights
+        // are positive).
+        if (__any(left_out)) {
 #pragma unroll 1
-        for (int at = first; at < end; at += kTile) {
-            if (!edge(at) && (uint32_t)page_of(at) < (uint32_t)a.cache.pages &&
-                (uint32_t)page_of(at + 16) < (uint32_t)a.cache.pages)
-                continue;
-#pragma unroll 1
-            for (int t = at; t < min(at + kStep, p.len); ++t) {
-                const Where w = where(page_of(t), t);
-                if (!w.there)
+            for (int at = first; at < end; at += kTile) {
+                if (!edge(at) && (uint32_t)page_of(at) < (uint32_t)a.cache.pages &&
+                    (uint32_t)page_of(at + 16) < (uint32_t)a.cache.pages)
                     continue;
+#pragma unroll 1
+                for (int t = at; t < min(at + kStep, seq.len); ++t) {
+                    const Where w = where(page_of(t), t);
+                    if (!w.there)
+                        continue;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t *from = reinterpret_cast<const uint32_t *>(w.keys + values + (4 * g + e) * (4 * kValWords));
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t *from = reinterpret_cast<const uint32_t *>(w.keys + values + (4 * g + e) * (4 * kValWords));
 #pragma unroll
-                    for (int c = 0; c < kValWords; ++c) {
-                        const uint32_t word = from[c] & not_finite<TQ, kF8>(from[c]);
+                        for (int c = 0; c < kValWords; ++c) {
+                            const uint32_t word = from[c] & not_finite<TQ, kF8>(from[c]);
 #pragma unroll
-                        for (int i = 0; i < 4 / kItem; ++i) {
-                            float v;
-                            if constexpr (kF8)
-                                v = ((word >> (8 * i)) & 255u) ? __builtin_nanf("") : 0.0f;
-                            else
-                                v = to_f32(TQ{(uint16_t)(word >> (16 * i))});
+                            for (int i = 0; i < 4 / kItem; ++i) {
+                                float v;
+                                if constexpr (kF8)
+                                    v = ((word >> (8 * i)) & 255u) ? __builtin_nanf("") : 0.0f;
+                                else
+                                    v = to_f32(TQ{(uint16_t)(word >> (16 * i))});
 #pragma unroll
-                            for (int n = 0; n < kTiles; ++n) {
-                                const int stop = all_end + mine[n], start = a.window ? stop - a.window : 0;
-                                acc[n][4 / kItem * c + i][e] += t < stop && t >= start ? v : 0.0f;
+                                for (int n = 0; n < kTiles; ++n) {
+                                    const int stop = all_end + mine[n], start = a.window ? stop - a.window : 0;
+                                    acc[n][4 / kItem * c + i][e] += t < stop && t >= start ? v : 0.0f;
+                                }
                             }
                         }
                     }
                 }
             }
         }
-    }
 
-    // the waves' sums, one tile of rows after the other
-    __shared__ float o[kWaves][16][D + 4];
-    __shared__ float ml[kWaves][16][2];
-    const Parts parts = parts_at(a.workspace, la.units, heads, la.rows, D);
+        // the waves' sums, one tile of rows after the other
+        const bool whole = p.base / p.run == (p.base + seq.tiles - 1) / p.run;   // the sequence is in this run alone
+        const Parts parts = parts_at(a.workspace, la.units, heads, la.rows, D);
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-        const float l = sum_over_groups(sum[n]);
-        if (n > 0)
+        for (int n = 0; n < kTiles; ++n) {
+            const float l = sum_over_groups(sum[n]);
+            __syncthreads();   // (the last tile's or sequence's readers)
+            if (g == 0)
+                ml[wave][r16][0] = top[n], ml[wave][r16][1] = l;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int d = 0; d < kOut; d += 4)
+                    *reinterpret_cast<f4_t *>(&o[wave][r16][(4 * g + e) * kOut + d]) =
+                        f4_t{acc[n][d][e], acc[n][d + 1][e], acc[n][d + 2][e], acc[n][d + 3][e]};
             __syncthreads();
-        if (g == 0)
-            ml[wave][r16][0] = top[n], ml[wave][r16][1] = l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int d = 0; d < kOut; d += 4)
-                *reinterpret_cast<f4_t *>(&o[wave][r16][(4 * g + e) * kOut + d]) =
-                    f4_t{acc[n][d][e], acc[n][d + 1][e], acc[n][d + 2][e], acc[n][d + 3][e]};
-        __syncthreads();
-        const int r = threadIdx.x >> 4, row = row0 + 16 * n + r;
-        if (row >= la.rows)
-            continue;
-        float m = -__builtin_inff(), total = 0.0f, weight[kWaves];
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            m = fmaxf(m, ml[w][r][0]);
-        const float from = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            weight[w] = __builtin_amdgcn_exp2f(ml[w][r][0] - from);
-            total += ml[w][r][1] * weight[w];
-        }
-        const int64_t part_row = ((int64_t)unit * heads + head) * la.rows + row;
-        const int i = row / a.share;
-        TQ *out = static_cast<TQ *>(a.out) +
-                  (((int64_t)p.b * a.M + i) * heads + head) * a.share * D + (int64_t)(row % a.share) * D;
-        const float inverse = total == 0.0f ? 0.0f : 1.0f / (total * kWeight);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const int d = 64 * c + 4 * (threadIdx.x & 15);
-            f4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+            const int r = threadIdx.x >> 4, row = row0 + 16 * n + r;
+            if (row >= la.rows)
+                continue;
+            float m = -__builtin_inff(), total = 0.0f, weight[kWaves];
 #pragma unroll
             for (int w = 0; w < kWaves; ++w)
-                v += *reinterpret_cast<const f4_t *>(&o[w][r][d]) * weight[w];
-            if (p.parts == 1) {
-                if (total == 0.0f)
-                    v = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-                v *= inverse;
-                *reinterpret_cast<Raw8 *>(out + d) = Raw8{pack2<TQ>(v[0], v[1]), pack2<TQ>(v[2], v[3])};
-            } else {
-                *reinterpret_cast<f4_t *>(parts.o + part_row * D + d) = v * (1.0f / kWeight);
+                m = fmaxf(m, ml[w][r][0]);
+            const float from = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                weight[w] = __builtin_amdgcn_exp2f(ml[w][r][0] - from);
+                total += ml[w][r][1] * weight[w];
+            }
+            const int64_t part_row = ((int64_t)(run + p.b) * heads + head) * la.rows + row;
+            const int i = row / a.share;
+            TQ *out = static_cast<TQ *>(a.out) +
+                      (((int64_t)p.b * a.M + i) * heads + head) * a.share * D + (int64_t)(row % a.share) * D;
+            const float inverse = total == 0.0f ? 0.0f : 1.0f / (total * kWeight);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const int d = 64 * c + 4 * (threadIdx.x & 15);
+                f4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w)
+                    v += *reinterpret_cast<const f4_t *>(&o[w][r][d]) * weight[w];
+                if (whole) {
+                    if (total == 0.0f)
+                        v = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                    v *= inverse;
+                    *reinterpret_cast<Raw8 *>(out + d) = Raw8{pack2<TQ>(v[0], v[1]), pack2<TQ>(v[2], v[3])};
+                } else {
+                    *reinterpret_cast<f4_t *>(parts.o + part_row * D + d) = v * (1.0f / kWeight);
+                }
+            }
+            if (!whole && (threadIdx.x & 15) == 0) {
+                parts.ml[2 * part_row] = m;
+                parts.ml[2 * part_row + 1] = total;
             }
         }
-        if (p.parts > 1 && (threadIdx.x & 15) == 0) {
-            parts.ml[2 * part_row] = m;
-            parts.ml[2 * part_row + 1] = total;
-        }
+        tile = p.base + t1;
+        if (tile >= run_end)
+            break;
+        p.base += seq.tiles;
+        ++p.b;
     }
 }
 
-// Joins the chunks of a row: a workgroup per row of a sequence and key head,
-// 16-byte pieces of D in consecutive threads, the chunks over the rest.
+// Joins the parts of a row: a workgroup per row of a sequence and key head,
+// 16-byte pieces of D in consecutive threads, the parts over the rest.
 template <typename TQ, int D>
 __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
 {
@@ -627,47 +683,49 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
     const AttendArgs &a = la.a;
     const int heads = a.cache.heads;
     const int row = blockIdx.x % la.rows, head = (blockIdx.x / la.rows) % heads, b = blockIdx.x / (la.rows * heads);
-    const int chunk = chunk_tiles(a, la.target);
-    const Plan p = find_sequence(a, b, chunk);
-    if (p.parts == 1)
+    const Plan p = plan<false>(a, la.target, b);
+    const int from_run = p.base / p.run, n = (p.base + sequence(a, b).tiles - 1) / p.run - from_run + 1;
+    if (n == 1)
         return;
     const Parts parts = parts_at(a.workspace, la.units, heads, la.rows, D);
-    const int64_t stride = (int64_t)heads * la.rows, at0 = (int64_t)p.base * stride + (int64_t)head * la.rows + row;
-    __shared__ float o[kRows][D], ml[kRows][2];
+    const int64_t stride = (int64_t)heads * la.rows;
+    const int64_t at0 = (int64_t)(from_run + b) * stride + (int64_t)head * la.rows + row;
+    __shared__ float o[kRows][D], ml[2][kWaves];
     const int lane = threadIdx.x % kPer, mine = threadIdx.x / kPer;
-    float m = -__builtin_inff(), total = 0.0f;
+    // the largest maximum and the sum under it: a part a thread
+    float m = -__builtin_inff();
+    for (int c = threadIdx.x; c < n; c += kBlock)
+        m = fmaxf(m, parts.ml[2 * (at0 + c * stride)]);
+    m = wave_max(m);
+    if ((threadIdx.x & 63) == 0)
+        ml[0][threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(ml[0][0], ml[0][1]), fmaxf(ml[0][2], ml[0][3]));
+    const float from = m == -__builtin_inff() ? 0.0f : m;
+    float total = 0.0f;
+    for (int c = threadIdx.x; c < n; c += kBlock) {
+        const int64_t at = at0 + c * stride;
+        total += parts.ml[2 * at + 1] * __builtin_amdgcn_exp2f(parts.ml[2 * at] - from);
+    }
+    total = wave_sum(total);
+    if ((threadIdx.x & 63) == 0)
+        ml[1][threadIdx.x >> 6] = total;
     f4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (mine < kRows) {
-        for (int c = mine; c < p.parts; c += kRows) {
+#pragma unroll 8
+        for (int c = mine; c < n; c += kRows) {
             const int64_t at = at0 + c * stride;
-            const float mc = parts.ml[2 * at], lc = parts.ml[2 * at + 1];
-            const f4_t x = *reinterpret_cast<const f4_t *>(parts.o + at * D + 4 * lane);
-            const float to = fmaxf(m, mc), from = to == -__builtin_inff() ? 0.0f : to;
-            const float wm = __builtin_amdgcn_exp2f(m - from), wc = __builtin_amdgcn_exp2f(mc - from);
-            v = v * wm + x * wc;
-            total = total * wm + lc * wc;
-            m = to;
+            v += *reinterpret_cast<const f4_t *>(parts.o + at * D + 4 * lane) * __builtin_amdgcn_exp2f(parts.ml[2 * at] - from);
         }
         *reinterpret_cast<f4_t *>(&o[mine][4 * lane]) = v;
-        if (lane == 0)
-            ml[mine][0] = m, ml[mine][1] = total;
     }
     __syncthreads();
     if (mine > 0)
         return;
-    m = -__builtin_inff();
+    total = (ml[1][0] + ml[1][1]) + (ml[1][2] + ml[1][3]);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
-        m = fmaxf(m, ml[r][0]);
-    const float from = m == -__builtin_inff() ? 0.0f : m;
-    total = 0.0f;
-    v = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const float w = __builtin_amdgcn_exp2f(ml[r][0] - from);
-        v += *reinterpret_cast<const f4_t *>(&o[r][4 * lane]) * w;
-        total += ml[r][1] * w;
-    }
+    for (int r = 1; r < kRows; ++r)
+        v += *reinterpret_cast<const f4_t *>(&o[r][4 * lane]);
     const float inverse = 1.0f / total;
     if (total == 0.0f)
         v = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -693,19 +751,18 @@ struct Cut {
     bool join;
 };
 
-Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, int page, int64_t width)
+Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page, int64_t width)
 {
     Cut c;
     c.rows = M * (q_heads / kv_heads);
     c.tiles = tiles_of_rows(c.rows, dim);
     c.row_groups = (c.rows + 16 * c.tiles - 1) / (16 * c.tiles);
-    c.target = std::max(1, kTargetGroups / (kv_heads * c.row_groups));
-    // a sequence has at most this many tiles (a window's first one may be cut); chunks of one tile at least
+    c.target = std::max(1, kRounds * kUnits * resident(dim, f8, c.tiles) / (kv_heads * c.row_groups));
+    // no sequence has more tiles than this (a window's first one may be cut): no more runs than tiles
     const int64_t most = ceil_div(width * page, kTile) + 1;
-    c.units = std::min(B * most, c.target + B);
-    c.join = width * page > kTile;
-    if (!c.join)
-        c.units = B;
+    c.target = (int)std::min<int64_t>(c.target, B * most);
+    c.units = c.target + B;
+    c.join = c.target > 1 && width * page > kTile;
     return c;
 }
 
@@ -720,7 +777,7 @@ hipError_t launch(const AttendLaunch &la, const Cut &c, hipStream_t stream)
     else if constexpr (D <= 128)
         fn = &attend_kernel<TQ, kF8, D, 4>;
     const hipError_t e = launch_kernel(reinterpret_cast<const void *>(fn),
-                                       dim3((unsigned)(c.units * la.a.cache.heads * c.row_groups)), dim3(kBlock), 0,
+                                       dim3((unsigned)(c.target * la.a.cache.heads * c.row_groups)), dim3(kBlock), 0,
                                        stream, la);
     if (e != hipSuccess || !c.join)
         return e;
@@ -742,15 +799,15 @@ hipError_t of_dim(const AttendLaunch &la, const Cut &c, hipStream_t stream)
 
 }  // namespace
 
-size_t attend_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int page, int64_t width)
+size_t attend_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int cache_type, int page, int64_t width)
 {
-    const Cut c = cut(B, M, q_heads, kv_heads, dim, page, width);
+    const Cut c = cut(B, M, q_heads, kv_heads, dim, cache_type == QG_F8, page, width);
     return c.join ? (size_t)c.units * kv_heads * c.rows * (dim + 2) * sizeof(float) : 0;
 }
 
 hipError_t launch_attend(const AttendArgs &a, int q_type, hipStream_t stream)
 {
-    const Cut c = cut(a.B, a.M, a.q_heads, a.cache.heads, a.cache.dim, a.cache.page, a.width);
+    const Cut c = cut(a.B, a.M, a.q_heads, a.cache.heads, a.cache.dim, a.cache.type == QG_F8, a.cache.page, a.width);
     const AttendLaunch la{a, c.target, (int)c.units, c.rows, c.row_groups};
     if (a.cache.type == QG_F8)
         return q_type == QG_F16 ? of_dim<Fp16, true>(la, c, stream) : of_dim<Bf16, true>(la, c, stream);

@@ -215,13 +215,14 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
     return status(launch_head_norm_rope_write(a, x_type, on(stream)));
 }
 
-size_t qattn_decode_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int page, int64_t width)
+size_t qattn_decode_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int cache_type, int page,
+                              int64_t width)
 {
     if (B < 1 || B > kAttnMaxBatch || M < 1 || M > kAttnMaxNew || kv_heads < 1 || q_heads < kv_heads ||
-        q_heads > kAttnMaxHeads || q_heads % kv_heads || B * M * q_heads > kAttnMaxRows || !cache_dim_ok(dim) || !page_ok(page) || width < 1 ||
-        width > kAttnMaxPlaces / page)
+        q_heads > kAttnMaxHeads || q_heads % kv_heads || B * M * q_heads > kAttnMaxRows || !cache_dim_ok(dim) || !cache_type_ok(cache_type) || !page_ok(page) || width < 1 ||
+        width > kAttnMaxPlaces / page || B * width * page > kAttnMaxTable)
         return 0;
-    return attend_workspace(B, M, q_heads, kv_heads, dim, page, width);
+    return attend_workspace(B, M, q_heads, kv_heads, dim, cache_type, page, width);
 }
 
 qg_status qattn_decode(const void *cache, int64_t pages, int page, int kv_heads, int dim, int cache_type,
@@ -237,9 +238,9 @@ qg_status qattn_decode(const void *cache, int64_t pages, int page, int kv_heads,
     if ((q_type != QG_F16 && q_type != QG_BF16) || (cache_type != QG_F8 && cache_type != q_type) || B < 1 ||
         B > kAttnMaxBatch || M < 1 || M > kAttnMaxNew || q_heads < kv_heads || q_heads > kAttnMaxHeads ||
         q_heads % kv_heads || B * M * q_heads > kAttnMaxRows || !qg::rows_ok(ldq, q_heads, dim, B * M) || width < 1 ||
-        width > kAttnMaxPlaces / page || window < 0 || window > INT32_MAX || !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f)
+        width > kAttnMaxPlaces / page || B * width * page > kAttnMaxTable || window < 0 || window > INT32_MAX || !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f)
         return QG_ERR_SHAPE;
-    if (!workspace && attend_workspace(B, M, q_heads, kv_heads, dim, page, width) > 0)
+    if (!workspace && attend_workspace(B, M, q_heads, kv_heads, dim, cache_type, page, width) > 0)
         return QG_ERR_NULL;
     if (!aligned(q, 2) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(out, 2) || !aligned(workspace, 16))
         return QG_ERR_ALIGN;

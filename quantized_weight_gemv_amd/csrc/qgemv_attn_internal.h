@@ -18,6 +18,7 @@ constexpr int kAttnMaxNew = 16;
 constexpr int kAttnMaxBatch = 1 << 16;
 constexpr int kMaxAxes = 4;
 constexpr int64_t kAttnMaxPlaces = 1 << 30;   // of a sequence: a place, a few steps on, fits 31 bits
+constexpr int64_t kAttnMaxTable = (int64_t)1 << 36;   // of all sequences: tiles of them are counted in 31 bits
 constexpr int64_t kAttnMaxRows = 1 << 23;     // query heads of all new tokens: workgroups of a launch
 
 inline bool cache_type_ok(int t) { return t == QG_F8 || t == QG_F16 || t == QG_BF16; }
@@ -173,7 +174,8 @@ struct AttendArgs {
     void *out;
     void *workspace;
 };
-size_t attend_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int page, int64_t width);
+size_t attend_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int cache_type, int page,
+                        int64_t width);
 hipError_t launch_attend(const AttendArgs &a, int q_type, hipStream_t stream);
 
 }  // namespace qg

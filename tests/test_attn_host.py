@@ -127,7 +127,7 @@ def test_norm_rope_write_refuses(kw, status):
     (dict(qt=0), SHAPE), (dict(qt=3), SHAPE), (dict(type=2, qt=1), SHAPE), (dict(ldq=511), SHAPE), (dict(B=0), SHAPE),
     (dict(B=65537), SHAPE), (dict(M=0), SHAPE), (dict(M=17), SHAPE), (dict(nq=3), SHAPE), (dict(nq=1), SHAPE),
     (dict(nq=1026, ldq=1 << 20), SHAPE), (dict(B=65536, M=16, nq=16, ldq=2048), SHAPE),
-    (dict(width=(1 << 30) // 64 + 1), SHAPE), (dict(width=0), SHAPE), (dict(width=(1 << 31) // 64), SHAPE),
+    (dict(width=(1 << 30) // 64 + 1), SHAPE), (dict(B=65, width=(1 << 30) // 64), SHAPE), (dict(width=0), SHAPE), (dict(width=(1 << 31) // 64), SHAPE),
     (dict(scale=float("inf")), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(window=-1), SHAPE),
     (dict(window=1 << 31), SHAPE), (dict(cap=-1.0), SHAPE), (dict(cap=float("inf")), SHAPE), (dict(q=P + 1), ALIGN),
     (dict(table=P + 2), ALIGN), (dict(lens=P + 2), ALIGN), (dict(out=P + 1), ALIGN), (dict(ws=P + 8), ALIGN)])
@@ -144,8 +144,8 @@ def test_workspaces_of_sizes_out_of_range():
     assert L.qhead_norm_rope_backward_workspace(0, 4, 2, 128, 1) == 0
     assert L.qhead_norm_rope_backward_workspace(5, 4, 2, 130, 1) == 0
     assert L.qhead_norm_rope_backward_workspace(5, 4, 2, 128, 1) > 0
-    assert L.qattn_decode_workspace(1, 17, 4, 2, 128, 64, 7) == 0
-    assert L.qattn_decode_workspace(1, 1, 3, 2, 128, 64, 7) == 0
+    assert L.qattn_decode_workspace(1, 17, 4, 2, 128, 3, 64, 7) == 0
+    assert L.qattn_decode_workspace(1, 1, 3, 2, 128, 3, 64, 7) == 0
 
 
 def test_the_binding_refuses_host_tensors():
