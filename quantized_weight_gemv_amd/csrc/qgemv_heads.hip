@@ -26,6 +26,32 @@ struct __attribute__((packed, aligned(4))) Raw16f {
     uint32_t w[4];
 };
 
+// A lane's eight elements as they lie in memory, loaded ahead of their use.
+template <typename T>
+struct Eight {
+    using Piece = std::conditional_t<sizeof(T) == 4, Raw16f, Raw8>;
+    Piece p[2];
+    __device__ __forceinline__ void load(const T *row, int lo, int hi)
+    {
+        p[0] = *reinterpret_cast<const Piece *>(row + lo);
+        p[1] = *reinterpret_cast<const Piece *>(row + hi);
+    }
+    // all zeros unless `on`
+    template <typename F>
+    __device__ __forceinline__ void values(bool on, F (&v)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float x;
+            if constexpr (sizeof(T) == 4)
+                x = __uint_as_float(p[i / 4].w[i & 3]);
+            else
+                x = to_f32(T{(uint16_t)(p[i / 4].w[(i & 3) / 2] >> (16 * (i & 1)))});
+            v[i] = on ? x : 0.0f;
+        }
+    }
+};
+
 template <typename T>
 __device__ __forceinline__ void load4(const T *p, float *v)
 {
@@ -137,9 +163,37 @@ __device__ __forceinline__ Place place(int D, int half, bool interleaved)
     return p;
 }
 
+// sin and cos of `turn` whole turns, to a few 2^-53: the nearest quarter is taken
+// out, the rest, up to an eighth, goes through the series of both (coefficients
+// (2 pi)^k / k!, the first term left out below 2^-54).
+__device__ __forceinline__ void sin_cos(double turn, double &s, double &c)
+{
+    constexpr double kSin[] = {6.283185307179586, -41.34170224039976, 81.60524927607506, -76.70585975306139,
+                               42.058693944897655, -15.09464257682299, 3.819952584848282, -0.7181223017785006};
+    constexpr double kCos[] = {1.0, -19.739208802178716, 64.9393940226683, -85.45681720669373,
+                               60.24464137187666, -26.4262567833744, 7.903536371318469, -1.714390711088672,
+                               0.28200596845579123};
+    const double quarter = rint(4.0 * turn);
+    const double r = fma(quarter, -0.25, turn), z = r * r;
+    double a = kSin[7], b = kCos[8];
+#pragma unroll
+    for (int i = 6; i >= 0; --i)
+        a = fma(a, z, kSin[i]);
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+        b = fma(b, z, kCos[i]);
+    a *= r;
+    const int q = (int)quarter;
+    s = (q & 1) ? b : a;
+    c = (q & 1) ? a : b;
+    s = (q & 2) ? -s : s;
+    c = ((q + 1) & 2) ? -c : c;
+}
+
 // Turns of the four pairs of a lane at a token's positions: position * freq /
-// 2 pi in 64 bits, whose whole turns are dropped before the sine (far positions
-// keep all 24 bits of the rest).
+// 2 pi in 64 bits, whose whole turns are dropped first; cosine and sine in 64
+// bits too (the vector units do those as fast as fp32), so that in fp32 they are
+// the nearest ones.
 template <typename F>
 __device__ __forceinline__ void turns(const HeadArgs &a, const Place &p, int64_t t, F (&c)[4], F (&s)[4])
 {
@@ -151,22 +205,21 @@ __device__ __forceinline__ void turns(const HeadArgs &a, const Place &p, int64_t
     const Raw16f f = *reinterpret_cast<const Raw16f *>(a.freq + 4 * p.l);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int pair = 4 * p.l + i;
         int axis = 0;
         for (int j = 0; j + 1 < a.axes; ++j)
-            axis += pair >= a.sections[j] ? 1 : 0;
+            axis += 4 * p.l + i >= a.sections[j] ? 1 : 0;
         double turn = (double)a.positions[axis * a.T + t] * (double)__uint_as_float(f.w[i]) * kInvTwoPi;
         turn -= rint(turn);
-        if constexpr (sizeof(F) == 8)
-            sincospi(2.0 * turn, &s[i], &c[i]);
-        else
-            sincospif((float)(2.0 * turn), &s[i], &c[i]);
+        double sine, cosine;
+        sin_cos(turn, sine, cosine);
+        c[i] = (F)cosine, s[i] = (F)sine;
     }
 }
 
 template <typename F>
 __device__ __forceinline__ void turn(const Place &p, bool interleaved, const F (&c)[4], const F (&s)[4], F (&v)[8])
 {
+#pragma clang fp contract(off)   // each product rounds by itself, as in a program of separate operations
     if (!p.turned)
         return;   // (what is not turned is left as it is, infinities too)
     if (interleaved) {
@@ -190,13 +243,13 @@ __device__ __forceinline__ float inverse_root(float v) { return rsqrtf(v); }
 __device__ __forceinline__ double inverse_root(double v) { return 1.0 / sqrt(v); }
 
 template <int L, typename F>
-__device__ __forceinline__ F inverse_norm(const F (&v)[8], int D, float eps)
+__device__ __forceinline__ F inverse_norm(const F (&v)[8], F inverse_dim, float eps)
 {
     F ss = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         ss += v[i] * v[i];
-    return inverse_root(group_sum<L>(ss) / (F)D + (F)eps);
+    return inverse_root(group_sum<L>(ss) * inverse_dim + (F)eps);
 }
 
 // A lane's eight values of an f8 vector held by L lanes: codes and scale byte,
@@ -272,108 +325,107 @@ __device__ __forceinline__ void put(const KvCache &c, int slot, int head, int kv
     }
 }
 
-// Heads of one kind of a token, groups first .. last - 1 of them.
-template <typename T, int L, typename F, typename Done>
-__device__ __forceinline__ void walk(const HeadArgs &a, const Place &p, int64_t t, int kind, int first, int last,
-                                     const F (&c)[4], const F (&s)[4], Done done)
+// A head's vector normed and turned, in fp32 or 64 bits.
+template <int L, typename F>
+__device__ __forceinline__ void norm_turn(const HeadArgs &a, const Place &p, const float (&gain)[8], const F (&c)[4],
+                                          const F (&s)[4], F (&v)[8])
 {
-    const bool plain = kind == 2;
-    float gain[8];
-    const bool normed = !plain && a.gain[0] != nullptr;
-    if (normed && p.on)
-        load8_as(a.gain_type, a.gain[kind], 0, p.lo, p.hi, gain);
-    const T *x = static_cast<const T *>(a.x[kind]) + t * a.ldx[kind];
-#pragma unroll 2
-    for (int g = first; g < last; ++g) {
-        const int head = g * (64 / L) + p.sub;
-        const bool on = p.on && head < a.heads[kind];
-        float in[8];
+    if (a.gain[0]) {
+        const F r = inverse_norm<L>(v, (F)1 / (F)a.D, a.eps);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            in[i] = 0.0f;
-        if (on) {
-            load4(x + head * a.D + p.lo, in);
-            load4(x + head * a.D + p.hi, in + 4);
-        }
-        F v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = in[i];
-        if (normed) {
-            const F r = inverse_norm<L>(v, a.D, a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = v[i] * r * (F)gain[i];
-        }
-        if (!plain)
-            turn(p, a.interleaved, c, s, v);
-        done(head, on, v);
+            v[i] = v[i] * r * (F)gain[i];
     }
+    turn(p, a.interleaved, c, s, v);
 }
 
 // Wave `unit` of the launch takes part unit % parts of the groups of heads of
-// token unit / parts.
+// token unit / parts: query heads, key heads and, when they are written to a
+// cache, value heads.  The next group is loaded ahead; the first one lies behind
+// the cosines.
 template <typename T, int L, bool kWrite, bool kF8>
 __global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
 {
     const Place p = place<L>(a.D, a.half, a.interleaved);
-    const int all = a.groups[0] + a.groups[1] + (kWrite ? a.groups[2] : 0);
+    const int k0 = a.groups[0], v0 = k0 + a.groups[1], all = v0 + (kWrite ? a.groups[2] : 0);
+    float gain[2][8];
+    if (a.gain[0] && p.on) {
+        load8_as(a.gain_type, a.gain[0], 0, p.lo, p.hi, gain[0]);
+        load8_as(a.gain_type, a.gain[1], 0, p.lo, p.hi, gain[1]);
+    }
     const int64_t units = a.T * a.parts;
     for (int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
          unit < units; unit += (int64_t)gridDim.x * (kBlock / 64)) {
         const int64_t t = unit / a.parts;
         const int part = (int)(unit - t * a.parts);
-        const int first = (int)((int64_t)part * all / a.parts), last = (int)((int64_t)(part + 1) * all / a.parts);
+        const int first = (int)((int64_t)part * all / a.parts);
+        int last = (int)((int64_t)(part + 1) * all / a.parts);
+        int slot = 0;
+        if constexpr (kWrite) {
+            if (last > k0) {
+                slot = a.slots[t];
+                if ((uint32_t)slot >= (uint32_t)a.cache.pages << a.cache.log_page)
+                    last = min(last, k0);
+            }
+        }
+        if (first >= last)
+            continue;
+        Eight<T> x;
+        int head;
+        bool on;
+        auto fetch = [&](int group) {
+            const int kind = group < k0 ? 0 : !kWrite || group < v0 ? 1 : 2;
+            head = (group - (kind == 0 ? 0 : kind == 1 ? k0 : v0)) * (64 / L) + p.sub;
+            on = p.on && head < (kind == 0 ? a.heads[0] : a.heads[1]);
+            const void *base = kind == 0 ? a.x[0] : kind == 1 ? a.x[1] : a.x[2];
+            const int64_t ld = kind == 0 ? a.ldx[0] : kind == 1 ? a.ldx[1] : a.ldx[2];
+            if (on)
+                x.load(static_cast<const T *>(base) + t * ld + head * a.D, p.lo, p.hi);
+        };
+        fetch(first);
         float c[4], s[4];
         double cd[4], sd[4];
-        const int k0 = a.groups[0], v0 = k0 + a.groups[1];
-        if constexpr (kF8) {
-            if (first < v0 && last > k0) {
+        if (first < v0) {
+            if constexpr (kF8) {
                 turns(a, p, t, cd, sd);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     c[i] = (float)cd[i], s[i] = (float)sd[i];
-            } else if (first < k0) {
+            } else {
                 turns(a, p, t, c, s);
             }
-        } else if (first < v0) {
-            turns(a, p, t, c, s);
         }
-        if (first < k0)
-            walk<T, L>(a, p, t, 0, first, min(last, k0), c, s, [&](int head, bool on, float (&v)[8]) {
-                if (on)
-                    store8_as(a.y_type, a.y[0], t * a.ldy[0] + head * a.D, p.lo, p.hi, v);
-            });
-        if (last <= k0)
-            continue;
-        if constexpr (!kWrite) {
-            walk<T, L>(a, p, t, 1, max(first - k0, 0), last - k0, c, s, [&](int head, bool on, float (&v)[8]) {
-                if (on)
-                    store8_as(a.y_type, a.y[1], t * a.ldy[1] + head * a.D, p.lo, p.hi, v);
-            });
-        } else {
-            const int slot = a.slots[t];
-            if ((uint32_t)slot >= (uint32_t)a.cache.pages << a.cache.log_page)
-                continue;
-            if (first < v0) {
-                const int from = max(first - k0, 0), to = min(last, v0) - k0;
-                if constexpr (kF8)
-                    walk<T, L>(a, p, t, 1, from, to, cd, sd, [&](int head, bool on, double (&v)[8]) {
-                        float f[8];
+        for (int group = first; group < last; ++group) {
+            const Eight<T> now = x;
+            const int h = head;
+            const bool is = on;
+            if (group + 1 < last)
+                fetch(group + 1);
+            float v[8];
+            if (kWrite && kF8 && group >= k0 && group < v0) {
+                double w[8];
+                now.values(is, w);
+                norm_turn<L>(a, p, gain[1], cd, sd, w);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            f[i] = sticky(v[i]);
-                        put<L>(a.cache, slot, head, 0, on, p.l, p.lo, p.hi, f);
-                    });
-                else
-                    walk<T, L>(a, p, t, 1, from, to, c, s, [&](int head, bool on, float (&v)[8]) {
-                        put<L>(a.cache, slot, head, 0, on, p.l, p.lo, p.hi, v);
-                    });
+                for (int i = 0; i < 8; ++i)
+                    v[i] = sticky(w[i]);
+                put<L>(a.cache, slot, h, 0, is, p.l, p.lo, p.hi, v);
+                continue;
             }
-            if (last > v0)
-                walk<T, L>(a, p, t, 2, max(first - v0, 0), last - v0, c, s, [&](int head, bool on, float (&v)[8]) {
-                    put<L>(a.cache, slot, head, 1, on, p.l, p.lo, p.hi, v);
-                });
+            now.values(is, v);
+            if (group < k0) {
+                norm_turn<L>(a, p, gain[0], c, s, v);
+                if (is)
+                    store8_as(a.y_type, a.y[0], t * a.ldy[0] + h * a.D, p.lo, p.hi, v);
+            } else if (group < v0) {
+                norm_turn<L>(a, p, gain[1], c, s, v);
+                if constexpr (kWrite)
+                    put<L>(a.cache, slot, h, 0, is, p.l, p.lo, p.hi, v);
+                else if (is)
+                    store8_as(a.y_type, a.y[1], t * a.ldy[1] + h * a.D, p.lo, p.hi, v);
+            } else if constexpr (kWrite) {
+                put<L>(a.cache, slot, h, 1, is, p.l, p.lo, p.hi, v);
+            }
         }
     }
 }
@@ -389,6 +441,7 @@ __global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
     const Place p = place<L>(a.D, a.half, a.interleaved);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool normed = a.gain[0] != nullptr;
+    const float inverse_dim = 1.0f / (float)a.D;
     float dg[2][8], gain[2][8];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -405,60 +458,66 @@ __global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
         const int64_t t = unit / a.parts;
         const int part = (int)(unit - t * a.parts);
         const int first = (int)((int64_t)part * all / a.parts), last = (int)((int64_t)(part + 1) * all / a.parts);
+        Eight<T> x;
+        Eight<TY> dy;
+        int head;
+        bool on;
+        const int k0 = a.groups[0];
+        auto fetch = [&](int group) {
+            const bool key = group >= k0;
+            head = (key ? group - k0 : group) * (64 / L) + p.sub;
+            on = p.on && head < (key ? a.heads[1] : a.heads[0]);
+            if (on) {
+                dy.load(static_cast<const TY *>(key ? a.y[1] : a.y[0]) + t * (key ? a.ldy[1] : a.ldy[0]) + head * a.D,
+                        p.lo, p.hi);
+                if (normed)
+                    x.load(static_cast<const T *>(key ? a.x[1] : a.x[0]) + t * (key ? a.ldx[1] : a.ldx[0]) +
+                               head * a.D, p.lo, p.hi);
+            }
+        };
+        fetch(first);
         float c[4], s[4];
         turns(a, p, t, c, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             s[i] = -s[i];
-        auto heads = [&](auto kind, int from, int to) {
+        auto one = [&](auto kind, int group) {
             constexpr int k = decltype(kind)::value;
-            const T *x = static_cast<const T *>(a.x[k]) + t * a.ldx[k];
-            const TY *dy = static_cast<const TY *>(a.y[k]) + t * a.ldy[k];
-            T *dx = static_cast<T *>(ga.g[k]) + t * ga.ldg[k];
-#pragma unroll 2
-            for (int g = from; g < to; ++g) {
-                const int head = g * (64 / L) + p.sub;
-                const bool on = p.on && head < a.heads[k];
-                float v[8], h[8];
+            const Eight<T> now = x;
+            const int at = head;
+            const bool is = on;
+            float h[8];
+            dy.values(is, h);
+            if (group + 1 < last)
+                fetch(group + 1);
+            turn(p, a.interleaved, c, s, h);
+            if (normed) {
+                float v[8], ss = 0.0f, dot = 0.0f;
+                now.values(is, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = h[i] = 0.0f;
-                if (on) {
-                    load4(dy + head * a.D + p.lo, h);
-                    load4(dy + head * a.D + p.hi, h + 4);
-                    if (normed) {
-                        load4(x + head * a.D + p.lo, v);
-                        load4(x + head * a.D + p.hi, v + 4);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    ss += v[i] * v[i];
+                    dot += h[i] * gain[k][i] * v[i];
                 }
-                turn(p, a.interleaved, c, s, h);
-                if (normed) {
-                    float ss = 0.0f, dot = 0.0f;
+                const float r = inverse_root(group_sum<L>(ss) * inverse_dim + a.eps);
+                const float mean = group_sum<L>(dot) * r * inverse_dim;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        ss += v[i] * v[i];
-                        dot += h[i] * gain[k][i] * v[i];
-                    }
-                    const float r = inverse_root(group_sum<L>(ss) / (float)a.D + a.eps);
-                    const float mean = group_sum<L>(dot) * r / (float)a.D;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float n = v[i] * r;
-                        dg[k][i] += on ? h[i] * n : 0.0f;
-                        h[i] = r * (h[i] * gain[k][i] - n * mean);
-                    }
-                }
-                if (on) {
-                    store4(dx + head * a.D + p.lo, h);
-                    store4(dx + head * a.D + p.hi, h + 4);
+                for (int i = 0; i < 8; ++i) {
+                    const float n = v[i] * r;
+                    dg[k][i] += is ? h[i] * n : 0.0f;
+                    h[i] = r * (h[i] * gain[k][i] - n * mean);
                 }
             }
+            if (is) {
+                T *to = static_cast<T *>(ga.g[k]) + t * ga.ldg[k] + at * a.D;
+                store4(to + p.lo, h);
+                store4(to + p.hi, h + 4);
+            }
         };
-        const int k0 = a.groups[0];
-        if (first < k0)
-            heads(std::integral_constant<int, 0>{}, first, min(last, k0));
-        if (last > k0)
-            heads(std::integral_constant<int, 1>{}, max(first - k0, 0), last - k0);
+        for (int group = first; group < min(last, k0); ++group)
+            one(std::integral_constant<int, 0>{}, group);
+        for (int group = max(first, k0); group < last; ++group)
+            one(std::integral_constant<int, 1>{}, group);
     }
     if (!normed)
         return;
