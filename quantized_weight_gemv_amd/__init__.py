@@ -19,6 +19,7 @@ include/qgemv_attn.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -411,10 +412,15 @@ def qquantize_f8(w: np.ndarray, out: np.ndarray | None = None) -> np.ndarray:
     return out
 
 
+_types: dict = {}
+
+
 def _type(dtype) -> int:
     """QG_F32 / QG_F16 / QG_BF16 of a torch dtype."""
-    torch = _torch()
-    code = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}.get(dtype)
+    if not _types:
+        torch = _torch()
+        _types.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    code = _types.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     return code
@@ -479,7 +485,7 @@ class _Call:
         # the stream's handle as it is: torch.cuda.current_stream() makes an
         # object around it first (2.7 us of the 9.7 that a small call took)
         stream = self.torch._C._cuda_getCurrentRawStream(index)
-        if index == self.torch.cuda.current_device():
+        if index == self.torch._C._cuda_getDevice():
             st = f(*args, stream)
         else:
             with self.torch.cuda.device(index):
@@ -703,17 +709,33 @@ class KVCache(NamedTuple):
     dtype: object
 
 
+_cache_types: dict = {}
+
+
 def _cache_type(dtype) -> int:
-    torch = _torch()
-    code = {torch.float8_e4m3fn: 3, torch.float16: 1, torch.bfloat16: 2}.get(dtype)
+    if not _cache_types:
+        torch = _torch()
+        _cache_types.update({torch.float8_e4m3fn: 3, torch.float16: 1, torch.bfloat16: 2})
+    code = _cache_types.get(dtype)
     if code is None:
         raise TypeError(f"a cache holds float8_e4m3fn, float16 or bfloat16, got {dtype}")
     return code
 
 
+# functions of sizes alone, asked for by every call
+@functools.lru_cache(maxsize=None)
+def _page_bytes(page: int, heads: int, dim: int, code: int) -> int:
+    return int(lib().qkv_page_bytes(page, heads, dim, code))
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace(fn: str, *sizes: int) -> int:
+    return int(getattr(lib(), fn)(*sizes))
+
+
 def qkv_page_bytes(page: int, heads: int, dim: int, dtype) -> int:
     """Bytes of one cache page (0 where the sizes are out of range)."""
-    return int(lib().qkv_page_bytes(page, heads, dim, _cache_type(dtype)))
+    return _page_bytes(page, heads, dim, _cache_type(dtype))
 
 
 def qkv_cache(pages: int, page: int, heads: int, dim: int, dtype=None, device="cuda") -> KVCache:
@@ -727,78 +749,88 @@ def qkv_cache(pages: int, page: int, heads: int, dim: int, dtype=None, device="c
 
 def _cache(c, fn: str, cache: KVCache):
     """The cache's arguments: address, pages, page, heads, dim, type."""
-    code = _cache_type(cache.dtype)
-    nb = int(lib().qkv_page_bytes(cache.page, cache.heads, cache.dim, code))
-    _sizes(fn, nb)
-    n = cache.data.numel()
-    if n % nb or n == 0:
-        raise ValueError(f"cache.data has {n} bytes, not a multiple of {nb}")
-    return c.ptr(cache.data, c.torch.uint8, "cache.data", n), n // nb, cache.page, cache.heads, cache.dim, code
+    data, page, heads, dim, dtype = cache
+    code = _cache_type(dtype)
+    nb = _page_bytes(page, heads, dim, code)
+    if not nb:
+        raise QGError(fn, 2)
+    at = c.ptr(data, c.torch.uint8, "cache.data", nb)
+    pages, rest = divmod(data.numel(), nb)
+    if rest:
+        raise ValueError(f"cache.data has {data.numel()} bytes, not a multiple of {nb}")
+    return at, pages, page, heads, dim, code
 
 
 def _rows(c, x, name: str, dtype, T: int, D: int, heads=None):
     """Address, distance of tokens and heads of a tensor [T][heads][D]."""
+    # one pass over what has to hold; the reasons are looked up only for a refusal
+    if isinstance(x, c.torch.Tensor) and x.get_device() == c.index and x.dtype is dtype and x.dim() == 3:
+        t, n, d = x.shape
+        if t == T and d == D and (heads is None or n == heads):
+            ld, of_head, of_element = x.stride()
+            if (of_element == 1 or D == 1) and (of_head == D or n == 1):
+                if x.requires_grad:
+                    c.no_grad(name)
+                return x.data_ptr(), ld if T > 1 else n * D, n
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
     if not isinstance(x, c.torch.Tensor) or not x.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
     if x.get_device() != c.index:
         raise ValueError(f"{name} is on {x.device}, the call's other tensors on {c.device}")
     if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{name} must be [{T}][{'heads' if heads is None else heads}][{D}], got {list(x.shape)}")
-    if x.requires_grad:
-        c.no_grad(name)
-    n = x.shape[1]
-    ld, of_head, of_element = x.stride()
-    if (D > 1 and of_element != 1) or (n > 1 and of_head != D):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return x.data_ptr(), ld if T > 1 else n * D, n
+    raise ValueError(f"{name} must be [{T}][{'heads' if heads is None else heads}][{D}], got {list(x.shape)}")
 
 
-def _turn(c, q, k, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, k_heads):
+def _turn(c, T: int, D: int, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, k_heads):
     """The arguments of norm and rotation that the calls have in common."""
-    torch = c.torch
-    T, _, D = q.shape
-    if (q_gain is None) != (k_gain is None) and k_heads:
-        raise ValueError("q_gain and k_gain: both or none")
-    gains, gain_type = (None, None), 0
+    gq = gk = None
+    gain_type = 0
     if q_gain is not None:
-        k_gain = q_gain if k_gain is None else k_gain
-        gain_type = _type(q_gain.dtype)
-        gains = tuple(c.ptr(g, q_gain.dtype, n, D) for g, n in ((q_gain, "q_gain"), (k_gain, "k_gain")))
+        if k_gain is None and not k_heads:
+            k_gain = q_gain
+        dtype = q_gain.dtype
+        gain_type = _type(dtype)
+        gq, gk = c.ptr(q_gain, dtype, "q_gain", D), c.ptr(k_gain, dtype, "k_gain", D)
         if q_gain.numel() != D or k_gain.numel() != D:
             raise ValueError(f"gains must be [{D}]")
-    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
-    if rot == 0:
-        return *gains, gain_type, eps, None, 1, None, None, 0, 0
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    if positions.shape[-1] != T or positions.dim() > 2:
-        raise ValueError(f"positions must be [{T}] or [axes][{T}], got {list(positions.shape)}")
+    elif k_gain is not None and k_heads:
+        raise ValueError("q_gain and k_gain: both or none")
+    half = inv_freq.numel() if inv_freq is not None else 0
+    if not half:
+        return gq, gk, gain_type, eps, None, 1, None, None, 0, 0
+    shape = positions.shape
+    axes = shape[0] if len(shape) == 2 else 1
+    if len(shape) > 2 or not shape or shape[-1] != T:
+        raise ValueError(f"positions must be [{T}] or [axes][{T}], got {list(shape)}")
     if sections is not None:
-        if len(sections) != axes or sum(sections) != rot // 2:
-            raise ValueError(f"sections must be {axes} numbers with the sum {rot // 2}, got {list(sections)}")
+        if len(sections) != axes or sum(sections) != half:
+            raise ValueError(f"sections must be {axes} numbers with the sum {half}, got {list(sections)}")
         sections = (ctypes.c_int32 * axes)(*sections)
     elif axes > 1:
         raise ValueError("positions of several axes need sections")
-    return (*gains, gain_type, eps, c.ptr(positions, torch.int32, "positions", axes * T), axes, sections,
-            c.ptr(inv_freq, torch.float32, "inv_freq", rot // 2), rot, int(interleaved))
+    return (gq, gk, gain_type, eps, c.ptr(positions, c.torch.int32, "positions", axes * T), axes, sections,
+            c.ptr(inv_freq, c.torch.float32, "inv_freq", half), 2 * half, int(interleaved))
 
 
 def _head_tensors(c, q, k):
-    if not isinstance(q, c.torch.Tensor) or q.dim() != 3:
+    if q.dim() != 3:
         raise ValueError("q must be [T][heads][D]")
     T, _, D = q.shape
-    qp, ldq, nq = _rows(c, q, "q", q.dtype, T, D)
-    kp, ldk, nk = _rows(c, k, "k", q.dtype, T, D) if k is not None else (None, 0, 0)
-    return T, D, nq, nk, (qp, ldq, nq, kp, ldk, nk, _type(q.dtype))
+    dtype = q.dtype
+    qp, ldq, nq = _rows(c, q, "q", dtype, T, D)
+    kp, ldk, nk = _rows(c, k, "k", dtype, T, D) if k is not None else (None, 0, 0)
+    return T, D, nq, nk, (qp, ldq, nq, kp, ldk, nk, _type(dtype))
 
 
 def _head_outputs(c, out, name: str, T: int, D: int, nq: int, nk: int, dtype):
     """Two head tensors of the caller's or new ones (no second one without k)."""
     if out is None:
         yq = c.new((T, nq, D), dtype)
-        yk = c.new((T, nk, D), dtype) if nk else None
-        return yq, yk, yq.data_ptr(), nq * D, yk.data_ptr() if nk else None, nk * D
+        if not nk:
+            return yq, None, yq.data_ptr(), nq * D, None, 0
+        yk = c.new((T, nk, D), dtype)
+        return yq, yk, yq.data_ptr(), nq * D, yk.data_ptr(), nk * D
     yq, yk = out
     qp, ldq, _ = _rows(c, yq, name + "[0]", dtype, T, D, nq)
     kp, ldk, _ = _rows(c, yk, name + "[1]", dtype, T, D, nk) if nk else (None, 0, 0)
@@ -819,7 +851,7 @@ def qhead_norm_rope(q, k, positions, inv_freq, q_gain=None, k_gain=None, eps: fl
     out: the two results' tensors, which may be q and k themselves."""
     c = _Call(q, "q")
     T, D, nq, nk, heads = _head_tensors(c, q, k)
-    turn = _turn(c, q, k, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
+    turn = _turn(c, T, D, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
     dtype = dtype or (q.dtype if out is None else out[0].dtype)
     code = _type(dtype)
     yq, yk, *ys = _head_outputs(c, out, "out", T, D, nq, nk, dtype)
@@ -834,17 +866,19 @@ def qhead_norm_rope_backward(dq, dk, q, k, positions, inv_freq, q_gain=None, k_g
     inputs' type, the gains' in fp32 (None without gains)."""
     c = _Call(q, "q")
     T, D, nq, nk, heads = _head_tensors(c, q, k)
-    turn = _turn(c, q, k, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
+    turn = _turn(c, T, D, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
     gqp, ldgq, _ = _rows(c, dq, "dq", dq.dtype, T, D, nq)
     gkp, ldgk, _ = _rows(c, dk, "dk", dq.dtype, T, D, nk) if nk else (None, 0, 0)
     gq, gk, *gs = _head_outputs(c, out, "out", T, D, nq, nk, q.dtype)
-    ws = int(lib().qhead_norm_rope_backward_workspace(T, nq, nk, D, int(q_gain is not None)))
-    g = w = None
-    if ws:
-        g, w = c.new((2, D), c.torch.float32), c.new((ws,), c.torch.uint8)
-    c("qhead_norm_rope_backward", gqp, ldgq, gkp, ldgk, _type(dq.dtype), *heads, *turn, T, D, *gs,
-      g.data_ptr() if ws else None, w.data_ptr() if ws else None)
-    return gq, gk, g[0] if ws else None, g[1] if ws and nk else None
+    code = _type(dq.dtype)
+    if q_gain is None:
+        c("qhead_norm_rope_backward", gqp, ldgq, gkp, ldgk, code, *heads, *turn, T, D, *gs, None, None)
+        return gq, gk, None, None
+    g = c.new((2, D), c.torch.float32)
+    w = c.new((_workspace("qhead_norm_rope_backward_workspace", T, nq, nk, D, 1),), c.torch.uint8)
+    c("qhead_norm_rope_backward", gqp, ldgq, gkp, ldgk, code, *heads, *turn, T, D, *gs, g.data_ptr(), w.data_ptr())
+    dgq, dgk = g.unbind()
+    return gq, gk, dgq, dgk if nk else None
 
 
 def qkv_write(cache: KVCache, k, v, slots):
@@ -883,7 +917,7 @@ def qkv_norm_rope_write(cache: KVCache, q, k, v, slots, positions, inv_freq, q_g
     vp, ldv, _ = _rows(c, v, "v", q.dtype, T, D, nk)
     if slots.numel() != T:
         raise ValueError(f"slots must be [{T}]")
-    turn = _turn(c, q, k, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
+    turn = _turn(c, T, D, positions, inv_freq, q_gain, k_gain, eps, interleaved, sections, nk)
     dtype = dtype or (q.dtype if out is None else out.dtype)
     code = _type(dtype)
     if out is None:
@@ -909,29 +943,37 @@ def qattn_decode(cache: KVCache, q, table, lens, scale: float | None = None, win
     tanh(s / softcap).  scale: dim ** -0.5 by default.  A query that sees
     nothing gets zeros."""
     c = _Call(q, "q")
-    torch = c.torch
     args = _cache(c, "qattn_decode", cache)
-    if q.dim() not in (3, 4) or q.shape[-1] != cache.dim:
-        raise ValueError(f"q must be [B][M][heads][{cache.dim}] or [B][heads][{cache.dim}]")
-    B, H, D = q.shape[0], q.shape[-2], cache.dim
-    M = q.shape[1] if q.dim() == 4 else 1
-    if q.stride(-1) != 1 or (H > 1 and q.stride(-2) != D):
+    D, heads = cache.dim, cache.heads
+    shape, strides = tuple(q.shape), q.stride()
+    if len(shape) == 3:
+        B, H, d = shape
+        M, ld = 1, strides[0]
+    elif len(shape) == 4:
+        B, M, H, d = shape
+        ld = strides[1] if M > 1 else strides[0]
+        if M > 1 and B > 1 and strides[0] != M * ld:
+            raise ValueError("q: the tokens must be the same distance apart in and between the sequences")
+    else:
+        d = -1
+    if d != D:
+        raise ValueError(f"q must be [B][M][heads][{D}] or [B][heads][{D}]")
+    if strides[-1] != 1 or (strides[-2] != D and H > 1):
         raise ValueError("q: the heads of a token must be contiguous")
-    ld = q.stride(0) if q.dim() == 3 else q.stride(1) if M > 1 else q.stride(0)
-    if M > 1 and B > 1 and q.stride(0) != M * ld:
-        raise ValueError("q: the tokens must be the same distance apart in and between the sequences")
     if B * M == 1:
         ld = H * D
-    if table.dim() != 2 or table.shape[0] != B or lens.numel() != B:
+    places = table.shape
+    if len(places) != 2 or places[0] != B or lens.numel() != B:
         raise ValueError(f"table must be [{B}][width], lens [{B}]")
-    W = table.shape[1]
-    code = _type(q.dtype)
-    out, op = c.result(out, tuple(q.shape), q.dtype, "out", B * M * H * D)
-    ws = int(lib().qattn_decode_workspace(B, M, H, cache.heads, D, args[5], cache.page, W))
-    w = c.new((ws,), torch.uint8) if ws else None
-    c("qattn_decode", *args, q.data_ptr(), code, ld, B, M, H, c.ptr(table, torch.int32, "table", B * W), W,
-      c.ptr(lens, torch.int32, "lens", B), D ** -0.5 if scale is None else scale, window, softcap, op,
-      w.data_ptr() if ws else None)
+    W = places[1]
+    dtype, i32 = q.dtype, c.torch.int32
+    code = _type(dtype)
+    tp, lp = c.ptr(table, i32, "table", B * W), c.ptr(lens, i32, "lens", B)
+    out, op = c.result(out, shape, dtype, "out", B * M * H * D)
+    ws = _workspace("qattn_decode_workspace", B, M, H, heads, D, args[5], cache.page, W)
+    w = c.new((ws,), c.torch.uint8) if ws else None
+    c("qattn_decode", *args, q.data_ptr(), code, ld, B, M, H, tp, W, lp, D ** -0.5 if scale is None else scale, window,
+      softcap, op, w.data_ptr() if ws else None)
     return out
 
 

@@ -42,6 +42,7 @@ constexpr float kSlack = 4.0f;            // weights reach 2^kSlack before they 
 // Rounds of workgroups over the compute units (256) that the work is cut for.
 constexpr int kUnits = 256;
 constexpr int kRounds = 1;
+constexpr int kManyRows = 1024;   // from here on a wave joins a row
 
 typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
@@ -262,6 +263,7 @@ struct AttendLaunch {
     int units;      // parts, at most
     int rows;       // M share
     int row_groups;
+    bool by_sequence;   // a workgroup a sequence, nothing to find or to join
 };
 
 // TQ: type of q, of the output and of 16-bit caches; kF8: an 8-bit cache.
@@ -289,16 +291,23 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
     const int head = blockIdx.x % heads;
     const int group = (blockIdx.x / heads) % la.row_groups;
     const int run = blockIdx.x / (heads * la.row_groups);
-    Plan p = plan<true>(a, la.target, run);
-    if (p.b < 0)
-        return;
-    const int run_end = min((run + 1) * p.run, p.total);
+    Plan p{};
+    if (la.by_sequence) {
+        p.b = run;
+        p.run = p.total = INT32_MAX;
+    } else {
+        p = plan<true>(a, la.target, run);
+        if (p.b < 0)
+            return;
+    }
+    const int run_begin = la.by_sequence ? 0 : run * p.run;
+    const int run_end = min(run_begin + p.run, p.total);
     const int row0 = group * 16 * kTiles;
     __shared__ float o[kWaves][16][D + 4];
     __shared__ float ml[kWaves][16][2];
 
     // one sequence's part of the run after the other
-    for (int tile = run * p.run;;) {
+    for (int tile = run_begin;;) {
         const Sequence seq = sequence(a, p.b);
         const int t0 = tile - p.base, t1 = min(seq.tiles, run_end - p.base);
 
@@ -328,10 +337,17 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
         auto page_of = [&](int token) {
             return scalar_int(a.table, (int64_t)p.b * a.width + min(token >> a.cache.log_page, last_page));
         };
-        // a tile's page, and whether there is one
+        // where a tile of 16 tokens lies, and whether its page is there
         struct Where {
             const uint8_t *keys, *scales;
             bool there;
+        };
+        // what a step multiplies
+        struct Stage {
+            uint32_t kw[2][kKeyLoads][4];
+            uint32_t vw[8][kValWords];
+            uint32_t ks[2], vs[2];
+            bool there[2];
         };
         auto where = [&](int page, int token) {
             Where w;
@@ -344,58 +360,57 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
         };
         const int64_t values = (int64_t)a.cache.page * kRow;
 
-        uint32_t kw[2][kKeyLoads][4];
-        uint32_t vw[8][kValWords];
-        uint32_t ks[2], vs[2];
         // Loads stay where they are written: one moved behind the values' loads would be waited for with all of them.
+        // With live 0, behind the last step, every lane reads the first piece (the count of loads stays the same).
         auto keep_order = [] {
             asm volatile("" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
         };
-        auto load_keys = [&](const Where (&w)[2]) {
+        auto load_keys = [&](Stage &b, const Where (&w)[2], int live) {
             keep_order();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                b.there[h] = w[h].there;
                 if constexpr (kScaledKeys)
-                    ks[h] = w[h].scales[r16];
+                    b.ks[h] = w[h].scales[r16];
                 else if constexpr (kF8)
-                    ks[h] = *reinterpret_cast<const uint32_t *>(w[h].scales + 4 * g);
+                    b.ks[h] = *reinterpret_cast<const uint32_t *>(w[h].scales + 4 * g);
             }
+            const int at = (kWholeLines ? (r16 & 7) * kRow + 64 * (r16 >> 3) + 16 * g : r16 * kRow + 16 * g) & live;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int c = 0; c < kKeyLoads; ++c) {
-                    const int at = kWholeLines ? ((r16 & 7) + 8 * (c & 1)) * kRow + 128 * (c / 2) + 64 * (r16 >> 3) + 16 * g
-                                               : r16 * kRow + 64 * c + 16 * g;
-                    load_once<4>(w[h].keys + at, kw[h][c]);
-                }
+                for (int c = 0; c < kKeyLoads; ++c)
+                    load_once<4>(w[h].keys + (at + (kWholeLines ? 8 * (c & 1) * kRow + 128 * (c / 2) : 64 * c)),
+                                 b.kw[h][c]);
+            keep_order();
+        };
+        auto load_values = [&](Stage &b, const Where (&w)[2], int live) {
+            keep_order();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if constexpr (kF8)
+                    b.vs[h] = *reinterpret_cast<const uint32_t *>(w[h].scales + a.cache.page + 4 * g);
+            const int at = (4 * g * kRow + r16 * (4 * kValWords)) & live;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    load_once<kValWords>(w[h].keys + values + (at + j * kRow), b.vw[4 * h + j]);
             keep_order();
         };
         // Lines to rows: lane r16 has half r16 / 8 of tokens r16 % 8 and 8 + r16 % 8, and wants both halves of token r16.
-        auto key_rows = [&](int h) {
+        auto key_rows = [&](Stage &b, int h) {
             if constexpr (kWholeLines) {
 #pragma unroll
                 for (int c = 0; c < kKeyLoads; c += 2)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int low = (int)kw[h][c][i], high = (int)kw[h][c + 1][i];
-                        kw[h][c][i] = (uint32_t)__builtin_amdgcn_update_dpp(low, high, 0x128, 0xF, 0xC, false);
-                        kw[h][c + 1][i] = (uint32_t)__builtin_amdgcn_update_dpp(high, low, 0x128, 0xF, 0x3, false);
+                        const int low = (int)b.kw[h][c][i], high = (int)b.kw[h][c + 1][i];
+                        b.kw[h][c][i] = (uint32_t)__builtin_amdgcn_update_dpp(low, high, 0x128, 0xF, 0xC, false);
+                        b.kw[h][c + 1][i] = (uint32_t)__builtin_amdgcn_update_dpp(high, low, 0x128, 0xF, 0x3, false);
                     }
             }
-        };
-        auto load_values = [&](const Where (&w)[2]) {
-            keep_order();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if constexpr (kF8)
-                    vs[h] = *reinterpret_cast<const uint32_t *>(w[h].scales + a.cache.page + 4 * g);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    load_once<kValWords>(w[h].keys + values + ((4 * g + j) * kRow + r16 * (4 * kValWords)), vw[4 * h + j]);
-            keep_order();
         };
 
         f4_t acc[kTiles][kOut];
@@ -429,20 +444,23 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
         int token = first;
         const int end = min(seq.first + t1 * kTile, seq.len);
         if (token < end) {
-            // pages a step ahead of the loads, loads a half step ahead of their products
-            int page[2] = {page_of(token), page_of(token + 16)};
-            Where now[2] = {where(page[0], token), where(page[1], token + 16)};
-            load_keys(now);
-            load_values(now);
-            int ahead = token + kTile < end ? token + kTile : token;
-            page[0] = page_of(ahead), page[1] = page_of(ahead + 16);
+            // pages a step ahead of their loads, loads a half step ahead of their products (another set of registers,
+            // and loads a whole step ahead, gained nothing: 92 us for 92, 142 for 143, 88 for 83 on 256 dimensions)
+            int next = token, page[2] = {page_of(next), page_of(next + 16)};
+            Stage b;
+            {
+                const Where now[2] = {where(page[0], next), where(page[1], next + 16)};
+                load_keys(b, now, -1);
+                load_values(b, now, -1);
+                next += kTile;
+                page[0] = page_of(next), page[1] = page_of(next + 16);
+            }
             for (;;) {
-                const bool there[2] = {now[0].there, now[1].there};
                 // scores
                 float s[kTiles][8];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    key_rows(h);
+                    key_rows(b, h);
                     f4_t c[kTiles];
 #pragma unroll
                     for (int n = 0; n < kTiles; ++n)
@@ -451,11 +469,11 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                     for (int st = 0; st < kSteps; ++st) {
                         typename Q::v8 k;
                         if constexpr (kF8) {
-                            const uint32_t (&w)[4] = kw[h][st / 2];
-                            const float to = kScaledKeys ? f8_exponent(ks[h]) : 1.0f;
+                            const uint32_t (&w)[4] = b.kw[h][st / 2];
+                            const float to = kScaledKeys ? f8_exponent(b.ks[h]) : 1.0f;
                             k = (st & 1) ? widen8<TQ>(w[2], w[3], to) : widen8<TQ>(w[0], w[1], to);
                         } else {
-                            k = __builtin_bit_cast(typename Q::v8, kw[h][st]);
+                            k = __builtin_bit_cast(typename Q::v8, b.kw[h][st]);
                         }
 #pragma unroll
                         for (int n = 0; n < kTiles; ++n)
@@ -467,13 +485,15 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                         for (int n = 0; n < kTiles; ++n) {
                             s[n][4 * h + i] = c[n][i] * scale;
                             if constexpr (kF8 && !kScaledKeys)
-                                s[n][4 * h + i] = ldexpf(s[n][4 * h + i], exponent_of(ks[h], i));
+                                s[n][4 * h + i] = ldexpf(s[n][4 * h + i], exponent_of(b.ks[h], i));
                         }
                     }
                 }
-                // the next step's keys
-                now[0] = where(page[0], ahead), now[1] = where(page[1], ahead + 16);
-                load_keys(now);
+                const bool whole_tiles = b.there[0] && b.there[1], there[2] = {b.there[0], b.there[1]};
+                // the keys of a step to come
+                const int live = next < end ? -1 : 0;
+                const Where now[2] = {where(page[0], next), where(page[1], next + 16)};
+                load_keys(b, now, live);
                 if (a.softcap > 0.0f) {
 #pragma unroll
                     for (int n = 0; n < kTiles; ++n)
@@ -481,7 +501,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                         for (int i = 0; i < 8; ++i)   // cap tanh(x) log2 e, from e^2x
                             s[n][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[n][i] * (2.0f * kLog2e)));
                 }
-                if (edge(token) || !there[0] || !there[1]) {
+                if (edge(token) || !whole_tiles) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int at = token + 16 * (i / 4) + 4 * g + (i & 3);
@@ -496,11 +516,11 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 #pragma unroll
                         for (int c = 0; c < kValWords; ++c) {
                             if (!seen)
-                                vw[i][c] = 0;
+                                b.vw[i][c] = 0;
                             // 0 times what is not finite is not 0: what some rows see and others do not comes afterwards
-                            const uint32_t odd = not_finite<TQ, kF8>(vw[i][c]);
+                            const uint32_t odd = not_finite<TQ, kF8>(b.vw[i][c]);
                             if (a.M > 1 && odd) {
-                                vw[i][c] &= ~odd;
+                                b.vw[i][c] &= ~odd;
                                 left_out = true;
                             }
                         }
@@ -532,7 +552,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                         sum[n] += e;
                         w[i] = e * kWeight;
                         if constexpr (kF8)   // (of 0 too: the scale of a place without a token may be anything)
-                            w[i] = ldexpf(e, exponent_of(vs[i / 4], i & 3));
+                            w[i] = ldexpf(e, exponent_of(b.vs[i / 4], i & 3));
                     }
                     u4_t h4, l4;
 #pragma unroll
@@ -547,8 +567,8 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 #pragma unroll
                 for (int c = 0; c < kValWords; ++c) {
                     if constexpr (kF8) {
-                        const u4_t x = turn4(vw[0][c], vw[1][c], vw[2][c], vw[3][c]);
-                        const u4_t y = turn4(vw[4][c], vw[5][c], vw[6][c], vw[7][c]);
+                        const u4_t x = turn4(b.vw[0][c], b.vw[1][c], b.vw[2][c], b.vw[3][c]);
+                        const u4_t y = turn4(b.vw[4][c], b.vw[5][c], b.vw[6][c], b.vw[7][c]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             add(widen8<TV>(x[i], y[i]), hi, lo, 4 * c + i);
@@ -556,20 +576,20 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t half = i ? 0x07060302 : 0x05040100;
-                            add(__builtin_bit_cast(typename V::v8, u4_t{__builtin_amdgcn_perm(vw[1][c], vw[0][c], half),
-                                                                        __builtin_amdgcn_perm(vw[3][c], vw[2][c], half),
-                                                                        __builtin_amdgcn_perm(vw[5][c], vw[4][c], half),
-                                                                        __builtin_amdgcn_perm(vw[7][c], vw[6][c], half)}),
+                            add(__builtin_bit_cast(typename V::v8, u4_t{__builtin_amdgcn_perm(b.vw[1][c], b.vw[0][c], half),
+                                                                        __builtin_amdgcn_perm(b.vw[3][c], b.vw[2][c], half),
+                                                                        __builtin_amdgcn_perm(b.vw[5][c], b.vw[4][c], half),
+                                                                        __builtin_amdgcn_perm(b.vw[7][c], b.vw[6][c], half)}),
                                 hi, lo, 2 * c + i);
                         }
                     }
                 }
-                load_values(now);
+                load_values(b, now, live);
                 token += kTile;
                 if (token >= end)
                     break;
-                ahead = token + kTile < end ? token + kTile : token;
-                page[0] = page_of(ahead), page[1] = page_of(ahead + 16);
+                next += kTile;
+                page[0] = page_of(next), page[1] = page_of(next + 16);
             }
         }
 
@@ -667,22 +687,28 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
             }
         }
         tile = p.base + t1;
-        if (tile >= run_end)
+        if (tile >= run_end || la.by_sequence)
             break;
         p.base += seq.tiles;
         ++p.b;
     }
 }
 
-// Joins the parts of a row: a workgroup per row of a sequence and key head,
-// 16-byte pieces of D in consecutive threads, the parts over the rest.
-template <typename TQ, int D>
+// Joins the parts of a row: kWavesRow waves (all four, or one where rows are
+// many: 3840 rows 9.8 us with four, JOINUS with one), 16-byte pieces of D in
+// consecutive lanes, the parts over the rest.
+template <typename TQ, int D, int kWavesRow>
 __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
 {
-    constexpr int kPer = D / 4, kRows = kBlock / kPer;
+    constexpr int kPer = D / 4, kRows = 64 * kWavesRow / kPer, kThreads = 64 * kWavesRow;
     const AttendArgs &a = la.a;
     const int heads = a.cache.heads;
-    const int row = blockIdx.x % la.rows, head = (blockIdx.x / la.rows) % heads, b = blockIdx.x / (la.rows * heads);
+    const int number = blockIdx.x * (kBlock / kThreads) + (kWavesRow == 1 ? (int)threadIdx.x / 64 : 0);
+    if (number >= a.B * heads * la.rows)
+        return;
+    const int thread = threadIdx.x % kThreads;
+    const int row = number % la.rows, head = (number / la.rows) % heads;
+    const int b = __builtin_amdgcn_readfirstlane(number / (la.rows * heads));
     const Plan p = plan<false>(a, la.target, b);
     const int from_run = p.base / p.run, n = (p.base + sequence(a, b).tiles - 1) / p.run - from_run + 1;
     if (n == 1)
@@ -690,42 +716,62 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
     const Parts parts = parts_at(a.workspace, la.units, heads, la.rows, D);
     const int64_t stride = (int64_t)heads * la.rows;
     const int64_t at0 = (int64_t)(from_run + b) * stride + (int64_t)head * la.rows + row;
-    __shared__ float o[kRows][D], ml[2][kWaves];
-    const int lane = threadIdx.x % kPer, mine = threadIdx.x / kPer;
+    __shared__ float o[kWavesRow == 1 ? 1 : kRows][D], ml[2][kWaves];
+    const int lane = thread % kPer, mine = thread / kPer;
     // the largest maximum and the sum under it: a part a thread
     float m = -__builtin_inff();
-    for (int c = threadIdx.x; c < n; c += kBlock)
+    for (int c = thread; c < n; c += kThreads)
         m = fmaxf(m, parts.ml[2 * (at0 + c * stride)]);
     m = wave_max(m);
-    if ((threadIdx.x & 63) == 0)
-        ml[0][threadIdx.x >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(ml[0][0], ml[0][1]), fmaxf(ml[0][2], ml[0][3]));
+    if constexpr (kWavesRow > 1) {
+        if ((threadIdx.x & 63) == 0)
+            ml[0][threadIdx.x >> 6] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(ml[0][0], ml[0][1]), fmaxf(ml[0][2], ml[0][3]));
+    }
     const float from = m == -__builtin_inff() ? 0.0f : m;
     float total = 0.0f;
-    for (int c = threadIdx.x; c < n; c += kBlock) {
+    for (int c = thread; c < n; c += kThreads) {
         const int64_t at = at0 + c * stride;
         total += parts.ml[2 * at + 1] * __builtin_amdgcn_exp2f(parts.ml[2 * at] - from);
     }
     total = wave_sum(total);
-    if ((threadIdx.x & 63) == 0)
-        ml[1][threadIdx.x >> 6] = total;
     f4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (mine < kRows) {
 #pragma unroll 8
         for (int c = mine; c < n; c += kRows) {
             const int64_t at = at0 + c * stride;
-            v += *reinterpret_cast<const f4_t *>(parts.o + at * D + 4 * lane) * __builtin_amdgcn_exp2f(parts.ml[2 * at] - from);
+            v += *reinterpret_cast<const f4_t *>(parts.o + at * D + 4 * lane) *
+                 __builtin_amdgcn_exp2f(parts.ml[2 * at] - from);
         }
-        *reinterpret_cast<f4_t *>(&o[mine][4 * lane]) = v;
     }
-    __syncthreads();
+    if constexpr (kWavesRow > 1) {
+        if ((threadIdx.x & 63) == 0)
+            ml[1][threadIdx.x >> 6] = total;
+        if (mine < kRows)
+            *reinterpret_cast<f4_t *>(&o[mine][4 * lane]) = v;
+        __syncthreads();
+        total = (ml[1][0] + ml[1][1]) + (ml[1][2] + ml[1][3]);
+        if (mine == 0) {
+#pragma unroll
+            for (int r = 1; r < kRows; ++r)
+                v += *reinterpret_cast<const f4_t *>(&o[r][4 * lane]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kRows >= 4) {
+                const f2_t x = pair16(v[i]);
+                v[i] = x[0] + x[1];
+            }
+            if constexpr (kRows >= 2) {
+                const f2_t x = pair32(v[i]);
+                v[i] = x[0] + x[1];
+            }
+        }
+    }
     if (mine > 0)
         return;
-    total = (ml[1][0] + ml[1][1]) + (ml[1][2] + ml[1][3]);
-#pragma unroll
-    for (int r = 1; r < kRows; ++r)
-        v += *reinterpret_cast<const f4_t *>(&o[r][4 * lane]);
     const float inverse = 1.0f / total;
     if (total == 0.0f)
         v = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -748,21 +794,32 @@ int tiles_of_rows(int rows, int D)
 struct Cut {
     int rows, tiles, row_groups, target;
     int64_t units;
-    bool join;
+    bool by_sequence;
 };
 
-Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page, int64_t width)
+Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page, int64_t width, int window)
 {
     Cut c;
     c.rows = M * (q_heads / kv_heads);
     c.tiles = tiles_of_rows(c.rows, dim);
     c.row_groups = (c.rows + 16 * c.tiles - 1) / (16 * c.tiles);
     c.target = std::max(1, kRounds * kUnits * resident(dim, f8, c.tiles) / (kv_heads * c.row_groups));
-    // no sequence has more tiles than this (a window's first one may be cut): no more runs than tiles
-    const int64_t most = ceil_div(width * page, kTile) + 1;
+    // no sequence has more tiles than this: no more runs than tiles
+    const int64_t places = window ? std::min<int64_t>(width * page, (int64_t)window + M + 16) : width * page;
+    const int64_t most = ceil_div(places, kTile);
     c.target = (int)std::min<int64_t>(c.target, B * most);
     c.units = c.target + B;
-    c.join = c.target > 1 && width * page > kTile;
+    // A workgroup a sequence: no plan, no second launch (5 us), but the longest sequence is one workgroup's.  Measured
+    // (us, runs / a sequence each; f8, D 128, 8 key heads, lengths from 0 to the table's): 1 sequence of 333 9.7 / 7.3,
+    // of 1000 9.8 / 11.7 (with the host's part of a second launch 14.4 / 12.1), of 2000 10.2 / 19.0; 32 of up to 2000
+    // 22.7 / 19.8, of 4000 32.6 / 35.6; 64 of 4000 49 / 47; 128 of 2000 58 / 47, of 4000 91 / 84.  By bytes of a key
+    // head's longest sequence; in bf16 64 of 8190 147 / 167; where a window makes all of them equal the last round of
+    // workgroups costs what the plan does.
+    const int64_t bytes = most * kTile * dim * (f8 ? 2 : 4), groups = B * kv_heads * c.row_groups;
+    c.by_sequence = bytes <= 256 << 10 ||
+                    (!window && ((bytes <= 512 << 10 && groups >= 256) || (bytes <= 1024 << 10 && groups >= 512)));
+    if (c.by_sequence)
+        c.target = (int)B;
     return c;
 }
 
@@ -779,11 +836,13 @@ hipError_t launch(const AttendLaunch &la, const Cut &c, hipStream_t stream)
     const hipError_t e = launch_kernel(reinterpret_cast<const void *>(fn),
                                        dim3((unsigned)(c.target * la.a.cache.heads * c.row_groups)), dim3(kBlock), 0,
                                        stream, la);
-    if (e != hipSuccess || !c.join)
+    if (e != hipSuccess || c.by_sequence)
         return e;
-    void (*join)(AttendLaunch) = &join_kernel<TQ, D>;
-    return launch_kernel(reinterpret_cast<const void *>(join), dim3((unsigned)(la.a.B * la.a.cache.heads * c.rows)),
-                         dim3(kBlock), 0, stream, la);
+    const int64_t rows = (int64_t)la.a.B * la.a.cache.heads * c.rows;
+    const bool many = rows >= kManyRows;
+    void (*join)(AttendLaunch) = many ? &join_kernel<TQ, D, 1> : &join_kernel<TQ, D, kWaves>;
+    return launch_kernel(reinterpret_cast<const void *>(join),
+                         dim3((unsigned)(many ? ceil_div(rows, kBlock / 64) : rows)), dim3(kBlock), 0, stream, la);
 }
 
 template <typename TQ, bool kF8>
@@ -801,14 +860,16 @@ hipError_t of_dim(const AttendLaunch &la, const Cut &c, hipStream_t stream)
 
 size_t attend_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int cache_type, int page, int64_t width)
 {
-    const Cut c = cut(B, M, q_heads, kv_heads, dim, cache_type == QG_F8, page, width);
-    return c.join ? (size_t)c.units * kv_heads * c.rows * (dim + 2) * sizeof(float) : 0;
+    const Cut c = cut(B, M, q_heads, kv_heads, dim, cache_type == QG_F8, page, width, 0);
+    return !c.by_sequence ? (size_t)c.units * kv_heads * c.rows * (dim + 2) * sizeof(float) : 0;
 }
 
 hipError_t launch_attend(const AttendArgs &a, int q_type, hipStream_t stream)
 {
-    const Cut c = cut(a.B, a.M, a.q_heads, a.cache.heads, a.cache.dim, a.cache.type == QG_F8, a.cache.page, a.width);
-    const AttendLaunch la{a, c.target, (int)c.units, c.rows, c.row_groups};
+    // (a window only makes the parts fewer)
+    const Cut c = cut(a.B, a.M, a.q_heads, a.cache.heads, a.cache.dim, a.cache.type == QG_F8, a.cache.page, a.width,
+                      a.window);
+    const AttendLaunch la{a, c.target, (int)c.units, c.rows, c.row_groups, c.by_sequence};
     if (a.cache.type == QG_F8)
         return q_type == QG_F16 ? of_dim<Fp16, true>(la, c, stream) : of_dim<Bf16, true>(la, c, stream);
     return q_type == QG_F16 ? of_dim<Fp16, false>(la, c, stream) : of_dim<Bf16, false>(la, c, stream);
