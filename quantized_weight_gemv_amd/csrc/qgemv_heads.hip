@@ -29,12 +29,18 @@ struct __attribute__((packed, aligned(4))) Raw16f {
 // A lane's eight elements as they lie in memory, loaded ahead of their use.
 template <typename T>
 struct Eight {
-    using Piece = std::conditional_t<sizeof(T) == 4, Raw16f, Raw8>;
+    typedef uint32_t Piece __attribute__((ext_vector_type(sizeof(T)), aligned(sizeof(T))));
     Piece p[2];
+    template <bool kOnce = false>
     __device__ __forceinline__ void load(const T *row, int lo, int hi)
     {
-        p[0] = *reinterpret_cast<const Piece *>(row + lo);
-        p[1] = *reinterpret_cast<const Piece *>(row + hi);
+        if constexpr (kOnce) {
+            p[0] = __builtin_nontemporal_load(reinterpret_cast<const Piece *>(row + lo));
+            p[1] = __builtin_nontemporal_load(reinterpret_cast<const Piece *>(row + hi));
+        } else {
+            p[0] = *reinterpret_cast<const Piece *>(row + lo);
+            p[1] = *reinterpret_cast<const Piece *>(row + hi);
+        }
     }
     // all zeros unless `on`
     template <typename F>
@@ -44,9 +50,9 @@ struct Eight {
         for (int i = 0; i < 8; ++i) {
             float x;
             if constexpr (sizeof(T) == 4)
-                x = __uint_as_float(p[i / 4].w[i & 3]);
+                x = __uint_as_float(p[i / 4][i & 3]);
             else
-                x = to_f32(T{(uint16_t)(p[i / 4].w[(i & 3) / 2] >> (16 * (i & 1)))});
+                x = to_f32(T{(uint16_t)(p[i / 4][(i & 3) / 2] >> (16 * (i & 1)))});
             v[i] = on ? x : 0.0f;
         }
     }
@@ -68,18 +74,20 @@ __device__ __forceinline__ void load4(const T *p, float *v)
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store4(T *p, const float *v)
+// Stores of large outputs leave nothing behind in the caches (kOnce).
+template <bool kOnce, typename T>
+__device__ __forceinline__ void store4(T *p, float a, float b, float c, float d)
 {
-    if constexpr (sizeof(T) == 4) {
-        Raw16f r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r.w[i] = __float_as_uint(v[i]);
-        *reinterpret_cast<Raw16f *>(p) = r;
-    } else {
-        *reinterpret_cast<Raw8 *>(p) = Raw8{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3])};
-    }
+    typedef uint32_t Piece __attribute__((ext_vector_type(sizeof(T)), aligned(sizeof(T))));
+    Piece r;
+    if constexpr (sizeof(T) == 4)
+        r = Piece{__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d)};
+    else
+        r = Piece{pack2<T>(a, b), pack2<T>(c, d)};
+    if constexpr (kOnce)
+        __builtin_nontemporal_store(r, reinterpret_cast<Piece *>(p));
+    else
+        *reinterpret_cast<Piece *>(p) = r;
 }
 
 // A lane's eight elements from `lo` and `hi` of a vector; the type is the
@@ -97,19 +105,28 @@ __device__ __forceinline__ void load8_as(int type, const void *base, int64_t at,
         load4(static_cast<const Bf16 *>(base) + at + hi, v + 4);
     }
 }
+template <bool kOnce, typename T>
+__device__ __forceinline__ void store8(T *row, int lo, int hi, const float (&v)[8])
+{
+    store4<kOnce>(row + lo, v[0], v[1], v[2], v[3]);
+    store4<kOnce>(row + hi, v[4], v[5], v[6], v[7]);
+}
+template <bool kOnce = false>
 __device__ __forceinline__ void store8_as(int type, void *base, int64_t at, int lo, int hi, const float (&v)[8])
 {
-    if (type == QG_F32) {
-        store4(static_cast<float *>(base) + at + lo, v);
-        store4(static_cast<float *>(base) + at + hi, v + 4);
-    } else if (type == QG_F16) {
-        store4(static_cast<Fp16 *>(base) + at + lo, v);
-        store4(static_cast<Fp16 *>(base) + at + hi, v + 4);
-    } else {
-        store4(static_cast<Bf16 *>(base) + at + lo, v);
-        store4(static_cast<Bf16 *>(base) + at + hi, v + 4);
-    }
+    // (a copy in front of the branches keeps the values in registers)
+    const float w[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+    if (type == QG_F32)
+        store8<kOnce>(static_cast<float *>(base) + at, lo, hi, w);
+    else if (type == QG_F16)
+        store8<kOnce>(static_cast<Fp16 *>(base) + at, lo, hi, w);
+    else
+        store8<kOnce>(static_cast<Bf16 *>(base) + at, lo, hi, w);
 }
+
+// (the declarations of fp32 stand beside those of 64 bits)
+using qg::dpp;
+using qg::group_sum;
 
 template <int kCtrl>
 __device__ __forceinline__ double dpp(double v)
@@ -157,9 +174,10 @@ __device__ __forceinline__ Place place(int D, int half, bool interleaved)
     p.l = lane % L;
     p.on = 8 * p.l < D;
     p.turned = p.on && 4 * p.l < half;
-    const bool halves = p.turned && !interleaved;
+    // (nothing turned: halves of the vector, whose pieces are whole lines over the lanes)
+    const bool halves = half == 0 || (p.turned && !interleaved);
     p.lo = halves ? 4 * p.l : 8 * p.l;
-    p.hi = halves ? half + 4 * p.l : 8 * p.l + 4;
+    p.hi = halves ? (half ? half : D / 2) + 4 * p.l : 8 * p.l + 4;
     return p;
 }
 
@@ -343,7 +361,7 @@ __device__ __forceinline__ void norm_turn(const HeadArgs &a, const Place &p, con
 // token unit / parts: query heads, key heads and, when they are written to a
 // cache, value heads.  The next group is loaded ahead; the first one lies behind
 // the cosines.
-template <typename T, int L, bool kWrite, bool kF8>
+template <typename T, int L, bool kWrite, bool kF8, bool kOnce>
 __global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
 {
     const Place p = place<L>(a.D, a.half, a.interleaved);
@@ -380,7 +398,7 @@ __global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
             const void *base = kind == 0 ? a.x[0] : kind == 1 ? a.x[1] : a.x[2];
             const int64_t ld = kind == 0 ? a.ldx[0] : kind == 1 ? a.ldx[1] : a.ldx[2];
             if (on)
-                x.load(static_cast<const T *>(base) + t * ld + head * a.D, p.lo, p.hi);
+                x.template load<kWrite>(static_cast<const T *>(base) + t * ld + head * a.D, p.lo, p.hi);
         };
         fetch(first);
         float c[4], s[4];
@@ -416,13 +434,13 @@ __global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
             if (group < k0) {
                 norm_turn<L>(a, p, gain[0], c, s, v);
                 if (is)
-                    store8_as(a.y_type, a.y[0], t * a.ldy[0] + h * a.D, p.lo, p.hi, v);
+                    store8_as<kOnce>(a.y_type, a.y[0], t * a.ldy[0] + h * a.D, p.lo, p.hi, v);
             } else if (group < v0) {
                 norm_turn<L>(a, p, gain[1], c, s, v);
                 if constexpr (kWrite)
                     put<L>(a.cache, slot, h, 0, is, p.l, p.lo, p.hi, v);
                 else if (is)
-                    store8_as(a.y_type, a.y[1], t * a.ldy[1] + h * a.D, p.lo, p.hi, v);
+                    store8_as<kOnce>(a.y_type, a.y[1], t * a.ldy[1] + h * a.D, p.lo, p.hi, v);
             } else if constexpr (kWrite) {
                 put<L>(a.cache, slot, h, 1, is, p.l, p.lo, p.hi, v);
             }
@@ -434,7 +452,7 @@ __global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
 // normed row:  dgain += h n,  dx = r (h gain - n mean(h gain n)).  A lane keeps
 // its eight sums of each gain over all the heads and tokens of its wave; the
 // workgroup leaves one row of sums.
-template <typename T, typename TY, int L>
+template <typename T, typename TY, int L, bool kOnce>
 __global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
 {
     const HeadArgs &a = ga.h;
@@ -510,8 +528,7 @@ __global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
             }
             if (is) {
                 T *to = static_cast<T *>(ga.g[k]) + t * ga.ldg[k] + at * a.D;
-                store4(to + p.lo, h);
-                store4(to + p.hi, h + 4);
+                store8<kOnce>(to, p.lo, p.hi, h);
             }
         };
         for (int group = first; group < min(last, k0); ++group)
@@ -542,21 +559,28 @@ __global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
     }
 }
 
-// The workgroups' rows of sums, 16 columns a workgroup, 16 threads a column.
-__global__ __launch_bounds__(kBlock) void gain_join_kernel(HeadGradArgs ga)
+// The workgroups' rows of sums, 16 columns a workgroup, 64 threads a column.
+__global__ __launch_bounds__(1024) void gain_join_kernel(HeadGradArgs ga)
 {
-    __shared__ double sums[16][16];
+    __shared__ double sums[64][17];
     const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
     const int at = blockIdx.x * 16 + col, width = 2 * ga.h.D;
     double sum = 0.0;
 #pragma unroll 8
-    for (int r = row; r < ga.groups_of_work; r += 16)
+    for (int r = row; r < ga.groups_of_work; r += 64)
         sum += (double)ga.workspace[(int64_t)r * width + at];
     sums[row][col] = sum;
     __syncthreads();
+    if (row < 8) {
+#pragma unroll
+        for (int r = 8; r < 64; r += 8)
+            sum += sums[row + r][col];
+        sums[row][col] = sum;
+    }
+    __syncthreads();
     if (row == 0) {
 #pragma unroll
-        for (int r = 1; r < 16; ++r)
+        for (int r = 1; r < 8; ++r)
             sum += sums[r][col];
         ga.g_gain[at] = (float)sum;
     }
@@ -575,20 +599,17 @@ __global__ __launch_bounds__(kBlock) void kv_write_kernel(KvArgs a)
         if (v < vectors)
             slot = a.slots[t];
         const bool on = (uint32_t)slot < (uint32_t)a.cache.pages << a.cache.log_page && 8 * l < a.cache.dim;
+        Eight<T> in;
+        if (on)
+            in.load(static_cast<const T *>(kv ? a.v : a.k) + t * (kv ? a.ldv : a.ldk) + head * a.cache.dim, 4 * l,
+                    a.cache.dim / 2 + 4 * l);
         float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = 0.0f;
-        if (on) {
-            const T *from = static_cast<const T *>(kv ? a.v : a.k) + t * (kv ? a.ldv : a.ldk) + head * a.cache.dim + 8 * l;
-            load4(from, x);
-            load4(from + 4, x + 4);
-        }
-        put<L>(a.cache, slot, head, kv, on, l, 8 * l, 8 * l + 4, x);
+        in.values(on, x);
+        put<L>(a.cache, slot, head, kv, on, l, 4 * l, a.cache.dim / 2 + 4 * l, x);
     }
 }
 
-template <typename TY, int L>
+template <typename TY, int L, bool kOnce>
 __global__ __launch_bounds__(kBlock) void kv_read_kernel(KvArgs a)
 {
     const int64_t vectors = a.T * 2 * a.cache.heads;
@@ -597,7 +618,7 @@ __global__ __launch_bounds__(kBlock) void kv_read_kernel(KvArgs a)
          v += (int64_t)gridDim.x * (kBlock / L)) {
         const int64_t row = v / a.cache.heads, t = row >> 1;
         const int head = (int)(v - row * a.cache.heads), kv = (int)(row & 1);
-        const int slot = a.slots[t];
+        const int slot = a.slots[t], lo = 4 * l, hi = a.cache.dim / 2 + 4 * l;
         if (8 * l >= a.cache.dim)
             continue;
         float x[8];
@@ -607,27 +628,20 @@ __global__ __launch_bounds__(kBlock) void kv_read_kernel(KvArgs a)
         if ((uint32_t)slot < (uint32_t)a.cache.pages << a.cache.log_page) {
             const SlotAt at = slot_at(a.cache, slot, head, kv);
             if (a.cache.type == QG_F8) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(at.codes + 8 * l);
                 const float scale = f8_scale(*at.scale);
-                float u[16];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t q = i ? w.y : w.x;
-                    u[4 * i] = __builtin_amdgcn_cvt_f32_fp8((int)q, 0);
-                    u[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8((int)q, 1);
-                    u[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8((int)q, 2);
-                    u[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8((int)q, 3);
+                    const int w = *reinterpret_cast<const int *>(at.codes + (i ? hi : lo));
+                    x[4 * i] = __builtin_amdgcn_cvt_f32_fp8(w, 0) * scale;
+                    x[4 * i + 1] = __builtin_amdgcn_cvt_f32_fp8(w, 1) * scale;
+                    x[4 * i + 2] = __builtin_amdgcn_cvt_f32_fp8(w, 2) * scale;
+                    x[4 * i + 3] = __builtin_amdgcn_cvt_f32_fp8(w, 3) * scale;
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[i] = u[i] * scale;
             } else {
-                load8_as(a.cache.type, at.codes, 0, 8 * l, 8 * l + 4, x);
+                load8_as(a.cache.type, at.codes, 0, lo, hi, x);
             }
         }
-        TY *to = static_cast<TY *>(kv ? a.yv : a.yk) + (t * a.cache.heads + head) * a.cache.dim + 8 * l;
-        store4(to, x);
-        store4(to + 4, x + 4);
+        store8<kOnce>(static_cast<TY *>(kv ? a.yv : a.yk) + (t * a.cache.heads + head) * a.cache.dim, lo, hi, x);
     }
 }
 
@@ -653,6 +667,17 @@ hipError_t by_type(int type, int D, Pick pick, int64_t grid, const P &a, hipStre
 
 int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
+// Outputs of at least a quarter of the last-level cache: their readers find
+// little of them there, and stores that go past it are faster (16384 tokens of 32
+// + 8 heads of 128 in bf16, forward and backward: 155 us for 172), if the lanes'
+// pieces make whole lines.  Inputs are loaded so only by the call that writes a
+// cache (8192 tokens with 40 query heads: 66 us for 70).
+bool large(int64_t vectors, int D, int type) { return vectors * D * type_bytes(type) >= (int64_t)64 << 20; }
+bool whole_lines(const HeadArgs &a) { return a.half == 0 || (!a.interleaved && 2 * a.half == a.D); }
+
+constexpr int64_t kForwardWaves = 4096;
+constexpr int64_t kBackwardWaves = 4096;
+
 // Groups of heads, and how many waves share a token: as few as give every
 // compute unit its waves, since each takes the token's sines anew.
 void split_heads(HeadArgs &a, int kinds, int64_t waves)
@@ -666,9 +691,6 @@ void split_heads(HeadArgs &a, int kinds, int64_t waves)
     a.parts = (int)std::min<int64_t>(all, ceil_div(waves, a.T));
 }
 
-constexpr int64_t kForwardWaves = 8192;
-constexpr int64_t kBackwardWaves = 4096;
-
 int64_t backward_groups(int64_t T, int heads, int D)
 {
     const int64_t units = std::min<int64_t>(T * ceil_div(heads, 64 / lanes_of(D)), kBackwardWaves);
@@ -681,10 +703,14 @@ hipError_t launch_head_norm_rope(const HeadArgs &args, int x_type, hipStream_t s
 {
     HeadArgs a = args;
     split_heads(a, 2, kForwardWaves);
+    const int64_t grid = ceil_div(a.T * a.parts, kBlock / 64);
+    if (whole_lines(a) && large(a.T * (a.heads[0] + a.heads[1]), a.D, a.y_type))
+        return by_type(
+            x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, false, false, true>; },
+            grid, a, stream);
     return by_type(
-        x_type, a.D,
-        [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, false, false>; },
-        ceil_div(a.T * a.parts, kBlock / 64), a, stream);
+        x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, false, false, false>; },
+        grid, a, stream);
 }
 
 hipError_t launch_head_norm_rope_write(const HeadArgs &args, int x_type, hipStream_t stream)
@@ -694,16 +720,31 @@ hipError_t launch_head_norm_rope_write(const HeadArgs &args, int x_type, hipStre
     const int64_t grid = ceil_div(a.T * a.parts, kBlock / 64);
     if (a.cache.type == QG_F8)
         return by_type(
-            x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, true, true>; },
+            x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, true, true, false>; },
             grid, a, stream);
     return by_type(
-        x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, true, false>; }, grid,
-        a, stream);
+        x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, true, false, false>; },
+        grid, a, stream);
 }
 
 size_t head_backward_workspace(int64_t T, int heads, int D)
 {
     return (size_t)backward_groups(T, heads, D) * 2 * D * sizeof(float);
+}
+
+template <bool kOnce>
+hipError_t backward(const HeadGradArgs &a, int x_type, hipStream_t stream)
+{
+    return by_type(
+        x_type, a.h.D,
+        [&](auto t, auto l) -> void (*)(HeadGradArgs) {
+            using T = decltype(t);
+            constexpr int L = decltype(l)::value;
+            return a.h.y_type == QG_F32   ? &head_backward_kernel<T, float, L, kOnce>
+                   : a.h.y_type == QG_F16 ? &head_backward_kernel<T, Fp16, L, kOnce>
+                                          : &head_backward_kernel<T, Bf16, L, kOnce>;
+        },
+        a.groups_of_work, a, stream);
 }
 
 hipError_t launch_head_norm_rope_backward(const HeadGradArgs &args, int x_type, hipStream_t stream)
@@ -712,19 +753,12 @@ hipError_t launch_head_norm_rope_backward(const HeadGradArgs &args, int x_type, 
     split_heads(a.h, 2, kBackwardWaves);
     a.groups_of_work = (int)std::min(backward_groups(a.h.T, a.h.heads[0] + a.h.heads[1], a.h.D),
                                      ceil_div(a.h.T * a.h.parts, kBlock / 64));
-    const hipError_t e = by_type(
-        x_type, a.h.D,
-        [&](auto t, auto l) -> void (*)(HeadGradArgs) {
-            using T = decltype(t);
-            constexpr int L = decltype(l)::value;
-            return a.h.y_type == QG_F32   ? &head_backward_kernel<T, float, L>
-                   : a.h.y_type == QG_F16 ? &head_backward_kernel<T, Fp16, L>
-                                          : &head_backward_kernel<T, Bf16, L>;
-        },
-        a.groups_of_work, a, stream);
+    const bool once = whole_lines(a.h) && large(a.h.T * (a.h.heads[0] + a.h.heads[1]), a.h.D, x_type);
+    const hipError_t e = once ? backward<true>(a, x_type, stream) : backward<false>(a, x_type, stream);
     if (e != hipSuccess || !a.h.gain[0])
         return e;
-    return go(&gain_join_kernel, a.h.D / 8, a, stream);
+    return launch_kernel(reinterpret_cast<const void *>(&gain_join_kernel), dim3((unsigned)(a.h.D / 8)), dim3(1024), 0,
+                         stream, a);
 }
 
 hipError_t launch_kv_write(const KvArgs &a, int x_type, hipStream_t stream)
@@ -736,9 +770,14 @@ hipError_t launch_kv_write(const KvArgs &a, int x_type, hipStream_t stream)
 
 hipError_t launch_kv_read(const KvArgs &a, int y_type, hipStream_t stream)
 {
+    const int64_t vectors = a.T * 2 * a.cache.heads, grid = ceil_div(vectors, kBlock / lanes_of(a.cache.dim));
+    if (large(vectors, a.cache.dim, y_type))
+        return by_type(
+            y_type, a.cache.dim, [](auto t, auto l) { return &kv_read_kernel<decltype(t), decltype(l)::value, true>; },
+            grid, a, stream);
     return by_type(
-        y_type, a.cache.dim, [](auto t, auto l) { return &kv_read_kernel<decltype(t), decltype(l)::value>; },
-        ceil_div(a.T * 2 * a.cache.heads, kBlock / lanes_of(a.cache.dim)), a, stream);
+        y_type, a.cache.dim, [](auto t, auto l) { return &kv_read_kernel<decltype(t), decltype(l)::value, false>; },
+        grid, a, stream);
 }
 
 }  // namespace qg
