@@ -64,23 +64,24 @@ __device__ __forceinline__ int scalar_int(const int32_t *p, int64_t i)
 // has the same work whatever the lengths are; a run may end inside a sequence
 // and begin the next one.  Run w's part of sequence b is number w + b of all
 // parts (both only grow along the runs).
-struct Plan {
-    int run, total;
-    int b;              // sequence
-    int base;           // its first tile among all
-};
-
 struct Sequence {
     int len;
     int first;          // its first token that anybody sees, down to a multiple of 16
     int tiles;
 };
 
-__device__ __forceinline__ Sequence sequence(const AttendArgs &a, int b)
+struct Plan {
+    int run, total;
+    int b;              // sequence
+    int base;           // its first tile among all
+    Sequence seq;
+};
+
+__device__ __forceinline__ Sequence sequence(const AttendArgs &a, int len)
 {
     const int64_t most = (int64_t)a.width << a.cache.log_page;
     Sequence s;
-    s.len = (int)min((int64_t)max(a.lens[b], 0), most);
+    s.len = (int)min((int64_t)max(len, 0), most);
     s.first = a.window ? max(0, s.len - a.M + 1 - a.window) & ~15 : 0;
     s.tiles = max(1, (s.len - s.first + kTile - 1) / kTile);
     return s;
@@ -93,28 +94,33 @@ __device__ __forceinline__ Plan plan(const AttendArgs &a, int target, int w)
 {
     const int lane = threadIdx.x & 63;
     Plan p{};
-    int mine = 0;
+    int len = 0, mine = 0;
+    auto take = [&](int b0) {
+        const bool is = b0 + lane < a.B;
+        len = is ? a.lens[b0 + lane] : 0;
+        mine = is ? sequence(a, len).tiles : 0;
+    };
     for (int b0 = 0; b0 < a.B; b0 += 64) {
-        mine = b0 + lane < a.B ? sequence(a, b0 + lane).tiles : 0;
+        take(b0);
         p.total += __builtin_amdgcn_readlane(prefix_sum(mine), 63);
     }
     p.run = (p.total + target - 1) / target;
     const int64_t tile = kOfRun ? (int64_t)w * p.run : 0;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
         if (a.B > 64)
-            mine = b0 + lane < a.B ? sequence(a, b0 + lane).tiles : 0;
+            take(b0);
         const int upto = prefix_sum(mine);
+        int at = w - b0;
+        bool here = at < 64;
         if (kOfRun) {
             const unsigned long long holds = __ballot(p.base + (int64_t)upto > tile);
-            if (holds) {
-                const int at = __ffsll(holds) - 1;
-                p.b = b0 + at;
-                p.base += __builtin_amdgcn_readlane(upto - mine, at);
-                return p;
-            }
-        } else if (w < b0 + 64) {
-            p.b = w;
-            p.base += __builtin_amdgcn_readlane(upto - mine, w - b0);
+            here = holds != 0;
+            at = __ffsll(holds) - 1;
+        }
+        if (here) {
+            p.b = b0 + at;
+            p.base += __builtin_amdgcn_readlane(upto - mine, at);
+            p.seq = sequence(a, __builtin_amdgcn_readlane(len, at));
             return p;
         }
         p.base += __builtin_amdgcn_readlane(upto, 63);
@@ -295,6 +301,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
     if (la.by_sequence) {
         p.b = run;
         p.run = p.total = INT32_MAX;
+        p.seq = sequence(a, a.lens[run]);
     } else {
         p = plan<true>(a, la.target, run);
         if (p.b < 0)
@@ -308,7 +315,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 
     // one sequence's part of the run after the other
     for (int tile = run_begin;;) {
-        const Sequence seq = sequence(a, p.b);
+        const Sequence seq = p.seq;
         const int t0 = tile - p.base, t1 = min(seq.tiles, run_end - p.base);
 
         // queries: row r is column r of the first product
@@ -691,6 +698,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
             break;
         p.base += seq.tiles;
         ++p.b;
+        p.seq = sequence(a, scalar_int(a.lens, p.b));
     }
 }
 
@@ -710,7 +718,7 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
     const int row = number % la.rows, head = (number / la.rows) % heads;
     const int b = __builtin_amdgcn_readfirstlane(number / (la.rows * heads));
     const Plan p = plan<false>(a, la.target, b);
-    const int from_run = p.base / p.run, n = (p.base + sequence(a, b).tiles - 1) / p.run - from_run + 1;
+    const int from_run = p.base / p.run, n = (p.base + p.seq.tiles - 1) / p.run - from_run + 1;
     if (n == 1)
         return;
     const Parts parts = parts_at(a.workspace, la.units, heads, la.rows, D);
