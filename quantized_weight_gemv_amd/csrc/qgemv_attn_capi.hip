@@ -117,7 +117,7 @@ size_t qhead_norm_rope_backward_workspace(int64_t T, int q_heads, int k_heads, i
     if (!gains || !tokens_ok(T) || q_heads < 1 || k_heads < 0 || q_heads > kAttnMaxHeads ||
         k_heads > kAttnMaxHeads - q_heads || D < 8 || D > 256 || D % 8)
         return 0;
-    return head_backward_workspace(T, q_heads + k_heads, D);
+    return head_backward_workspace(T, q_heads, k_heads, D);
 }
 
 qg_status qhead_norm_rope_backward(const void *gyq, int64_t ldgq, const void *gyk, int64_t ldgk, int y_type,

@@ -130,7 +130,6 @@ struct HeadArgs {
     void *y[2];
     int64_t ldy[2];
     int y_type;
-    int parts;              // waves that share a token
     const int32_t *slots;
     KvCache cache;
 };
@@ -141,12 +140,12 @@ struct HeadGradArgs {
     int64_t ldg[2];
     float *g_gain;          // [2][D]
     float *workspace;       // [workgroups][2][D]
-    int groups_of_work;     // workgroups
+    int rows;               // of it
 };
 
 hipError_t launch_head_norm_rope(const HeadArgs &a, int x_type, hipStream_t stream);
 hipError_t launch_head_norm_rope_write(const HeadArgs &a, int x_type, hipStream_t stream);
-size_t head_backward_workspace(int64_t T, int heads, int D);
+size_t head_backward_workspace(int64_t T, int q_heads, int k_heads, int D);
 hipError_t launch_head_norm_rope_backward(const HeadGradArgs &a, int x_type, hipStream_t stream);
 
 struct KvArgs {

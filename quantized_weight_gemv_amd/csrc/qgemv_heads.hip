@@ -357,10 +357,9 @@ __device__ __forceinline__ void norm_turn(const HeadArgs &a, const Place &p, con
     turn(p, a.interleaved, c, s, v);
 }
 
-// Wave `unit` of the launch takes part unit % parts of the groups of heads of
-// token unit / parts: query heads, key heads and, when they are written to a
-// cache, value heads.  The next group is loaded ahead; the first one lies behind
-// the cosines.
+// A wave takes the blockIdx.y-th part of a token's groups of heads: query heads,
+// key heads and, when they are written to a cache, value heads.  The next group is
+// loaded ahead; the first one lies behind the cosines.
 template <typename T, int L, bool kWrite, bool kF8, bool kOnce>
 __global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
 {
@@ -371,13 +370,10 @@ __global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
         load8_as(a.gain_type, a.gain[0], 0, p.lo, p.hi, gain[0]);
         load8_as(a.gain_type, a.gain[1], 0, p.lo, p.hi, gain[1]);
     }
-    const int64_t units = a.T * a.parts;
-    for (int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-         unit < units; unit += (int64_t)gridDim.x * (kBlock / 64)) {
-        const int64_t t = unit / a.parts;
-        const int part = (int)(unit - t * a.parts);
-        const int first = (int)((int64_t)part * all / a.parts);
-        int last = (int)((int64_t)(part + 1) * all / a.parts);
+    const int first = (int)(blockIdx.y * all / gridDim.y), upto = (int)((blockIdx.y + 1) * all / gridDim.y);
+    for (int64_t t = (int64_t)blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); t < a.T;
+         t += (int64_t)gridDim.x * (kBlock / 64)) {
+        int last = upto;
         int slot = 0;
         if constexpr (kWrite) {
             if (last > k0) {
@@ -470,12 +466,8 @@ __global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
             load8_as(a.gain_type, a.gain[k], 0, p.lo, p.hi, gain[k]);
     }
     const int all = a.groups[0] + a.groups[1];
-    const int64_t units = a.T * a.parts;
-    for (int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + wave; unit < units;
-         unit += (int64_t)gridDim.x * (kBlock / 64)) {
-        const int64_t t = unit / a.parts;
-        const int part = (int)(unit - t * a.parts);
-        const int first = (int)((int64_t)part * all / a.parts), last = (int)((int64_t)(part + 1) * all / a.parts);
+    const int first = (int)(blockIdx.y * all / gridDim.y), last = (int)((blockIdx.y + 1) * all / gridDim.y);
+    for (int64_t t = (int64_t)blockIdx.x * (kBlock / 64) + wave; t < a.T; t += (int64_t)gridDim.x * (kBlock / 64)) {
         Eight<T> x;
         Eight<TY> dy;
         int head;
@@ -555,7 +547,7 @@ __global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
 #pragma unroll
             for (int j = 0; j < 64 / L; ++j)
                 sum += sums[w][k][j][at];
-        ga.workspace[(int64_t)blockIdx.x * 2 * a.D + i] = sum;
+        ga.workspace[((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.D + i] = sum;
     }
 }
 
@@ -567,7 +559,7 @@ __global__ __launch_bounds__(1024) void gain_join_kernel(HeadGradArgs ga)
     const int at = blockIdx.x * 16 + col, width = 2 * ga.h.D;
     double sum = 0.0;
 #pragma unroll 8
-    for (int r = row; r < ga.groups_of_work; r += 64)
+    for (int r = row; r < ga.rows; r += 64)
         sum += (double)ga.workspace[(int64_t)r * width + at];
     sums[row][col] = sum;
     __syncthreads();
@@ -586,47 +578,71 @@ __global__ __launch_bounds__(1024) void gain_join_kernel(HeadGradArgs ga)
     }
 }
 
+// The vectors of a token ([keys, values][head]) over the groups of L lanes: a
+// wave takes several tokens where they fit, or blockIdx.y-th part of one token's.
+// (Found once a wave: a division for each vector had kept the vector units busy
+// 97 % of the time.)
+template <int L>
+struct KvPlace {
+    int l;              // lane of the vector
+    int head, kv;
+    int64_t token;      // first token
+    int64_t step;
+    bool on;
+    __device__ __forceinline__ KvPlace(const KvArgs &a)
+    {
+        constexpr int kGroups = 64 / L;
+        const int all = 2 * a.cache.heads, group = (threadIdx.x & 63) / L;
+        const int per = all <= kGroups ? kGroups / all : 1;
+        const int of = all <= kGroups ? group / all : 0;
+        const int j = (int)blockIdx.y * kGroups + group - of * all;
+        const int64_t wave = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
+        l = threadIdx.x % L;
+        kv = j >= a.cache.heads ? 1 : 0;
+        head = j - kv * a.cache.heads;
+        token = wave * per + of;
+        step = (int64_t)gridDim.x * (kBlock / 64) * per;
+        on = of < per && j < all && 8 * l < a.cache.dim;
+    }
+};
+
 template <typename T, int L>
 __global__ __launch_bounds__(kBlock) void kv_write_kernel(KvArgs a)
 {
-    const int64_t vectors = a.T * 2 * a.cache.heads;
-    const int l = threadIdx.x % L;
-    for (int64_t v0 = (int64_t)blockIdx.x * (kBlock / L); v0 < vectors; v0 += (int64_t)gridDim.x * (kBlock / L)) {
-        const int64_t v = v0 + threadIdx.x / L;
-        const int64_t row = v / a.cache.heads, t = row >> 1;
-        const int head = (int)(v - row * a.cache.heads), kv = (int)(row & 1);
-        int slot = -1;
-        if (v < vectors)
-            slot = a.slots[t];
-        const bool on = (uint32_t)slot < (uint32_t)a.cache.pages << a.cache.log_page && 8 * l < a.cache.dim;
+    const KvPlace<L> p(a);
+    const int lo = 4 * p.l, hi = a.cache.dim / 2 + 4 * p.l;
+    const T *from = static_cast<const T *>(p.kv ? a.v : a.k) + p.head * a.cache.dim;
+    const int64_t ld = p.kv ? a.ldv : a.ldk;
+    // (lanes of a vector, and so of a group that is quantized together, have one token)
+    for (int64_t t = p.token; t < a.T; t += p.step) {
+        const int slot = a.slots[t];
+        const bool on = p.on && (uint32_t)slot < (uint32_t)a.cache.pages << a.cache.log_page;
         Eight<T> in;
         if (on)
-            in.load(static_cast<const T *>(kv ? a.v : a.k) + t * (kv ? a.ldv : a.ldk) + head * a.cache.dim, 4 * l,
-                    a.cache.dim / 2 + 4 * l);
+            in.load(from + t * ld, lo, hi);
         float x[8];
         in.values(on, x);
-        put<L>(a.cache, slot, head, kv, on, l, 4 * l, a.cache.dim / 2 + 4 * l, x);
+        put<L>(a.cache, slot, p.head, p.kv, on, p.l, lo, hi, x);
     }
 }
 
 template <typename TY, int L, bool kOnce>
 __global__ __launch_bounds__(kBlock) void kv_read_kernel(KvArgs a)
 {
-    const int64_t vectors = a.T * 2 * a.cache.heads;
-    const int l = threadIdx.x % L;
-    for (int64_t v = (int64_t)blockIdx.x * (kBlock / L) + threadIdx.x / L; v < vectors;
-         v += (int64_t)gridDim.x * (kBlock / L)) {
-        const int64_t row = v / a.cache.heads, t = row >> 1;
-        const int head = (int)(v - row * a.cache.heads), kv = (int)(row & 1);
-        const int slot = a.slots[t], lo = 4 * l, hi = a.cache.dim / 2 + 4 * l;
-        if (8 * l >= a.cache.dim)
-            continue;
+    const KvPlace<L> p(a);
+    if (!p.on)
+        return;
+    const int lo = 4 * p.l, hi = a.cache.dim / 2 + 4 * p.l;
+    TY *to = static_cast<TY *>(p.kv ? a.yv : a.yk) + p.head * a.cache.dim;
+    const int64_t ld = (int64_t)a.cache.heads * a.cache.dim;
+    for (int64_t t = p.token; t < a.T; t += p.step) {
+        const int slot = a.slots[t];
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             x[i] = 0.0f;
         if ((uint32_t)slot < (uint32_t)a.cache.pages << a.cache.log_page) {
-            const SlotAt at = slot_at(a.cache, slot, head, kv);
+            const SlotAt at = slot_at(a.cache, slot, p.head, p.kv);
             if (a.cache.type == QG_F8) {
                 const float scale = f8_scale(*at.scale);
 #pragma unroll
@@ -641,20 +657,19 @@ __global__ __launch_bounds__(kBlock) void kv_read_kernel(KvArgs a)
                 load8_as(a.cache.type, at.codes, 0, lo, hi, x);
             }
         }
-        store8<kOnce>(static_cast<TY *>(kv ? a.yv : a.yk) + (t * a.cache.heads + head) * a.cache.dim, lo, hi, x);
+        store8<kOnce>(to + t * ld, lo, hi, x);
     }
 }
 
 template <typename P>
-hipError_t go(void (*fn)(P), int64_t grid, const P &a, hipStream_t stream)
+hipError_t go(void (*fn)(P), dim3 grid, const P &a, hipStream_t stream)
 {
-    return launch_kernel(reinterpret_cast<const void *>(fn), dim3((unsigned)std::min<int64_t>(grid, kMaxBlocks)),
-                         dim3(kBlock), 0, stream, a);
+    return launch_kernel(reinterpret_cast<const void *>(fn), grid, dim3(kBlock), 0, stream, a);
 }
 
 // fn<T, L> of the element type and of the lanes that a head takes.
 template <typename P, typename Pick>
-hipError_t by_type(int type, int D, Pick pick, int64_t grid, const P &a, hipStream_t stream)
+hipError_t by_type(int type, int D, Pick pick, dim3 grid, const P &a, hipStream_t stream)
 {
     auto lanes = [&](auto t) {
         return D <= 64    ? pick(t, std::integral_constant<int, 8>{})
@@ -678,23 +693,35 @@ bool whole_lines(const HeadArgs &a) { return a.half == 0 || (!a.interleaved && 2
 constexpr int64_t kForwardWaves = 4096;
 constexpr int64_t kBackwardWaves = 4096;
 
-// Groups of heads, and how many waves share a token: as few as give every
-// compute unit its waves, since each takes the token's sines anew.
-void split_heads(HeadArgs &a, int kinds, int64_t waves)
+// Groups of heads; the grid: how many waves share a token (y), as few as give
+// every compute unit its waves, since each takes the token's cosines anew, and
+// workgroups over the tokens (x), at most `most` in all.
+dim3 split_heads(int (&groups)[3], const int (&heads)[3], int64_t T, int D, int64_t waves, int64_t most)
 {
-    const int per = 64 / lanes_of(a.D);
+    const int per = 64 / lanes_of(D);
     int all = 0;
     for (int i = 0; i < 3; ++i) {
-        a.groups[i] = i < kinds ? (a.heads[i] + per - 1) / per : 0;
-        all += a.groups[i];
+        groups[i] = (heads[i] + per - 1) / per;
+        all += groups[i];
     }
-    a.parts = (int)std::min<int64_t>(all, ceil_div(waves, a.T));
+    const int64_t parts = std::min<int64_t>(all, ceil_div(waves, T));
+    return dim3((unsigned)std::min(ceil_div(T, kBlock / 64), std::max<int64_t>(1, most / parts)), (unsigned)parts);
 }
 
-int64_t backward_groups(int64_t T, int heads, int D)
+dim3 backward_grid(int (&groups)[3], int q_heads, int k_heads, int64_t T, int D)
 {
-    const int64_t units = std::min<int64_t>(T * ceil_div(heads, 64 / lanes_of(D)), kBackwardWaves);
-    return ceil_div(std::max<int64_t>(units, 1), kBlock / 64);
+    const int heads[3] = {q_heads, k_heads, 0};
+    return split_heads(groups, heads, T, D, kBackwardWaves, kBackwardWaves / (kBlock / 64));
+}
+
+// A wave for each portion of KvPlace.
+dim3 kv_grid(const KvArgs &a)
+{
+    const int groups = 64 / lanes_of(a.cache.dim), all = 2 * a.cache.heads;
+    const int64_t waves = all <= groups ? ceil_div(a.T, groups / all) : a.T;
+    const unsigned parts = (unsigned)ceil_div(all, groups);
+    const int64_t most = std::max<int64_t>(1, kMaxBlocks / parts);
+    return dim3((unsigned)std::min(ceil_div(waves, kBlock / 64), most), parts);
 }
 
 }  // namespace
@@ -702,8 +729,7 @@ int64_t backward_groups(int64_t T, int heads, int D)
 hipError_t launch_head_norm_rope(const HeadArgs &args, int x_type, hipStream_t stream)
 {
     HeadArgs a = args;
-    split_heads(a, 2, kForwardWaves);
-    const int64_t grid = ceil_div(a.T * a.parts, kBlock / 64);
+    const dim3 grid = split_heads(a.groups, a.heads, a.T, a.D, kForwardWaves, kMaxBlocks);
     if (whole_lines(a) && large(a.T * (a.heads[0] + a.heads[1]), a.D, a.y_type))
         return by_type(
             x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, false, false, true>; },
@@ -716,8 +742,7 @@ hipError_t launch_head_norm_rope(const HeadArgs &args, int x_type, hipStream_t s
 hipError_t launch_head_norm_rope_write(const HeadArgs &args, int x_type, hipStream_t stream)
 {
     HeadArgs a = args;
-    split_heads(a, 3, kForwardWaves);
-    const int64_t grid = ceil_div(a.T * a.parts, kBlock / 64);
+    const dim3 grid = split_heads(a.groups, a.heads, a.T, a.D, kForwardWaves, kMaxBlocks);
     if (a.cache.type == QG_F8)
         return by_type(
             x_type, a.D, [](auto t, auto l) { return &head_kernel<decltype(t), decltype(l)::value, true, true, false>; },
@@ -727,13 +752,15 @@ hipError_t launch_head_norm_rope_write(const HeadArgs &args, int x_type, hipStre
         grid, a, stream);
 }
 
-size_t head_backward_workspace(int64_t T, int heads, int D)
+size_t head_backward_workspace(int64_t T, int q_heads, int k_heads, int D)
 {
-    return (size_t)backward_groups(T, heads, D) * 2 * D * sizeof(float);
+    int groups[3];
+    const dim3 grid = backward_grid(groups, q_heads, k_heads, T, D);
+    return (size_t)grid.x * grid.y * 2 * D * sizeof(float);
 }
 
 template <bool kOnce>
-hipError_t backward(const HeadGradArgs &a, int x_type, hipStream_t stream)
+hipError_t backward(const HeadGradArgs &a, int x_type, dim3 grid, hipStream_t stream)
 {
     return by_type(
         x_type, a.h.D,
@@ -744,17 +771,16 @@ hipError_t backward(const HeadGradArgs &a, int x_type, hipStream_t stream)
                    : a.h.y_type == QG_F16 ? &head_backward_kernel<T, Fp16, L, kOnce>
                                           : &head_backward_kernel<T, Bf16, L, kOnce>;
         },
-        a.groups_of_work, a, stream);
+        grid, a, stream);
 }
 
 hipError_t launch_head_norm_rope_backward(const HeadGradArgs &args, int x_type, hipStream_t stream)
 {
     HeadGradArgs a = args;
-    split_heads(a.h, 2, kBackwardWaves);
-    a.groups_of_work = (int)std::min(backward_groups(a.h.T, a.h.heads[0] + a.h.heads[1], a.h.D),
-                                     ceil_div(a.h.T * a.h.parts, kBlock / 64));
+    const dim3 grid = backward_grid(a.h.groups, a.h.heads[0], a.h.heads[1], a.h.T, a.h.D);
+    a.rows = (int)(grid.x * grid.y);
     const bool once = whole_lines(a.h) && large(a.h.T * (a.h.heads[0] + a.h.heads[1]), a.h.D, x_type);
-    const hipError_t e = once ? backward<true>(a, x_type, stream) : backward<false>(a, x_type, stream);
+    const hipError_t e = once ? backward<true>(a, x_type, grid, stream) : backward<false>(a, x_type, grid, stream);
     if (e != hipSuccess || !a.h.gain[0])
         return e;
     return launch_kernel(reinterpret_cast<const void *>(&gain_join_kernel), dim3((unsigned)(a.h.D / 8)), dim3(1024), 0,
@@ -765,19 +791,18 @@ hipError_t launch_kv_write(const KvArgs &a, int x_type, hipStream_t stream)
 {
     return by_type(
         x_type, a.cache.dim, [](auto t, auto l) { return &kv_write_kernel<decltype(t), decltype(l)::value>; },
-        ceil_div(a.T * 2 * a.cache.heads, kBlock / lanes_of(a.cache.dim)), a, stream);
+        kv_grid(a), a, stream);
 }
 
 hipError_t launch_kv_read(const KvArgs &a, int y_type, hipStream_t stream)
 {
-    const int64_t vectors = a.T * 2 * a.cache.heads, grid = ceil_div(vectors, kBlock / lanes_of(a.cache.dim));
-    if (large(vectors, a.cache.dim, y_type))
+    if (large(a.T * 2 * a.cache.heads, a.cache.dim, y_type))
         return by_type(
             y_type, a.cache.dim, [](auto t, auto l) { return &kv_read_kernel<decltype(t), decltype(l)::value, true>; },
-            grid, a, stream);
+            kv_grid(a), a, stream);
     return by_type(
         y_type, a.cache.dim, [](auto t, auto l) { return &kv_read_kernel<decltype(t), decltype(l)::value, false>; },
-        grid, a, stream);
+        kv_grid(a), a, stream);
 }
 
 }  // namespace qg
