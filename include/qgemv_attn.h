@@ -110,16 +110,18 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
  *   j q_heads / kv_heads .. share key head j; 1 <= B <= 65536, B M q_heads <=
  *   2^23.
  *   table: int32 [B][width], the pages of a sequence in order, width * page <=
- *   2^30 and B times that <= 2^36; lens: int32 [B], its tokens, the M new ones among them (already
- *   written).
+ *   2^30 and B times that <= 2^36; lens: int32 [B], its tokens, the M new ones
+ *   among them (already written).
  * Token i of the M new ones stands at place p = lens[b] - M + i and sees the
  * places max(0, p - window + 1) .. p (window 0: all up to p):
- *   s = scale * q.k,  softcap > 0: s = softcap * tanh(s / softcap),
+ *   s = scale * q.k,  softcap > 0: s = softcap * tanh(s / softcap)  (scale /
+ *   softcap finite),
  *   out = sum softmax(s) v          [B][M][q_heads][dim], q_type, contiguous.
  * A query that sees no token gets zeros.  lens are held to 0 .. width * page;
  * a table entry outside 0 .. pages - 1 holds no tokens.  What lies in places
  * that a query does not see, NaN or infinity, does not reach it.  Products are
- * exact with fp32 sums; the softmax's weights enter the second product as two
+ * exact with fp32 sums (8-bit keys beside bf16 queries down to multiples of
+ * 2^-133); the softmax's weights enter the second product as two
  * 16-bit parts (2^-16 of a weight is lost); one rounding to q_type.
  * workspace: qattn_decode_workspace bytes (0: may be NULL), 16-byte aligned,
  * used by this call only. */

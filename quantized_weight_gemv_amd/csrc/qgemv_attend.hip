@@ -17,11 +17,24 @@
 // in a lane: it loads D / 16 consecutive elements of eight tokens and turns the
 // 8 x D / 16 piece with byte permutes in registers.  Nothing passes through LDS.
 //
-// 8-bit codes are widened as they are (exact); a key's scale multiplies its
-// score, a value's scale its weight.  A weight (fp32) enters the second product
-// as two 16-bit parts, hi = round(p), lo = round(p - hi): 2^-16 of it is lost.
-// bf16 for f8 and bf16 values; with fp16 values fp16, taken times 2^11 (they
-// reach 2^4) so that small weights stay normal.
+// 8-bit codes are widened exactly; a key's scale goes along (bf16) or multiplies
+// its score (fp16), a value's scale its weight.  A weight (fp32) enters the second
+// product as two 16-bit parts, hi = round(p), lo = round(p - hi): 2^-16 of it is
+// lost, where one part would lose 2^-8, as much as the output's rounding, for a
+// product that waits for memory anyway.  bf16 for f8 and bf16 values; with fp16
+// values fp16, taken times 2^11 (they reach 2^4) so that small weights stay
+// normal.
+//
+// Bound by the cache's bytes where rows are few: 262143 tokens of 8 key heads in f8
+// (541 MB) 84 us, 6.4 TB/s, with the loads alone at 6.8; 64 ragged sequences in
+// bf16 (877 MB) 136 us, 6.4 TB/s; vector units 40 and 16 % busy.  With 30 rows
+// (f8, 230 MB) 49 us: the vector units are 60 % busy with softmax and conversions.
+// Steps on the way (us, 262143 tokens / ragged / 30 rows): work in equal chunks of a
+// sequence 108 / 167 / 79; scale factors by ldexp and with the widening, sums scaled
+// anew only beyond a slack 102 / 169 / 74; loads that leave nothing in the caches, of
+// whole lines 92 / 159 / 73; runs of equal length in one round of workgroups, and a
+// bound on registers that keeps accumulators out of the other register file
+// 92 / 148 / 60; a lighter join 90 / 139 / 57.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -406,7 +419,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                     load_once<kValWords>(w[h].keys + values + (at + j * kRow), b.vw[4 * h + j]);
             keep_order();
         };
-        // Lines to rows: lane r16 has half r16 / 8 of tokens r16 % 8 and 8 + r16 % 8, and wants both halves of token r16.
+        // Lines to rows: lane r16 has half r16 / 8 of tokens r16 % 8 and 8 + r16 % 8, and wants both halves of r16's.
         auto key_rows = [&](Stage &b, int h) {
             if constexpr (kWholeLines) {
 #pragma unroll
@@ -431,7 +444,8 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                 acc[n][d] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
         }
 
-        auto add = [&](const typename V::v8 &v, const typename V::v8 (&hi)[kTiles], const typename V::v8 (&lo)[kTiles], int d) {
+        using V8 = typename V::v8;
+        auto add = [&](const V8 &v, const V8 (&hi)[kTiles], const V8 (&lo)[kTiles], int d) {
 #pragma unroll
             for (int n = 0; n < kTiles; ++n)
                 acc[n][d] = V::mfma(v, lo[n], V::mfma(v, hi[n], acc[n][d]));
@@ -505,8 +519,10 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 #pragma unroll
                     for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)   // cap tanh(x) log2 e, from e^2x
-                            s[n][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s[n][i] * (2.0f * kLog2e)));
+                        for (int i = 0; i < 8; ++i) {   // cap tanh(x) log2 e, from e^2x
+                            const float e2 = __builtin_amdgcn_exp2f(s[n][i] * (2.0f * kLog2e));
+                            s[n][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + e2);
+                        }
                 }
                 if (edge(token) || !whole_tiles) {
 #pragma unroll
@@ -524,7 +540,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                         for (int c = 0; c < kValWords; ++c) {
                             if (!seen)
                                 b.vw[i][c] = 0;
-                            // 0 times what is not finite is not 0: what some rows see and others do not comes afterwards
+                            // 0 times what is not finite is not 0: what some rows see and others do not comes later
                             const uint32_t odd = not_finite<TQ, kF8>(b.vw[i][c]);
                             if (a.M > 1 && odd) {
                                 b.vw[i][c] &= ~odd;
@@ -583,11 +599,11 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t half = i ? 0x07060302 : 0x05040100;
-                            add(__builtin_bit_cast(typename V::v8, u4_t{__builtin_amdgcn_perm(b.vw[1][c], b.vw[0][c], half),
-                                                                        __builtin_amdgcn_perm(b.vw[3][c], b.vw[2][c], half),
-                                                                        __builtin_amdgcn_perm(b.vw[5][c], b.vw[4][c], half),
-                                                                        __builtin_amdgcn_perm(b.vw[7][c], b.vw[6][c], half)}),
-                                hi, lo, 2 * c + i);
+                            u4_t pairs;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                pairs[j] = __builtin_amdgcn_perm(b.vw[2 * j + 1][c], b.vw[2 * j][c], half);
+                            add(__builtin_bit_cast(V8, pairs), hi, lo, 2 * c + i);
                         }
                     }
                 }
@@ -615,7 +631,8 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                         continue;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t *from = reinterpret_cast<const uint32_t *>(w.keys + values + (4 * g + e) * (4 * kValWords));
+                        const auto *from =
+                            reinterpret_cast<const uint32_t *>(w.keys + values + (4 * g + e) * (4 * kValWords));
 #pragma unroll
                         for (int c = 0; c < kValWords; ++c) {
                             const uint32_t word = from[c] & not_finite<TQ, kF8>(from[c]);
@@ -703,7 +720,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 }
 
 // Joins the parts of a row: kWavesRow waves (all four, or one where rows are
-// many: 3840 rows 9.8 us with four, JOINUS with one), 16-byte pieces of D in
+// many: 3840 rows 9.8 us with four, 6.1 with one), 16-byte pieces of D in
 // consecutive lanes, the parts over the rest.
 template <typename TQ, int D, int kWavesRow>
 __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)

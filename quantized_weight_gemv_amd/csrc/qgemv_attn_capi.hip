@@ -22,6 +22,14 @@ inline bool rows_ok(int64_t ld, int heads, int D, int64_t T)
     return ld >= (int64_t)heads * D && ld <= INT64_MAX / 8 / T;
 }
 
+// The queries and the table of an attention call.
+inline bool batch_ok(int64_t B, int M, int q_heads, int kv_heads, int page, int64_t width)
+{
+    return B >= 1 && B <= kAttnMaxBatch && M >= 1 && M <= kAttnMaxNew && kv_heads >= 1 && q_heads >= kv_heads &&
+           q_heads <= kAttnMaxHeads && q_heads % kv_heads == 0 && B * M * q_heads <= kAttnMaxRows && width >= 1 &&
+           width <= kAttnMaxPlaces / page && B * width * page <= kAttnMaxTable;
+}
+
 qg_status check_cache(const void *cache, int64_t pages, int page, int heads, int dim, int type)
 {
     if (!cache)
@@ -218,9 +226,8 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
 size_t qattn_decode_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int cache_type, int page,
                               int64_t width)
 {
-    if (B < 1 || B > kAttnMaxBatch || M < 1 || M > kAttnMaxNew || kv_heads < 1 || q_heads < kv_heads ||
-        q_heads > kAttnMaxHeads || q_heads % kv_heads || B * M * q_heads > kAttnMaxRows || !cache_dim_ok(dim) || !cache_type_ok(cache_type) || !page_ok(page) || width < 1 ||
-        width > kAttnMaxPlaces / page || B * width * page > kAttnMaxTable)
+    if (!page_ok(page) || !cache_dim_ok(dim) || !cache_type_ok(cache_type) ||
+        !batch_ok(B, M, q_heads, kv_heads, page, width))
         return 0;
     return attend_workspace(B, M, q_heads, kv_heads, dim, cache_type, page, width);
 }
@@ -235,10 +242,10 @@ qg_status qattn_decode(const void *cache, int64_t pages, int page, int kv_heads,
     const qg_status st = check_cache(cache, pages, page, kv_heads, dim, cache_type);
     if (st != QG_OK)
         return st;
-    if ((q_type != QG_F16 && q_type != QG_BF16) || (cache_type != QG_F8 && cache_type != q_type) || B < 1 ||
-        B > kAttnMaxBatch || M < 1 || M > kAttnMaxNew || q_heads < kv_heads || q_heads > kAttnMaxHeads ||
-        q_heads % kv_heads || B * M * q_heads > kAttnMaxRows || !qg::rows_ok(ldq, q_heads, dim, B * M) || width < 1 ||
-        width > kAttnMaxPlaces / page || B * width * page > kAttnMaxTable || window < 0 || window > INT32_MAX || !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f)
+    if ((q_type != QG_F16 && q_type != QG_BF16) || (cache_type != QG_F8 && cache_type != q_type) ||
+        !batch_ok(B, M, q_heads, kv_heads, page, width) || !qg::rows_ok(ldq, q_heads, dim, B * M) || window < 0 ||
+        window > INT32_MAX || !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f ||
+        (softcap > 0.0f && !std::isfinite(scale / softcap)))
         return QG_ERR_SHAPE;
     if (!workspace && attend_workspace(B, M, q_heads, kv_heads, dim, cache_type, page, width) > 0)
         return QG_ERR_NULL;

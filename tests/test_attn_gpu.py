@@ -426,7 +426,7 @@ def test_many_sequences():
 
 
 def test_pages_that_are_not_there_hold_no_tokens():
-    """Entries outside 0 .. pages - 1, inside a sequence's length: at its start, in the middle, at the end, everywhere."""
+    """Entries outside 0 .. pages - 1, inside a sequence's length: at its start, its middle, its end, everywhere."""
     b = _Batch([200, 200, 200, 200, 200], 2, 4, 2, 128, 16, "f8", "bfloat16")
     for row, col, page in ((0, 0, -1), (1, 5, b.pages), (2, 12, 1 << 30), (1, 6, -(1 << 31))):
         b.table[row, col] = page
@@ -542,7 +542,8 @@ def test_refusals_of_the_binding():
         lambda: q.qkv_write(cache._replace(data=cache.data[:, :-1].contiguous()), k, k, pos),
         lambda: q.qkv_write(cache._replace(data=cache.data.float()), k, k, pos),
         lambda: q.qkv_read(cache, pos, dtype=torch.float64), lambda: q.qkv_read(cache, pos[:0]),
-        lambda: q.qkv_norm_rope_write(cache, x, x, k, pos, pos, f), lambda: q.qkv_norm_rope_write(cache, x, k, x, pos, pos, f),
+        lambda: q.qkv_norm_rope_write(cache, x, x, k, pos, pos, f),
+        lambda: q.qkv_norm_rope_write(cache, x, k, x, pos, pos, f),
         lambda: q.qkv_norm_rope_write(cache, x, k, k, pos[:2], pos, f),
         lambda: q.qattn_decode(cache, x.float(), table, pos), lambda: q.qattn_decode(cache, x[:, :5], table, pos),
         lambda: q.qattn_decode(cache, x, table[:3], pos), lambda: q.qattn_decode(cache, x, table, pos[:3]),

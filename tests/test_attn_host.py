@@ -92,7 +92,8 @@ def _cache(**kw):
 
 @pytest.mark.parametrize("kw,status", CACHE_REFUSALS + [
     (dict(k=None), NULL), (dict(v=None), NULL), (dict(slots=None), NULL), (dict(ldk=255), SHAPE),
-    (dict(ldv=255), SHAPE), (dict(xt=3), SHAPE), (dict(T=0), SHAPE), (dict(k=P + 1), ALIGN), (dict(slots=P + 2), ALIGN)])
+    (dict(ldv=255), SHAPE), (dict(xt=3), SHAPE), (dict(T=0), SHAPE), (dict(k=P + 1), ALIGN),
+    (dict(slots=P + 2), ALIGN)])
 def test_write_refuses(kw, status):
     cache, kw = _cache(**kw)
     a = dict(k=P, ldk=256, v=P, ldv=256, xt=2, slots=P, T=5)
@@ -116,8 +117,8 @@ def test_read_refuses(kw, status):
     (dict(v=P + 1), ALIGN), (dict(yq=P + 1), ALIGN)])
 def test_norm_rope_write_refuses(kw, status):
     cache, kw = _cache(**kw)
-    a = dict(q=P, ldq=1024, nq=4, k=P, ldk=1024, v=P, ldv=1024, xt=2, gq=P, gk=P, gt=0, eps=1e-6, pos=P, axes=1, sec=None,
-             freq=P, rot=128, inter=0, T=3, slots=P, yq=P, ldyq=512, yt=2)
+    a = dict(q=P, ldq=1024, nq=4, k=P, ldk=1024, v=P, ldv=1024, xt=2, gq=P, gk=P, gt=0, eps=1e-6, pos=P, axes=1,
+             sec=None, freq=P, rot=128, inter=0, T=3, slots=P, yq=P, ldyq=512, yt=2)
     a.update(kw)
     assert _lib().qkv_norm_rope_write(*a.values(), *cache, None) == status
 
@@ -127,9 +128,11 @@ def test_norm_rope_write_refuses(kw, status):
     (dict(qt=0), SHAPE), (dict(qt=3), SHAPE), (dict(type=2, qt=1), SHAPE), (dict(ldq=511), SHAPE), (dict(B=0), SHAPE),
     (dict(B=65537), SHAPE), (dict(M=0), SHAPE), (dict(M=17), SHAPE), (dict(nq=3), SHAPE), (dict(nq=1), SHAPE),
     (dict(nq=1026, ldq=1 << 20), SHAPE), (dict(B=65536, M=16, nq=16, ldq=2048), SHAPE),
-    (dict(width=(1 << 30) // 64 + 1), SHAPE), (dict(B=65, width=(1 << 30) // 64), SHAPE), (dict(width=0), SHAPE), (dict(width=(1 << 31) // 64), SHAPE),
+    (dict(width=(1 << 30) // 64 + 1), SHAPE), (dict(B=65, width=(1 << 30) // 64), SHAPE), (dict(width=0), SHAPE),
+    (dict(width=(1 << 31) // 64), SHAPE),
     (dict(scale=float("inf")), SHAPE), (dict(scale=float("nan")), SHAPE), (dict(window=-1), SHAPE),
-    (dict(window=1 << 31), SHAPE), (dict(cap=-1.0), SHAPE), (dict(cap=float("inf")), SHAPE), (dict(q=P + 1), ALIGN),
+    (dict(window=1 << 31), SHAPE), (dict(cap=-1.0), SHAPE), (dict(cap=float("inf")), SHAPE), (dict(cap=1e-40), SHAPE),
+    (dict(q=P + 1), ALIGN),
     (dict(table=P + 2), ALIGN), (dict(lens=P + 2), ALIGN), (dict(out=P + 1), ALIGN), (dict(ws=P + 8), ALIGN)])
 def test_attend_refuses(kw, status):
     cache, kw = _cache(**kw)
@@ -168,8 +171,8 @@ def test_the_binding_refuses_host_tensors():
 
 
 # ------------------------------------------------------------- the references
-@pytest.mark.parametrize("D,rot,interleaved,sections", [(16, 16, False, [8]), (24, 16, True, [3, 5]), (8, 0, False, [0]),
-                                                        (32, 24, False, [2, 4, 6])])
+@pytest.mark.parametrize("D,rot,interleaved,sections", [(16, 16, False, [8]), (24, 16, True, [3, 5]),
+                                                        (8, 0, False, [0]), (32, 24, False, [2, 4, 6])])
 @pytest.mark.parametrize("normed", [False, True])
 def test_reference_gradient_against_differences(D, rot, interleaved, sections, normed):
     g = np.random.default_rng([D, rot, normed])
@@ -206,7 +209,8 @@ def test_reference_rotation_is_a_turn():
         one = au.rotate(x, *au.turns(p, f, [8]), 16, inter)
         a, b = au.pairs(16, inter)
         assert np.allclose(one[..., a] ** 2 + one[..., b] ** 2, x[..., a] ** 2 + x[..., b] ** 2)
-        assert np.allclose(au.rotate(one, *au.turns(q, f, [8]), 16, inter), au.rotate(x, *au.turns(p + q, f, [8]), 16, inter))
+        two = au.rotate(one, *au.turns(q, f, [8]), 16, inter)
+        assert np.allclose(two, au.rotate(x, *au.turns(p + q, f, [8]), 16, inter))
 
 
 @pytest.mark.parametrize("cache", ["f8", "float16", "bfloat16"])

@@ -107,8 +107,8 @@ def test_norm_rope_as_an_autograd_function(axes):
         def backward(ctx, dq, dk):
             qkv, gq, gk = ctx.saved_tensors
             d = torch.empty_like(qkv)
-            grads = q.qhead_norm_rope_backward(dq.contiguous(), dk.contiguous(), qkv[:, :H], qkv[:, H:], p, freq, gq, gk,
-                                               out=(d[:, :H], d[:, H:]), **how)
+            grads = q.qhead_norm_rope_backward(dq.contiguous(), dk.contiguous(), qkv[:, :H], qkv[:, H:], p, freq, gq,
+                                               gk, out=(d[:, :H], d[:, H:]), **how)
             return d, grads[2], grads[3]
 
     leaves = [to_dev(rng.normal(size=s).astype(np.float32)).requires_grad_() for s in ((T, H + KV, D), (D,), (D,))]
