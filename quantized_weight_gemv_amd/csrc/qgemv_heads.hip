@@ -263,17 +263,34 @@ __device__ __forceinline__ void turn(const Place &p, bool interleaved, const F (
     }
 }
 
-__device__ __forceinline__ float inverse_root(float v) { return rsqrtf(v); }
+// 1 / sqrt(v), the nearest fp32 value: the hardware's 64-bit estimate (2^-24) and one
+// step of Newton's method, which squares its error.
+__device__ __forceinline__ float inverse_root(float v)
+{
+    const double x = v, r = __builtin_amdgcn_rsq(x);
+    const double better = fma(0.5 * r, fma(-x * r, r, 1.0), r);
+    return v > 0.0f && v < __builtin_inff() ? (float)better : rsqrtf(v);
+}
 __device__ __forceinline__ double inverse_root(double v) { return 1.0 / sqrt(v); }
 
+// 1 / sqrt(mean of squares + eps).  Squares round by themselves and are summed four
+// neighbours first (one after the other; in pairs up to 64 elements), then
+// neighbouring fours: the order in which the mean of a row of 64, 128 or 256 is
+// taken by separate operations on this card, so that those give the same bits.
+// `apart`: a lane's two pieces are of the vector's two halves.
 template <int L, typename F>
-__device__ __forceinline__ F inverse_norm(const F (&v)[8], F inverse_dim, float eps)
+__device__ __forceinline__ F inverse_norm(const F (&v)[8], bool apart, F inverse_dim, float eps)
 {
-    F ss = 0;
+#pragma clang fp contract(off)
+    F four[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        ss += v[i] * v[i];
-    return inverse_root(group_sum<L>(ss) * inverse_dim + (F)eps);
+    for (int i = 0; i < 2; ++i) {
+        const F a = v[4 * i] * v[4 * i], b = v[4 * i + 1] * v[4 * i + 1];
+        const F c = v[4 * i + 2] * v[4 * i + 2], d = v[4 * i + 3] * v[4 * i + 3];
+        four[i] = L == 8 ? (a + b) + (c + d) : ((a + b) + c) + d;
+    }
+    const F ss = apart ? group_sum<L>(four[0]) + group_sum<L>(four[1]) : group_sum<L>(four[0] + four[1]);
+    return inverse_root(ss * inverse_dim + (F)eps);
 }
 
 // A lane's eight values of an f8 vector held by L lanes: codes and scale byte,
@@ -354,8 +371,10 @@ template <int L, typename F>
 __device__ __forceinline__ void norm_turn(const HeadArgs &a, const Place &p, const float (&gain)[8], const F (&c)[4],
                                           const F (&s)[4], F (&v)[8])
 {
+#pragma clang fp contract(off)
     if (a.gain[0]) {
-        const F r = inverse_norm<L>(v, (F)1 / (F)a.D, a.eps);
+        const bool apart = a.half == 0 || (!a.interleaved && 2 * a.half == a.D);
+        const F r = inverse_norm<L>(v, apart, (F)1 / (F)a.D, a.eps);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = v[i] * r * (F)gain[i];
