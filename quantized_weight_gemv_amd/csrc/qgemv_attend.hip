@@ -185,18 +185,20 @@ __device__ __forceinline__ typename Half<T>::v8 widen8(uint32_t lo, uint32_t hi,
 // e of the i-th of four scale bytes.
 __device__ __forceinline__ int exponent_of(uint32_t bytes, int i) { return (int)((bytes >> (8 * i)) & 255u) - 127; }
 
-// Words of the cache, each read once by one workgroup: loads that leave nothing
-// behind in the caches stream at 6.8 TB/s where ordinary ones reach 5.9 (541 MB
-// in pages of 64 tokens, loads alone).  They have to take whole lines, or the
-// other half is read again.
-template <int kWords>
-__device__ __forceinline__ void load_once(const uint8_t *from, uint32_t *to)
+// Words of the cache.  Where one workgroup reads each (kOnce), loads that leave
+// nothing behind in the caches stream at 6.8 TB/s where ordinary ones reach 5.9
+// (541 MB in pages of 64 tokens, loads alone); they have to take whole lines, or the
+// other half is read again.  Where several groups of rows read the same cache,
+// ordinary loads find it in the caches (128 rows a key head in bf16 91 us for 121).
+template <int kWords, bool kOnce>
+__device__ __forceinline__ void load_words(const uint8_t *from, uint32_t *to)
 {
     constexpr int kN = kWords % 4 == 0 ? 4 : kWords % 3 == 0 ? 3 : kWords % 2 == 0 ? 2 : 1;
     typedef uint32_t piece __attribute__((ext_vector_type(kN), aligned(4 * (kN == 3 ? 1 : kN))));
 #pragma unroll
     for (int i = 0; i < kWords; i += kN) {
-        const piece p = __builtin_nontemporal_load(reinterpret_cast<const piece *>(from + 4 * i));
+        const piece *at = reinterpret_cast<const piece *>(from + 4 * i);
+        const piece p = kOnce ? __builtin_nontemporal_load(at) : *at;
 #pragma unroll
         for (int j = 0; j < kN; ++j)
             to[i + j] = p[j];
@@ -271,9 +273,7 @@ constexpr int resident(int D, bool f8, int tiles)
 {
     if (tiles == 1)
         return D == 64 ? 4 : D == 128 ? (f8 ? 3 : 2) : D == 192 ? 2 : f8 ? 2 : 1;
-    if (tiles == 2)
-        return D == 64 ? 3 : D == 128 ? 2 : 1;
-    return 1;
+    return D == 64 ? 3 : D == 128 ? 2 : 1;
 }
 
 struct AttendLaunch {
@@ -285,8 +285,9 @@ struct AttendLaunch {
     bool by_sequence;   // a workgroup a sequence, nothing to find or to join
 };
 
-// TQ: type of q, of the output and of 16-bit caches; kF8: an 8-bit cache.
-template <typename TQ, bool kF8, int D, int kTiles>
+// TQ: type of q, of the output and of 16-bit caches; kF8: an 8-bit cache; kOnce: no
+// other group of rows reads the cache.
+template <typename TQ, bool kF8, int D, int kTiles, bool kOnce>
 __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kernel(AttendLaunch la)
 {
     using TV = std::conditional_t<kF8, Bf16, TQ>;   // of the second product
@@ -401,7 +402,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int c = 0; c < kKeyLoads; ++c)
-                    load_once<4>(w[h].keys + (at + (kWholeLines ? 8 * (c & 1) * kRow + 128 * (c / 2) : 64 * c)),
+                    load_words<4, kOnce>(w[h].keys + (at + (kWholeLines ? 8 * (c & 1) * kRow + 128 * (c / 2) : 64 * c)),
                                  b.kw[h][c]);
             keep_order();
         };
@@ -416,7 +417,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    load_once<kValWords>(w[h].keys + values + (at + j * kRow), b.vw[4 * h + j]);
+                    load_words<kValWords, kOnce>(w[h].keys + values + (at + j * kRow), b.vw[4 * h + j]);
             keep_order();
         };
         // Lines to rows: lane r16 has half r16 / 8 of tokens r16 % 8 and 8 + r16 % 8, and wants both halves of r16's.
@@ -807,14 +808,10 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
     *reinterpret_cast<Raw8 *>(out + 4 * lane) = Raw8{pack2<TQ>(v[0], v[1]), pack2<TQ>(v[2], v[3])};
 }
 
-// Tiles of 16 rows a workgroup takes: all rows where their accumulators fit the
-// registers, else several groups read the cache anew.
-int tiles_of_rows(int rows, int D)
-{
-    const int most = D <= 128 ? 4 : 2;
-    const int tiles = (rows + 15) / 16;
-    return tiles <= 1 ? 1 : tiles == 2 ? 2 : most;
-}
+// Tiles of 16 rows a workgroup takes: one or two, more rows in groups that read the
+// cache each.  (Four tiles, one wave a SIMD, at 128 dimensions: 64 rows a key head in
+// f8 74 us for 56, 128 rows 109 for 85; in bf16 74 for 55, 106 for 91.)
+int tiles_of_rows(int rows) { return rows <= 16 ? 1 : 2; }
 
 struct Cut {
     int rows, tiles, row_groups, target;
@@ -826,7 +823,7 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
 {
     Cut c;
     c.rows = M * (q_heads / kv_heads);
-    c.tiles = tiles_of_rows(c.rows, dim);
+    c.tiles = tiles_of_rows(c.rows);
     c.row_groups = (c.rows + 16 * c.tiles - 1) / (16 * c.tiles);
     c.target = std::max(1, kRounds * kUnits * resident(dim, f8, c.tiles) / (kv_heads * c.row_groups));
     // no sequence has more tiles than this: no more runs than tiles
@@ -851,13 +848,9 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
 template <typename TQ, bool kF8, int D>
 hipError_t launch(const AttendLaunch &la, const Cut &c, hipStream_t stream)
 {
-    void (*fn)(AttendLaunch) = nullptr;
-    if (c.tiles == 1)
-        fn = &attend_kernel<TQ, kF8, D, 1>;
-    else if (c.tiles == 2)
-        fn = &attend_kernel<TQ, kF8, D, 2>;
-    else if constexpr (D <= 128)
-        fn = &attend_kernel<TQ, kF8, D, 4>;
+    void (*fn)(AttendLaunch) = c.tiles == 1        ? &attend_kernel<TQ, kF8, D, 1, true>
+                               : c.row_groups == 1 ? &attend_kernel<TQ, kF8, D, 2, true>
+                                                   : &attend_kernel<TQ, kF8, D, 2, false>;
     const hipError_t e = launch_kernel(reinterpret_cast<const void *>(fn),
                                        dim3((unsigned)(c.target * la.a.cache.heads * c.row_groups)), dim3(kBlock), 0,
                                        stream, la);
