@@ -52,6 +52,7 @@ HEADS = [
     (11, 4, 2, 128, 0, False, 1, "float32", "bfloat16", "bfloat16"),
     (4, 3, 0, 128, 128, False, 1, "float32", "bfloat16", "float32"),
     (4200, 2, 1, 64, 64, False, 1, "float32", "bfloat16", "bfloat16"),
+    (2, 1000, 24, 64, 64, False, 1, "float32", "bfloat16", "bfloat16"),
 ]
 
 
@@ -210,7 +211,8 @@ def test_backward_into_the_parts_of_one_gradient():
 CACHES = [(1, 1, 64, 16, "f8", "bfloat16"), (37, 3, 64, 32, "f8", "float32"), (50, 8, 128, 64, "f8", "float16"),
           (21, 2, 192, 16, "f8", "bfloat16"), (9, 1, 256, 1024, "f8", "float32"), (30, 2, 64, 16, "float16", "float32"),
           (40, 3, 128, 128, "bfloat16", "bfloat16"), (13, 2, 192, 32, "float16", "float16"),
-          (17, 5, 256, 64, "bfloat16", "float32")]
+          (17, 5, 256, 64, "bfloat16", "float32"), (12, 1024, 64, 16, "f8", "bfloat16"),
+          (11, 7, 256, 16, "f8", "float32")]
 
 
 def _slots(rng, T, total):
@@ -399,6 +401,18 @@ def test_attend(case):
     _Batch(*case).check()
 
 
+@pytest.mark.parametrize("case", ATTEND)
+def test_attend_under_a_wide_table(case):
+    """A table for long sequences: work is cut into runs and joined, however short the sequences are."""
+    _Batch(*case, width=40000 // case[5]).check()
+
+
+@pytest.mark.parametrize("case", [ATTEND[3], ATTEND[9], ATTEND[14], ATTEND[18], ATTEND[20]])
+@pytest.mark.parametrize("kw", [dict(window=2000), dict(window=70, softcap=9.0), dict(scale=0.0)])
+def test_attend_options_under_a_wide_table(case, kw):
+    _Batch(*case, width=40000 // case[5]).check(**kw)
+
+
 @pytest.mark.parametrize("case", [ATTEND[3], ATTEND[6], ATTEND[14], ATTEND[15], ATTEND[17]])
 @pytest.mark.parametrize("window", [1, 16, 33, 100, 100000])
 def test_attend_in_a_window(case, window):
@@ -420,9 +434,25 @@ def test_attend_over_long_caches(cache, q, lens, M, H, KV, window):
     _Batch(lens, M, H, KV, 128, 64, cache, q).check(window=window)
 
 
-def test_many_sequences():
-    rng = np.random.default_rng(1)
-    _Batch([int(n) for n in rng.integers(0, 70, 150)], 1, 2, 1, 64, 16, "f8", "bfloat16").check()
+@pytest.mark.parametrize("width", [5, 4000])
+@pytest.mark.parametrize("count,most", [(64, 70), (65, 70), (150, 70), (700, 20), (100, 400)])
+def test_many_sequences(count, most, width):
+    """More sequences than lanes, many of them empty, in portions of one and in runs over several."""
+    rng = np.random.default_rng([count, most])
+    lens = [int(n) if rng.random() > 0.2 else 0 for n in rng.integers(0, most, count)]
+    _Batch(lens, 1, 2, 1, 64, 16, "f8", "bfloat16", width=max(width, most // 16 + 1)).check()
+
+
+@pytest.mark.parametrize("D,cache,q", [(64, "f8", "float16"), (192, "bfloat16", "bfloat16"), (256, "f8", "bfloat16"),
+                                       (256, "float16", "float16")])
+def test_one_long_sequence_of_every_width(D, cache, q):
+    _Batch([7001], 1, 4, 1, D, 128, cache, q).check()
+
+
+def test_all_sequences_empty():
+    for width in (2, 4000):
+        b = _Batch([0] * 70, 2, 4, 2, 128, 16, "bfloat16", "bfloat16", width=width)
+        assert not _np(b.check()).any()
 
 
 def test_pages_that_are_not_there_hold_no_tokens():
@@ -446,10 +476,11 @@ def test_lengths_are_held_to_the_table():
 
 @pytest.mark.parametrize("cache,q", [("f8", "bfloat16"), ("bfloat16", "bfloat16"), ("float16", "float16")])
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
-def test_values_that_are_not_finite_reach_only_who_sees_them(cache, q, D):
+@pytest.mark.parametrize("heads", [4, 20])
+def test_values_that_are_not_finite_reach_only_who_sees_them(cache, q, D, heads):
     """New tokens behind a query, and tokens in front of its window, may be NaN or infinite."""
-    M, window = 4, 40
-    b = _Batch([100, 37], M, 4, 2, D, 16, cache, q)
+    M, window, share = 4, 40, heads // 2
+    b = _Batch([100, 37], M, heads, 2, D, 16, cache, q)
     ref, bound = b.reference(window=window)
     for place, value in ((99, np.nan), (98, np.inf if cache != "f8" else np.nan), (57, np.nan)):
         slot = b.table[0, place // 16] * 16 + place % 16
@@ -462,7 +493,7 @@ def test_values_that_are_not_finite_reach_only_who_sees_them(cache, q, D):
     got = _np(b.run(window=window))
     # query i stands at 96 + i and sees 57 + i ..: place 57 only query 0, place 98 queries 2 and 3, place 99 query 3
     touched = np.zeros(ref.shape, bool)
-    touched[0, 0, :2, 5] = touched[0, 2, :2, 5] = touched[0, 3, :2, 5] = True
+    touched[0, 0, :share, 5] = touched[0, 2, :share, 5] = touched[0, 3, :share, 5] = True
     assert np.array_equal(~np.isfinite(got), touched)
     au.assert_attend(np.where(touched, 0, got), np.where(touched, 0, ref), bound, q, "others")
 
@@ -491,6 +522,49 @@ def test_queries_of_a_projection_and_a_given_output():
     assert b.run(wide[:, :, 1:5], out=out) is out and torch.equal(out, y)
     one = _Batch([90, 33], 1, 4, 2, 128, 16, "f8", "bfloat16")
     assert torch.equal(one.run(one.q[:, 0]), one.run()[:, 0])
+
+
+def test_a_query_that_is_not_finite():
+    torch = torch_cuda()
+    b = _Batch([50, 700], 2, 8, 2, 128, 16, "f8", "bfloat16")
+    want = b.run()
+    b.q[1, 0, 3, 7] = float("nan")
+    got = b.run()
+    assert torch.isnan(got[1, 0, 3]).all()
+    got[1, 0, 3] = want[1, 0, 3]
+    assert torch.equal(got, want)
+
+
+def test_tensors_at_any_element():
+    """Inputs and outputs that begin one element behind an aligned address."""
+    q, torch = qg(), torch_cuda()
+
+    def moved(t):
+        out = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)[1:].view(t.shape)
+        return out.copy_(t)
+
+    for dtype in (torch.float32, torch.bfloat16):
+        x, dy = (torch.randn(7, 6, 128, device="cuda").to(dtype) for _ in "xd")
+        pos, f = torch.arange(7, dtype=torch.int32, device="cuda"), torch.rand(64, device="cuda")
+        g = [torch.rand(128, device="cuda").to(dtype) for _ in "qk"]
+        args = (moved(pos), moved(f), *(moved(t) for t in g))
+        want = q.qhead_norm_rope(x[:, :4], x[:, 4:], pos, f, *g)
+        y = moved(x)
+        got = q.qhead_norm_rope(y[:, :4], y[:, 4:], *args, out=(y[:, :4], y[:, 4:]))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        want = q.qhead_norm_rope_backward(dy[:, :4], dy[:, 4:], x[:, :4], x[:, 4:], pos, f, *g)
+        y, d = moved(x), moved(dy)
+        got = q.qhead_norm_rope_backward(d[:, :4], d[:, 4:], y[:, :4], y[:, 4:], *args, out=(d[:, :4], d[:, 4:]))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        caches = [q.qkv_cache(2, 16, 2, 128) for _ in "ab"]
+        slots = torch.arange(7, dtype=torch.int32, device="cuda")
+        q.qkv_write(caches[0], x[:, :2], x[:, 2:4], slots)
+        y = moved(x)
+        q.qkv_write(caches[1], y[:, :2], y[:, 2:4], moved(slots))
+        assert torch.equal(caches[0].data, caches[1].data)
+    b = _Batch([50, 700], 2, 8, 2, 128, 16, "f8", "bfloat16")
+    want = b.run()
+    assert torch.equal(b.run(moved(b.q), out=moved(want)), want)
 
 
 def test_results_repeat_bit_for_bit():
