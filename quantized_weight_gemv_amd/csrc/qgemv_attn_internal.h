@@ -125,6 +125,7 @@ struct HeadArgs {
     int axes;
     int half;               // pairs that are turned (rot / 2)
     bool interleaved;
+    int split;              // lanes whose two pieces are of different halves (set by the launcher)
     int64_t T;
     int D;
     void *y[2];

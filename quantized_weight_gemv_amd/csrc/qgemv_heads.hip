@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "qgemv_attn_internal.h"
 
@@ -130,9 +131,8 @@ __device__ __forceinline__ void store8_as(int type, void *base, int64_t at, int 
         store8<kOnce>(static_cast<Bf16 *>(base) + at, lo, hi, w);
 }
 
-// (the declarations of fp32 stand beside those of 64 bits)
+// (the declaration of fp32 stands beside that of 64 bits)
 using qg::dpp;
-using qg::group_sum;
 
 template <int kCtrl>
 __device__ __forceinline__ double dpp(double v)
@@ -142,25 +142,6 @@ __device__ __forceinline__ double dpp(double v)
     const uint32_t hi =
         (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, true);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-template <int L>
-__device__ __forceinline__ double group_sum(double v)
-{
-    v += dpp<0xB1>(v);
-    v += dpp<0x4E>(v);
-    v += dpp<0x141>(v);
-    if constexpr (L >= 16)
-        v += dpp<0x140>(v);
-    if constexpr (L >= 32) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        const f2_t lo = pair16(__uint_as_float((uint32_t)u)), hi = pair16(__uint_as_float((uint32_t)(u >> 32)));
-        auto of = [](float h, float l) {
-            return __builtin_bit_cast(double, (uint64_t)__float_as_uint(h) << 32 | __float_as_uint(l));
-        };
-        v = of(hi[0], lo[0]) + of(hi[1], lo[1]);
-    }
-    return v;
 }
 
 // A wave's lane inside its head vector.
@@ -273,13 +254,34 @@ __device__ __forceinline__ float inverse_root(float v)
 }
 __device__ __forceinline__ double inverse_root(double v) { return 1.0 / sqrt(v); }
 
+// One step of a sum over the lanes of a group: lanes `kStep` apart hold sums of as
+// many lanes each.
+template <int kStep, typename F>
+__device__ __forceinline__ F add_lanes(F v)
+{
+    if constexpr (kStep == 16 && sizeof(F) == 4) {
+        const f2_t p = pair16(v);
+        return p[0] + p[1];
+    } else if constexpr (kStep == 16) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        const f2_t lo = pair16(__uint_as_float((uint32_t)u)), hi = pair16(__uint_as_float((uint32_t)(u >> 32)));
+        auto of = [](float h, float l) {
+            return __builtin_bit_cast(double, (uint64_t)__float_as_uint(h) << 32 | __float_as_uint(l));
+        };
+        return of(hi[0], lo[0]) + of(hi[1], lo[1]);
+    } else {
+        return v + dpp<kStep == 1 ? 0xB1 : kStep == 2 ? 0x4E : kStep == 4 ? 0x141 : 0x140>(v);
+    }
+}
+
 // 1 / sqrt(mean of squares + eps).  Squares round by themselves and are summed four
 // neighbours first (one after the other; in pairs up to 64 elements), then
 // neighbouring fours: the order in which the mean of a row of 64, 128 or 256 is
-// taken by separate operations on this card, so that those give the same bits.
-// `apart`: a lane's two pieces are of the vector's two halves.
+// taken by separate operations on this card, so that those give the same bits.  The
+// first `split` lanes (a power of two) have one four of either half of the turned
+// elements: the halves are summed apart until they are neighbours.
 template <int L, typename F>
-__device__ __forceinline__ F inverse_norm(const F (&v)[8], bool apart, F inverse_dim, float eps)
+__device__ __forceinline__ F inverse_norm(const F (&v)[8], int split, F inverse_dim, float eps)
 {
 #pragma clang fp contract(off)
     F four[2];
@@ -289,7 +291,25 @@ __device__ __forceinline__ F inverse_norm(const F (&v)[8], bool apart, F inverse
         const F c = v[4 * i + 2] * v[4 * i + 2], d = v[4 * i + 3] * v[4 * i + 3];
         four[i] = L == 8 ? (a + b) + (c + d) : ((a + b) + c) + d;
     }
-    const F ss = apart ? group_sum<L>(four[0]) + group_sum<L>(four[1]) : group_sum<L>(four[0] + four[1]);
+    const bool apart = (int)(threadIdx.x % L) < split;
+    F ss = apart ? four[0] : four[0] + four[1], other = apart ? four[1] : (F)0;
+    auto step = [&](auto lanes) {
+        constexpr int kStep = decltype(lanes)::value;
+        if (kStep == split)
+            ss += other;
+        ss = add_lanes<kStep>(ss);
+        if (kStep < split)
+            other = add_lanes<kStep>(other);
+    };
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 4>{});
+    if constexpr (L >= 16)
+        step(std::integral_constant<int, 8>{});
+    if constexpr (L >= 32)
+        step(std::integral_constant<int, 16>{});
+    if (split >= L)
+        ss += other;
     return inverse_root(ss * inverse_dim + (F)eps);
 }
 
@@ -373,8 +393,7 @@ __device__ __forceinline__ void norm_turn(const HeadArgs &a, const Place &p, con
 {
 #pragma clang fp contract(off)
     if (a.gain[0]) {
-        const bool apart = a.half == 0 || (!a.interleaved && 2 * a.half == a.D);
-        const F r = inverse_norm<L>(v, apart, (F)1 / (F)a.D, a.eps);
+        const F r = inverse_norm<L>(v, a.split, (F)1 / (F)a.D, a.eps);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = v[i] * r * (F)gain[i];
@@ -718,6 +737,15 @@ bool whole_lines(const HeadArgs &a) { return a.half == 0 || (!a.interleaved && 2
 constexpr int64_t kForwardWaves = 4096;
 constexpr int64_t kBackwardWaves = 4096;
 
+// Lanes that hold one piece of either half (place()): all if nothing is turned,
+// those of the turned pairs, none with neighbours; 0 too where they are no power of
+// two.
+int split_lanes(const HeadArgs &a)
+{
+    const int n = a.half == 0 ? a.D / 8 : a.interleaved ? 0 : a.half / 4;
+    return (n & (n - 1)) ? 0 : n;
+}
+
 // Groups of heads; the grid: how many waves share a token (y), as few as give
 // every compute unit its waves, since each takes the token's cosines anew, and
 // workgroups over the tokens (x), at most `most` in all.
@@ -754,6 +782,7 @@ dim3 kv_grid(const KvArgs &a)
 hipError_t launch_head_norm_rope(const HeadArgs &args, int x_type, hipStream_t stream)
 {
     HeadArgs a = args;
+    a.split = split_lanes(a);
     const dim3 grid = split_heads(a.groups, a.heads, a.T, a.D, kForwardWaves, kMaxBlocks);
     if (whole_lines(a) && large(a.T * (a.heads[0] + a.heads[1]), a.D, a.y_type))
         return by_type(
@@ -768,6 +797,7 @@ hipError_t launch_head_norm_rope(const HeadArgs &args, int x_type, hipStream_t s
 hipError_t launch_head_norm_rope_write(const HeadArgs &args, int x_type, hipStream_t stream)
 {
     HeadArgs a = args;
+    a.split = split_lanes(a);
     const dim3 grid = split_heads(a.groups, a.heads, a.T, a.D, kForwardWaves, kMaxBlocks);
     if (a.cache.type == QG_F8)
         return by_type(

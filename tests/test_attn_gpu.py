@@ -143,6 +143,24 @@ def test_what_is_not_turned_stays_with_its_infinities():
     assert torch.isnan(y[1, 0, 101]) and torch.isfinite(y[1, 0, 102:]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_the_norm_is_the_same_however_many_pairs_turn(D, dtype):
+    """The squares are summed in one order: what no pair turns has the bits that it has where none does."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(D)
+    q, k = (_rows(rng, 300, n, D, dtype) for n in (4, 2))
+    gains = [to_dev((1 + 0.3 * rng.normal(size=D)).astype(np.float32)) for _ in "qk"]
+    pos = to_dev(rng.integers(0, 5000, 300).astype(np.int32))
+    still = qg().qhead_norm_rope(q, k, pos, None, *gains, EPS, dtype=torch.float32)
+    rot = 8
+    while rot < D:
+        freq = to_dev(rng.uniform(0.001, 1, rot // 2).astype(np.float32))
+        for y, z in zip(qg().qhead_norm_rope(q, k, pos, freq, *gains, EPS, dtype=torch.float32), still):
+            assert torch.equal(y[..., rot:], z[..., rot:]), rot
+        rot *= 2
+
+
 @pytest.mark.parametrize("case", HEADS)
 def test_norm_rope_backward(case):
     h, q = _Heads(case), qg()
