@@ -835,11 +835,13 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
     // (us, runs / a sequence each; f8, D 128, 8 key heads, lengths from 0 to the table's): 1 sequence of 333 9.7 / 7.3,
     // of 1000 9.8 / 11.7 (with the host's part of a second launch 14.4 / 12.1), of 2000 10.2 / 19.0; 32 of up to 2000
     // 22.7 / 19.8, of 4000 32.6 / 35.6; 64 of 4000 49 / 47; 128 of 2000 58 / 47, of 4000 91 / 84.  By bytes of a key
-    // head's longest sequence; in bf16 64 of 8190 147 / 167; where a window makes all of them equal the last round of
-    // workgroups costs what the plan does.
-    const int64_t bytes = most * kTile * dim * (f8 ? 2 : 4), groups = B * kv_heads * c.row_groups;
-    c.by_sequence = bytes <= 256 << 10 ||
-                    (!window && ((bytes <= 512 << 10 && groups >= 256) || (bytes <= 1024 << 10 && groups >= 512)));
+    // head's longest sequence; in bf16 64 of 8190 147 / 167.
+    // The workspace is sized without the window, so a window may never turn this off: it shortens the sequences of
+    // the first rule (down from the table's), the others ask for the table's own.
+    const int64_t token = dim * (f8 ? 2 : 4), groups = B * kv_heads * c.row_groups;
+    const int64_t bytes = most * kTile * token, table = ceil_div(width * page, kTile) * kTile * token;
+    c.by_sequence = bytes <= 256 << 10 || (table <= 512 << 10 && groups >= 256) ||
+                    (table <= 1024 << 10 && groups >= 512);
     if (c.by_sequence)
         c.target = (int)B;
     return c;
@@ -887,6 +889,8 @@ hipError_t launch_attend(const AttendArgs &a, int q_type, hipStream_t stream)
     // (a window only makes the parts fewer)
     const Cut c = cut(a.B, a.M, a.q_heads, a.cache.heads, a.cache.dim, a.cache.type == QG_F8, a.cache.page, a.width,
                       a.window);
+    if (!c.by_sequence && !a.workspace)
+        return hipErrorInvalidValue;
     const AttendLaunch la{a, c.target, (int)c.units, c.rows, c.row_groups, c.by_sequence};
     if (a.cache.type == QG_F8)
         return q_type == QG_F16 ? of_dim<Fp16, true>(la, c, stream) : of_dim<Bf16, true>(la, c, stream);

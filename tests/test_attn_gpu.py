@@ -437,6 +437,18 @@ def test_attend_in_a_window(case, window):
     _Batch(*case).check(window=window)
 
 
+@pytest.mark.parametrize("window", [300, 1200, 1900, 100000])
+@pytest.mark.parametrize("M,H,KV,D,cache,q,width", [
+    (1, 8, 8, 128, "f8", "bfloat16", 32), (3, 8, 4, 64, "f8", "float16", 63),
+    (1, 16, 16, 128, "bfloat16", "bfloat16", 32)])
+def test_windows_of_many_sequences_under_a_table_of_middle_length(window, M, H, KV, D, cache, q, width):
+    """Where the table alone gives a workgroup a sequence, and so asks for no workspace, a window does too."""
+    from quantized_weight_gemv_amd import lib
+    lens = [2048, 1999, 0, 1] + [int(n) for n in np.random.default_rng(window).integers(0, 150, 60)]
+    assert lib().qattn_decode_workspace(len(lens), M, H, KV, D, {"f8": 3, "bfloat16": 2}[cache], 64, width) == 0
+    _Batch(lens, M, H, KV, D, 64, cache, q, width=width).check(window=window)
+
+
 @pytest.mark.parametrize("case", [ATTEND[2], ATTEND[9], ATTEND[14]])
 @pytest.mark.parametrize("kw", [dict(softcap=5.0), dict(softcap=50.0, window=40), dict(scale=0.0), dict(scale=-0.3),
                                 dict(scale=2.0)])
