@@ -803,6 +803,8 @@ def _turn(c, T: int, D: int, positions, inv_freq, q_gain, k_gain, eps, interleav
     half = inv_freq.numel() if inv_freq is not None else 0
     if not half:
         return gq, gk, gain_type, eps, None, 1, None, None, 0, 0
+    if positions is None:
+        raise TypeError("positions must be a device tensor")
     shape = positions.shape
     axes = shape[0] if len(shape) == 2 else 1
     if len(shape) > 2 or not shape or shape[-1] != T:

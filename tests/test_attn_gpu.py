@@ -665,6 +665,16 @@ def test_refusals_of_the_binding():
     torch.cuda.synchronize()
 
 
+def test_a_rotation_without_positions_is_refused():
+    q, torch = qg(), torch_cuda()
+    x = torch.zeros(4, 6, 128, device="cuda", dtype=torch.bfloat16)
+    f = torch.zeros(64, device="cuda")
+    for call in (lambda: q.qhead_norm_rope(x, x, None, f), lambda: q.qhead_norm_rope_backward(x, x, x, x, None, f)):
+        with pytest.raises(TypeError, match="positions"):
+            call()
+    assert torch.equal(q.qhead_norm_rope(x, x, None, None)[0], x)
+
+
 def test_calls_that_would_lose_a_gradient_are_refused():
     q, torch = qg(), torch_cuda()
     x = torch.randn(2, 4, 128, device="cuda", dtype=torch.bfloat16)
