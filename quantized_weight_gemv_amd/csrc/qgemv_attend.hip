@@ -34,7 +34,9 @@
 // anew only beyond a slack 102 / 169 / 74; loads that leave nothing in the caches, of
 // whole lines 92 / 159 / 73; runs of equal length in one round of workgroups, and a
 // bound on registers that keeps accumulators out of the other register file
-// 92 / 148 / 60; a lighter join 90 / 139 / 57.
+// 92 / 148 / 60; a lighter join 90 / 139 / 57; scores as distances by one fma, the
+// row's maximum across lanes only beyond the slack 89 / 139 / 56 (64 rows of 192
+// dimensions 77 to 74).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -435,10 +437,13 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
         };
 
         f4_t acc[kTiles][kOut];
-        float top[kTiles], sum[kTiles];
+        // A row's scores are held as their distance from `from`; the sums are taken anew from a larger one if a
+        // distance passes `limit`: any does while the row has seen nothing.
+        float from[kTiles], limit[kTiles], sum[kTiles];
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
-            top[n] = -__builtin_inff();
+            from[n] = 0.0f;
+            limit[n] = -__builtin_inff();
             sum[n] = 0.0f;
 #pragma unroll
             for (int d = 0; d < kOut; ++d)
@@ -505,9 +510,10 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                     for (int i = 0; i < 4; ++i) {
 #pragma unroll
                         for (int n = 0; n < kTiles; ++n) {
-                            s[n][4 * h + i] = c[n][i] * scale;
+                            float product = c[n][i];
                             if constexpr (kF8 && !kScaledKeys)
-                                s[n][4 * h + i] = ldexpf(s[n][4 * h + i], exponent_of(b.ks[h], i));
+                                product = ldexpf(product, exponent_of(b.ks[h], i));
+                            s[n][4 * h + i] = fmaf(product, scale, a.softcap > 0.0f ? 0.0f : -from[n]);
                         }
                     }
                 }
@@ -522,7 +528,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {   // cap tanh(x) log2 e, from e^2x
                             const float e2 = __builtin_amdgcn_exp2f(s[n][i] * (2.0f * kLog2e));
-                            s[n][i] = cap - 2.0f * cap * __builtin_amdgcn_rcpf(1.0f + e2);
+                            s[n][i] = fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(1.0f + e2), cap - from[n]);
                         }
                 }
                 if (edge(token) || !whole_tiles) {
@@ -554,25 +560,32 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                 typename V::v8 hi[kTiles], lo[kTiles];
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n) {
-                    float m = top[n];
+                    float m = s[n][0];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int i = 1; i < 8; ++i)
                         m = fmaxf(m, s[n][i]);
-                    m = max_over_groups(m);
-                    // weights up to 2^kSlack are as good as up to 1: the sums are scaled anew only beyond
-                    if (__any(m > top[n] + kSlack)) {
-                        const float old = __builtin_amdgcn_exp2f(top[n] - (m == -__builtin_inff() ? 0.0f : m));
+                    // weights up to 2^kSlack are as good as up to 1: only beyond is the row's largest score looked for
+                    // (its lanes are four) and everything scaled anew
+                    if (__any(m > limit[n])) {
+                        m = max_over_groups(m);
+                        const bool fresh = limit[n] == -__builtin_inff(), none = m == -__builtin_inff();
+                        const float by = fresh ? (none ? 0.0f : m) : fmaxf(m, 0.0f);
+                        const float old = fresh ? 0.0f : __builtin_amdgcn_exp2f(-by);
                         sum[n] *= old;
 #pragma unroll
                         for (int d = 0; d < kOut; ++d)
                             acc[n][d] *= old;
-                        top[n] = m;
+                        from[n] += by;
+                        if (!none)
+                            limit[n] = kSlack;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            s[n][i] -= by;
                     }
-                    const float from = top[n] == -__builtin_inff() ? 0.0f : top[n];
                     float w[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float e = __builtin_amdgcn_exp2f(s[n][i] - from);
+                        const float e = __builtin_amdgcn_exp2f(s[n][i]);
                         sum[n] += e;
                         w[i] = e * kWeight;
                         if constexpr (kF8)   // (of 0 too: the scale of a place without a token may be anything)
@@ -664,7 +677,7 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
             const float l = sum_over_groups(sum[n]);
             __syncthreads();   // (the last tile's or sequence's readers)
             if (g == 0)
-                ml[wave][r16][0] = top[n], ml[wave][r16][1] = l;
+                ml[wave][r16][0] = limit[n] == kSlack ? from[n] : -__builtin_inff(), ml[wave][r16][1] = l;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -810,8 +823,11 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
 
 // Tiles of 16 rows a workgroup takes: one or two, more rows in groups that read the
 // cache each.  (Four tiles, one wave a SIMD, at 128 dimensions: 64 rows a key head in
-// f8 74 us for 56, 128 rows 109 for 85; in bf16 74 for 55, 106 for 91.)
-int tiles_of_rows(int rows) { return rows <= 16 ? 1 : 2; }
+// f8 74 us for 56, 128 rows 109 for 85; in bf16 74 for 55, 106 for 91.)  One where two
+// spill: 256 dimensions in 16 bits, 16 sequences of up to 8000, 20 / 32 / 64 rows a key
+// head 107 / 113 / 173 us for 119 / 124 / 165, 8 of up to 20000 with 256 rows 107 for 113.
+constexpr int most_tiles(int D, bool f8) { return D == 256 && !f8 ? 1 : 2; }
+int tiles_of_rows(int rows, int D, bool f8) { return rows <= 16 ? 1 : most_tiles(D, f8); }
 
 struct Cut {
     int rows, tiles, row_groups, target;
@@ -823,7 +839,7 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
 {
     Cut c;
     c.rows = M * (q_heads / kv_heads);
-    c.tiles = tiles_of_rows(c.rows);
+    c.tiles = tiles_of_rows(c.rows, dim, f8);
     c.row_groups = (c.rows + 16 * c.tiles - 1) / (16 * c.tiles);
     c.target = std::max(1, kRounds * kUnits * resident(dim, f8, c.tiles) / (kv_heads * c.row_groups));
     // no sequence has more tiles than this: no more runs than tiles
@@ -835,7 +851,8 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
     // (us, runs / a sequence each; f8, D 128, 8 key heads, lengths from 0 to the table's): 1 sequence of 333 9.7 / 7.3,
     // of 1000 9.8 / 11.7 (with the host's part of a second launch 14.4 / 12.1), of 2000 10.2 / 19.0; 32 of up to 2000
     // 22.7 / 19.8, of 4000 32.6 / 35.6; 64 of 4000 49 / 47; 128 of 2000 58 / 47, of 4000 91 / 84.  By bytes of a key
-    // head's longest sequence; in bf16 64 of 8190 147 / 167.
+    // head's longest sequence; in bf16 64 of 8190 147 / 167.  In windows of 1200 and 1500 32 of 2000 21.5 / 16.1 and
+    // 23.0 / 17.3, of 1500 and 3000 64 of 4000 38 / 33 and 52 / 53.
     // The workspace is sized without the window, so a window may never turn this off: it shortens the sequences of
     // the first rule (down from the table's), the others ask for the table's own.
     const int64_t token = dim * (f8 ? 2 : 4), groups = B * kv_heads * c.row_groups;
@@ -850,9 +867,10 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
 template <typename TQ, bool kF8, int D>
 hipError_t launch(const AttendLaunch &la, const Cut &c, hipStream_t stream)
 {
-    void (*fn)(AttendLaunch) = c.tiles == 1        ? &attend_kernel<TQ, kF8, D, 1, true>
-                               : c.row_groups == 1 ? &attend_kernel<TQ, kF8, D, 2, true>
-                                                   : &attend_kernel<TQ, kF8, D, 2, false>;
+    constexpr int kMost = most_tiles(D, kF8);
+    void (*fn)(AttendLaunch) = c.row_groups > 1 ? &attend_kernel<TQ, kF8, D, kMost, false>
+                               : c.tiles == 1   ? &attend_kernel<TQ, kF8, D, 1, true>
+                                                : &attend_kernel<TQ, kF8, D, kMost, true>;
     const hipError_t e = launch_kernel(reinterpret_cast<const void *>(fn),
                                        dim3((unsigned)(c.target * la.a.cache.heads * c.row_groups)), dim3(kBlock), 0,
                                        stream, la);
