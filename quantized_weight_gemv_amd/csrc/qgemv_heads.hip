@@ -313,6 +313,36 @@ __device__ __forceinline__ F inverse_norm(const F (&v)[8], int split, F inverse_
     return inverse_root(ss * inverse_dim + (F)eps);
 }
 
+// The same of 192 elements: separate operations take 32 sums there, the first 16 of
+// two fours added element by element.  No lanes hold those, so the squares go through
+// LDS, within the wave (8192 tokens of 40 + 8 + 8 heads into a 16-bit cache and read
+// back 113 us for 111).
+__device__ __forceinline__ float inverse_norm_192(const Place &p, const float (&v)[8], float eps)
+{
+#pragma clang fp contract(off)
+    __shared__ __attribute__((aligned(16))) float squares[kBlock / 64][2][192];
+    float *row = squares[threadIdx.x >> 6][p.sub];
+    if (p.on) {
+        *reinterpret_cast<f4_t *>(row + p.lo) = f4_t{v[0] * v[0], v[1] * v[1], v[2] * v[2], v[3] * v[3]};
+        *reinterpret_cast<f4_t *>(row + p.hi) = f4_t{v[4] * v[4], v[5] * v[5], v[6] * v[6], v[7] * v[7]};
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    f4_t q = *reinterpret_cast<const f4_t *>(row + 4 * p.l);
+    if (p.l < 16)
+        q += *reinterpret_cast<const f4_t *>(row + 128 + 4 * p.l);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();   // (the next vector's squares)
+    float ss = ((q[0] + q[1]) + q[2]) + q[3];
+    ss = add_lanes<1>(ss);
+    ss = add_lanes<2>(ss);
+    ss = add_lanes<4>(ss);
+    ss = add_lanes<8>(ss);
+    ss = add_lanes<16>(ss);
+    return inverse_root(ss * (1.0f / 192.0f) + eps);
+}
+
 // A lane's eight values of an f8 vector held by L lanes: codes and scale byte,
 // by the rule of f8_quantize16.
 template <int L>
@@ -393,7 +423,11 @@ __device__ __forceinline__ void norm_turn(const HeadArgs &a, const Place &p, con
 {
 #pragma clang fp contract(off)
     if (a.gain[0]) {
-        const F r = inverse_norm<L>(v, a.split, (F)1 / (F)a.D, a.eps);
+        F r;
+        if constexpr (L == 32 && sizeof(F) == 4)
+            r = a.D == 192 ? inverse_norm_192(p, v, a.eps) : inverse_norm<L>(v, a.split, (F)1 / (F)a.D, a.eps);
+        else
+            r = inverse_norm<L>(v, a.split, (F)1 / (F)a.D, a.eps);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = v[i] * r * (F)gain[i];

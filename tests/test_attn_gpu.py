@@ -143,7 +143,7 @@ def test_what_is_not_turned_stays_with_its_infinities():
     assert torch.isnan(y[1, 0, 101]) and torch.isfinite(y[1, 0, 102:]).all()
 
 
-@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_the_norm_is_the_same_however_many_pairs_turn(D, dtype):
     """The squares are summed in one order: what no pair turns has the bits that it has where none does."""
