@@ -27,8 +27,8 @@
 //
 // Bound by the cache's bytes where rows are few: 262143 tokens of 8 key heads in f8
 // (541 MB) 84 us, 6.4 TB/s, with the loads alone at 6.8; 64 ragged sequences in
-// bf16 (877 MB) 136 us, 6.4 TB/s; vector units 40 and 16 % busy.  With 30 rows
-// (f8, 230 MB) 49 us: the vector units are 60 % busy with softmax and conversions.
+// bf16 (877 MB) 136 us, 6.4 TB/s; vector units 37 and 15 % busy.  With 30 rows
+// (f8, 230 MB) 48 us: the vector units are 58 % busy with softmax and conversions.
 // Steps on the way (us, 262143 tokens / ragged / 30 rows): work in equal chunks of a
 // sequence 108 / 167 / 79; scale factors by ldexp and with the widening, sums scaled
 // anew only beyond a slack 102 / 169 / 74; loads that leave nothing in the caches, of
@@ -191,7 +191,8 @@ __device__ __forceinline__ int exponent_of(uint32_t bytes, int i) { return (int)
 // nothing behind in the caches stream at 6.8 TB/s where ordinary ones reach 5.9
 // (541 MB in pages of 64 tokens, loads alone); they have to take whole lines, or the
 // other half is read again.  Where several groups of rows read the same cache,
-// ordinary loads find it in the caches (128 rows a key head in bf16 91 us for 121).
+// ordinary loads find it in the caches (16 sequences of up to 8000, 128 rows a key
+// head in bf16 104 us for 120).
 template <int kWords, bool kOnce>
 __device__ __forceinline__ void load_words(const uint8_t *from, uint32_t *to)
 {
@@ -822,10 +823,11 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
 }
 
 // Tiles of 16 rows a workgroup takes: one or two, more rows in groups that read the
-// cache each.  (Four tiles, one wave a SIMD, at 128 dimensions: 64 rows a key head in
-// f8 74 us for 56, 128 rows 109 for 85; in bf16 74 for 55, 106 for 91.)  One where two
-// spill: 256 dimensions in 16 bits, 16 sequences of up to 8000, 20 / 32 / 64 rows a key
-// head 107 / 113 / 173 us for 119 / 124 / 165, 8 of up to 20000 with 256 rows 107 for 113.
+// cache each.  (Four tiles, one wave a SIMD, at 128 dimensions, the cache in part in the
+// last-level one: 64 rows a key head in f8 74 us for 56, 128 rows 109 for 85; in bf16 74
+// for 55, 106 for 91.)  One where two spill: 256 dimensions in 16 bits, 16 sequences of up
+// to 8000, 20 / 32 / 64 / 128 rows a key head 110 / 117 / 176 / 311 us for 121 / 126 / 169
+// / 281, 8 of up to 20000 with 256 rows 111 for 115.
 constexpr int most_tiles(int D, bool f8) { return D == 256 && !f8 ? 1 : 2; }
 int tiles_of_rows(int rows, int D, bool f8) { return rows <= 16 ? 1 : most_tiles(D, f8); }
 
