@@ -115,7 +115,7 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
  * Token i of the M new ones stands at place p = lens[b] - M + i and sees the
  * places max(0, p - window + 1) .. p (window 0: all up to p):
  *   s = scale * q.k,  softcap > 0: s = softcap * tanh(s / softcap)  (scale /
- *   softcap finite),
+ *   softcap finite; right to a few 2^-24 of the score however large the cap),
  *   out = sum softmax(s) v          [B][M][q_heads][dim], q_type, contiguous.
  * A query that sees no token gets zeros.  lens are held to 0 .. width * page;
  * a table entry outside 0 .. pages - 1 holds no tokens.  What lies in places

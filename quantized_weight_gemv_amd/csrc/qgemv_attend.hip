@@ -41,6 +41,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <limits>
 
 #include "qgemv_attn_internal.h"
 
@@ -229,6 +230,20 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)
         return ((((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u) >> 15) * 65535u;
 }
 
+// cap tanh(x), x = product to_cap, a score in powers of two.  Up to |x| = 1/2 it is the
+// score without a cap times tanh(x) / x, a series in x^2 (its coefficients for the least
+// largest error there, 2^-26 of the value): right to a few 2^-24 of the score however
+// large the cap is, where 1 - 2 / (1 + e^2x) alone is off by as much of the cap.
+__device__ __forceinline__ float capped_score(float product, float to_score, float to_cap, float cap)
+{
+    const float x = product * to_cap, z = x * x;
+    const float ratio =
+        fmaf(fmaf(fmaf(fmaf(0.01724149f, z, -0.05304549f), z, 0.13325879f), z, -0.33333144f), z, 1.0f);
+    const float e2 = __builtin_amdgcn_exp2f(fabsf(x) * (2.0f * kLog2e));
+    const float far = cap * fmaf(-2.0f, __builtin_amdgcn_rcpf(1.0f + e2), 1.0f);
+    return fabsf(x) <= 0.5f ? product * to_score * ratio : copysignf(far, x);
+}
+
 __device__ __forceinline__ float max_over_groups(float v)
 {
     f2_t p = pair16(v);
@@ -286,6 +301,8 @@ struct AttendLaunch {
     int rows;       // M share
     int row_groups;
     bool by_sequence;   // a workgroup a sequence, nothing to find or to join
+    float to_score;     // scale in powers of two
+    float to_cap, cap;  // scale / softcap, the cap in powers of two
 };
 
 // TQ: type of q, of the output and of 16-bit caches; kF8: an 8-bit cache; kOnce: no
@@ -462,8 +479,8 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
         const int all_end = seq.len - a.M + 1;
         const int all_from = a.window ? max(0, seq.len - a.window) : 0;
         const int any_from = a.window ? max(0, all_end - a.window) : 0;
-        const float scale = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
-        const float cap = a.softcap * kLog2e;
+        // (under a cap products stay as they are until capped_score)
+        const float scale = a.softcap > 0.0f ? 1.0f : la.to_score;
 
         auto edge = [&](int at) { return at + kStep > all_end || at < all_from; };
         bool left_out = false;   // values that are not finite, of places that some rows do not see
@@ -527,10 +544,8 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
 #pragma unroll
                     for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {   // cap tanh(x) log2 e, from e^2x
-                            const float e2 = __builtin_amdgcn_exp2f(s[n][i] * (2.0f * kLog2e));
-                            s[n][i] = fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(1.0f + e2), cap - from[n]);
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            s[n][i] = capped_score(s[n][i], la.to_score, la.to_cap, la.cap) - from[n];
                 }
                 if (edge(token) || !whole_tiles) {
 #pragma unroll
@@ -911,7 +926,9 @@ hipError_t launch_attend(const AttendArgs &a, int q_type, hipStream_t stream)
                       a.window);
     if (!c.by_sequence && !a.workspace)
         return hipErrorInvalidValue;
-    const AttendLaunch la{a, c.target, (int)c.units, c.rows, c.row_groups, c.by_sequence};
+    const AttendLaunch la{a, c.target, (int)c.units, c.rows, c.row_groups, c.by_sequence, a.scale * kLog2e,
+                          a.softcap > 0.0f ? a.scale / a.softcap : 0.0f,
+                          std::min(a.softcap * kLog2e, std::numeric_limits<float>::max())};
     if (a.cache.type == QG_F8)
         return q_type == QG_F16 ? of_dim<Fp16, true>(la, c, stream) : of_dim<Bf16, true>(la, c, stream);
     return q_type == QG_F16 ? of_dim<Fp16, false>(la, c, stream) : of_dim<Bf16, false>(la, c, stream);
