@@ -21,7 +21,8 @@
  * positions: int32 [axes][T], 1 <= axes <= 4 (time, height, width, ...);
  * pair i takes axis 0 if i < sections[0], axis 1 for the next sections[1]
  * pairs and so on, the sections summing up to rot / 2.  Any int32 is a
- * position.  The angle is taken in 64 bits and reduced before the sine.
+ * position: the angle's whole turns are taken out exactly to 2^-53 of a turn
+ * (up to 2^51 turns), whatever their number.
  * freq: fp32 [rot / 2]; gains: type gain_type [D].
  * Everything is computed in fp32 and rounded once.  The gradient of a row
  * needs nothing of the forward pass but its inputs.

@@ -27,7 +27,8 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int kMaxBlocks = 1 << 20;
-constexpr double kInvTwoPi = 0.15915494309189533577;
+// 1 / (2 pi) and what its 64 bits leave out.
+constexpr double kInvTwoPi = 0.15915494309189535, kInvTwoPiRest = -9.839338337591243e-18;
 
 struct __attribute__((packed, aligned(4))) Raw16f {
     uint32_t w[4];
@@ -195,10 +196,21 @@ __device__ __forceinline__ void sin_cos(double turn, double &s, double &c)
     c = ((q + 1) & 2) ? -c : c;
 }
 
-// Turns of the four pairs of a lane at a token's positions: position * freq /
-// 2 pi in 64 bits, whose whole turns are dropped first; cosine and sine in 64
-// bits too (the vector units do those as fast as fp32), so that in fp32 they are
-// the nearest ones.
+// position * freq / 2 pi without its whole turns.  The product of the two is exact in
+// two parts, 1 / 2 pi has two parts, and the whole turns leave by an fma: the error is
+// 2^-53 of a turn wherever the position is, where products of one part are off by
+// 2^-53 of all the turns (half a step of an fp32 cosine from positions of 2^27 on).
+__device__ __forceinline__ double turn_of(int position, float freq)
+{
+    const double angle = (double)position * (double)freq;
+    const double rest = fma((double)position, (double)freq, -angle);
+    const double whole = rint(angle * kInvTwoPi);
+    return fma(angle, kInvTwoPi, -whole) + fma(angle, kInvTwoPiRest, rest * kInvTwoPi);
+}
+
+// Cosines and sines of the four pairs of a lane at a token's positions, in 64 bits
+// too (the vector units do those as fast as fp32), so that in fp32 they are the
+// nearest ones but for a value within a few 2^-53 of a border.
 template <typename F>
 __device__ __forceinline__ void turns(const HeadArgs &a, const Place &p, int64_t t, F (&c)[4], F (&s)[4])
 {
@@ -213,10 +225,8 @@ __device__ __forceinline__ void turns(const HeadArgs &a, const Place &p, int64_t
         int axis = 0;
         for (int j = 0; j + 1 < a.axes; ++j)
             axis += 4 * p.l + i >= a.sections[j] ? 1 : 0;
-        double turn = (double)a.positions[axis * a.T + t] * (double)__uint_as_float(f.w[i]) * kInvTwoPi;
-        turn -= rint(turn);
         double sine, cosine;
-        sin_cos(turn, sine, cosine);
+        sin_cos(turn_of(a.positions[axis * a.T + t], __uint_as_float(f.w[i])), sine, cosine);
         c[i] = (F)cosine, s[i] = (F)sine;
     }
 }

@@ -4,7 +4,8 @@ import numpy as np
 import pytest
 
 import attn_util as au
-from gpu_util import torch_cuda
+import f8_util as fu
+from gpu_util import qg, to_dev, torch_cuda
 from test_attn_gpu import _Batch
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +68,53 @@ def test_caps_of_every_size(case, cap, window, wide):
     y = b.run(scale=scale, window=window, softcap=cap)
     out, bound = _capped(b, float(np.float32(scale)), window, float(np.float32(cap)))
     au.assert_attend(_np(y), out, bound, b.q_type, f"cap {cap}")
+
+
+# -------------------------------------------------------------- far positions
+FAR = (1 << 31) - 1, -(1 << 31), (1 << 30) + 7, -(1 << 29) - 3, (1 << 27) + 1, 1 << 24, 131071, -1
+
+
+def _turns(pos, freq):
+    """cos, sin [T][1][pairs] of the exact angles: position * freq has 55 bits, 64 are kept here."""
+    assert np.finfo(np.longdouble).nmant >= 63
+    angle = np.asarray(pos, np.longdouble)[:, None] * np.asarray(freq, np.float32).astype(np.longdouble)
+    return np.cos(angle).astype(np.float64)[:, None], np.sin(angle).astype(np.float64)[:, None]
+
+
+def _freq(rng, n):
+    """From 1, the first pair's of every usual rotation, down."""
+    return np.concatenate([[1.0], rng.uniform(0.4, 1, n - 1)]).astype(np.float32)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_the_angle_of_a_far_position_is_as_good_as_of_a_near_one(interleaved, dtype):
+    """Forward and backward without a norm: cosine and sine half a step off, two products and a sum rounded, at any
+    position: 3 half steps of 2^-24 of |a| + |b|."""
+    q, torch = qg(), torch_cuda()
+    rng = np.random.default_rng(8)
+    T, D = len(FAR), 128
+    freq = _freq(rng, D // 2)
+    x = to_dev(rng.normal(size=(T, 16, D)).astype(np.float32)).to(getattr(torch, dtype))
+    pos = to_dev(np.array(FAR, np.int32))
+    cos, sin = _turns(FAR, freq)
+    how = dict(interleaved=interleaved)
+    y, _ = q.qhead_norm_rope(x, None, pos, to_dev(freq), dtype=torch.float32, **how)
+    bound = 3 * U * au.spread(_np(x), D, interleaved)
+    fu.assert_close(_np(y), au.rotate(_np(x), cos, sin, D, interleaved), bound, "forward")
+    d = q.qhead_norm_rope_backward(x, None, x.float(), None, pos, to_dev(freq), **how)[0]
+    fu.assert_close(_np(d), au.rotate(_np(x), cos, -sin, D, interleaved), bound, "backward")
+
+
+def test_keys_of_far_positions_have_the_codes_of_the_exact_values():
+    q, torch = qg(), torch_cuda()
+    rng = np.random.default_rng(9)
+    T, H, D = 2048, 4, 128
+    freq = _freq(rng, D // 2)
+    pos = rng.integers(-(1 << 31), 1 << 31, T).astype(np.int32)
+    x = to_dev(rng.normal(size=(T, 3 * H, D)).astype(np.float32))
+    cache = q.qkv_cache(T // 64, 64, H, D)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    q.qkv_norm_rope_write(cache, x[:, :H], x[:, H:2 * H], x[:, 2 * H:], slots, to_dev(pos), to_dev(freq))
+    want = au.rotate(_np(x[:, H:2 * H]), *_turns(pos, freq), D, False)
+    assert np.array_equal(_np(q.qkv_read(cache, slots)[0]), au.held(want, "f8")[0])
