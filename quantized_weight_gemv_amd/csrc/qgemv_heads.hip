@@ -453,10 +453,12 @@ __global__ __launch_bounds__(kBlock) void head_kernel(HeadArgs a)
 {
     const Place p = place<L>(a.D, a.half, a.interleaved);
     const int k0 = a.groups[0], v0 = k0 + a.groups[1], all = v0 + (kWrite ? a.groups[2] : 0);
+    // (lanes without elements take the first ones' gains: a vector's quantization looks at their zeros too)
     float gain[2][8];
-    if (a.gain[0] && p.on) {
-        load8_as(a.gain_type, a.gain[0], 0, p.lo, p.hi, gain[0]);
-        load8_as(a.gain_type, a.gain[1], 0, p.lo, p.hi, gain[1]);
+    if (a.gain[0]) {
+        const int lo = p.on ? p.lo : 0, hi = p.on ? p.hi : 4;
+        load8_as(a.gain_type, a.gain[0], 0, lo, hi, gain[0]);
+        load8_as(a.gain_type, a.gain[1], 0, lo, hi, gain[1]);
     }
     const int first = (int)(blockIdx.y * all / gridDim.y), upto = (int)((blockIdx.y + 1) * all / gridDim.y);
     for (int64_t t = (int64_t)blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); t < a.T;
