@@ -287,8 +287,9 @@ __device__ __forceinline__ F add_lanes(F v)
 // 1 / sqrt(mean of squares + eps).  Squares round by themselves and are summed four
 // neighbours first (one after the other; in pairs up to 64 elements), then
 // neighbouring fours: the order in which the mean of a row of 64, 128 or 256 is
-// taken by separate operations on this card, so that those give the same bits.  The
-// first `split` lanes (a power of two) have one four of either half of the turned
+// taken by separate operations on this card.  Any order is as exact; in this one those
+// give the same bits (a test compares them), so that 16-bit caches hold the same bytes
+// whichever of the two wrote them.  The first `split` lanes (a power of two) have one four of either half of the turned
 // elements: the halves are summed apart until they are neighbours.
 template <int L, typename F>
 __device__ __forceinline__ F inverse_norm(const F (&v)[8], int split, F inverse_dim, float eps)
@@ -326,7 +327,7 @@ __device__ __forceinline__ F inverse_norm(const F (&v)[8], int split, F inverse_
 // The same of 192 elements: separate operations take 32 sums there, the first 16 of
 // two fours added element by element.  No lanes hold those, so the squares go through
 // LDS, within the wave (8192 tokens of 40 + 8 + 8 heads into a 16-bit cache and read
-// back 113 us for 111).
+// back 113 us, 111 in the lanes' own order).
 __device__ __forceinline__ float inverse_norm_192(const Place &p, const float (&v)[8], float eps)
 {
 #pragma clang fp contract(off)

@@ -1,4 +1,5 @@
-"""Norms of head vectors: heads of 192 elements, whose lanes are not all in use, against the binary64 references."""
+"""Norms of head vectors: heads of 192 elements, whose lanes are not all in use, against the binary64 references, and
+the bits that separate operations give."""
 import numpy as np
 import pytest
 
@@ -61,3 +62,39 @@ def test_rows_of_zeros_between_others(eps):
     n = want[~zero & heads]
     base.fu.assert_close(got[~zero & heads], n, base.au.HEADS * np.abs(n), "q")
     assert np.array_equal(got[~zero & ~heads], base.au.held(want[~zero & ~heads], "f8")[0])
+
+
+def _separate(x, gain, cos, sin, rot, interleaved):
+    """The norm and the rotation by one operation after the other, in fp32."""
+    torch = torch_cuda()
+    x = x.float()
+    x = x * torch.rsqrt((x * x).mean(-1, keepdim=True) + base.EPS) * gain
+    if not rot:
+        return x
+    a, b = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
+    y = x.clone()
+    y[..., a] = x[..., a] * cos - x[..., b] * sin
+    y[..., b] = x[..., b] * cos + x[..., a] * sin
+    return y
+
+
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+def test_the_bits_of_separate_operations(D, dtype):
+    """Squares are summed in the order that a mean over these row lengths takes, the root is the nearest, every
+    product rounds by itself, and cosine and sine are the nearest: no bit differs (another order of that mean, in
+    another release, shows here)."""
+    q, torch = qg(), torch_cuda()
+    rng = np.random.default_rng(D)
+    for T, H in ((1, 1), (1, 7), (5, 32), (300, 3), (5000, 8)):
+        x = rng.normal(size=(T, H, D)) * np.exp(rng.normal(size=(T, H, 1)))
+        x = to_dev(x.astype(np.float32)).to(getattr(torch, dtype))
+        gain = to_dev((1 + 0.2 * rng.normal(size=D)).astype(np.float32))
+        pos = to_dev(rng.integers(0, 1 << 17, T).astype(np.int32))
+        for rot, interleaved in ((0, False), (D, False), (D, True), (D // 16 * 8, True), (32, False)):
+            freq = to_dev(np.exp(-np.arange(rot // 2) / max(rot // 2, 1) * 13).astype(np.float32))
+            angle = pos.double()[:, None, None] * freq.double()
+            want = _separate(x, gain, torch.cos(angle).float(), torch.sin(angle).float(), rot, interleaved)
+            got = q.qhead_norm_rope(x, None, pos, freq if rot else None, gain, interleaved=interleaved,
+                                    dtype=torch.float32)[0]
+            assert torch.equal(got, want), (T, H, rot, interleaved)
