@@ -9,8 +9,9 @@ and sizes (the C ABI cannot see buffer sizes), passes raw pointers and the
 current HIP stream, and turns a non-zero status into an exception.  Every step
 of the computation runs in the library's HIP kernels; there is no fallback.
 Autograd records none of the calls.  The f8, routing and attention calls
-refuse tensors that require a gradient while gradients are recorded; torch.autograd.Function's forward and backward run
-without.
+refuse tensors that require a gradient while gradients are recorded, and
+tensors with a forward-mode tangent; torch.autograd.Function's forward and
+backward run without either.
 If the library is missing the import of any entry point fails loudly.
 
 Names follow the C ABI in include/qgemv.h, include/qgemv_f8.h and
@@ -430,29 +431,35 @@ class _Call:
     """One call's device: every tensor has to be on it, and the call is made
     with it as the current device, on its current stream."""
 
-    __slots__ = ("device", "index", "torch")
+    __slots__ = ("device", "dual", "index", "torch")
 
     def __init__(self, first, name: str):
         self.torch = torch = _torch()
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError(f"{name} must be a device tensor")
-        if first.requires_grad:
-            self.no_grad(name)
+        # a level of forward-mode differentiation is open: tensors may have tangents
+        self.dual = torch.autograd.forward_ad._current_level >= 0
+        if first.requires_grad or self.dual:
+            self.no_grad(first, name)
         self.device = first.device
         self.index = first.get_device()
 
-    def no_grad(self, name: str):
-        # the calls are not recorded: an output without a gradient would end the backward pass unseen
-        if self.torch.is_grad_enabled():
+    def no_grad(self, t, name: str):
+        # the calls are not recorded: an output without a gradient would end the backward pass unseen, one
+        # without a tangent the forward pass
+        if t.requires_grad and self.torch.is_grad_enabled():
             raise ValueError(f"{name} requires a gradient, which this call would not pass on: make it under "
                              "torch.no_grad() or inside a torch.autograd.Function")
+        if self.dual and self.torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{name} has a forward-mode tangent, which this call would not pass on: make it "
+                             "inside a torch.autograd.Function with a jvp")
 
     def ptr(self, t, dtype, name: str, numel: int):
         # one pass over what has to hold; the reasons are looked up only for a refusal
         if isinstance(t, self.torch.Tensor) and t.get_device() == self.index and t.dtype is dtype and \
                 t.numel() >= numel and t.is_contiguous():
-            if t.requires_grad:
-                self.no_grad(name)
+            if t.requires_grad or self.dual:
+                self.no_grad(t, name)
             return t.data_ptr()
         if not isinstance(t, self.torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a device tensor")
@@ -773,8 +780,8 @@ def _rows(c, x, name: str, dtype, T: int, D: int, heads=None):
         if t == T and d == D and (heads is None or n == heads):
             ld, of_head, of_element = x.stride()
             if (of_element == 1 or D == 1) and (of_head == D or n == 1):
-                if x.requires_grad:
-                    c.no_grad(name)
+                if x.requires_grad or c.dual:
+                    c.no_grad(x, name)
                 return x.data_ptr(), ld if T > 1 else n * D, n
             raise ValueError(f"{name}: the heads of a token must be contiguous")
     if not isinstance(x, c.torch.Tensor) or not x.is_cuda:
