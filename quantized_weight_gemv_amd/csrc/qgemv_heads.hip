@@ -231,23 +231,29 @@ __device__ __forceinline__ void turns(const HeadArgs &a, const Place &p, int64_t
     }
 }
 
-template <typename F>
+// kCopy: a copy in front of the branches keeps the values in registers.  The gradient
+// needs it (without one a lane's eight values went to memory and back for every head
+// with fp32 inputs: 16384 tokens of 32 + 8 heads, inputs and gradients in fp32, 282 us
+// for 196); the kernels that write a cache would take five more registers and a wave less.
+template <bool kCopy = false, typename F>
 __device__ __forceinline__ void turn(const Place &p, bool interleaved, const F (&c)[4], const F (&s)[4], F (&v)[8])
 {
 #pragma clang fp contract(off)   // each product rounds by itself, as in a program of separate operations
     if (!p.turned)
         return;   // (what is not turned is left as it is, infinities too)
+    const F copy[8] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+    const F(&w)[8] = kCopy ? copy : v;
     if (interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const F x = v[2 * i], y = v[2 * i + 1];
+            const F x = w[2 * i], y = w[2 * i + 1];
             v[2 * i] = x * c[i] - y * s[i];
             v[2 * i + 1] = y * c[i] + x * s[i];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const F x = v[i], y = v[4 + i];
+            const F x = w[i], y = w[4 + i];
             v[i] = x * c[i] - y * s[i];
             v[4 + i] = y * c[i] + x * s[i];
         }
@@ -591,7 +597,7 @@ __global__ __launch_bounds__(kBlock) void head_backward_kernel(HeadGradArgs ga)
             dy.values(is, h);
             if (group + 1 < last)
                 fetch(group + 1);
-            turn(p, a.interleaved, c, s, h);
+            turn<true>(p, a.interleaved, c, s, h);
             if (normed) {
                 float v[8], ss = 0.0f, dot = 0.0f;
                 now.values(is, v);
