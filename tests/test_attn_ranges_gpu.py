@@ -118,3 +118,13 @@ def test_keys_of_far_positions_have_the_codes_of_the_exact_values():
     q.qkv_norm_rope_write(cache, x[:, :H], x[:, H:2 * H], x[:, 2 * H:], slots, to_dev(pos), to_dev(freq))
     want = au.rotate(_np(x[:, H:2 * H]), *_turns(pos, freq), D, False)
     assert np.array_equal(_np(q.qkv_read(cache, slots)[0]), au.held(want, "f8")[0])
+
+
+# ------------------------------------------------------- rows of a key head
+@pytest.mark.parametrize("cache", ["bfloat16", "float16", "f8"])
+@pytest.mark.parametrize("M,share", [(1, 16), (1, 17), (5, 4), (8, 4), (3, 11), (12, 4), (16, 5), (4, 33)])
+def test_rows_of_a_key_head_around_the_tiles_at_256_dimensions(cache, M, share):
+    """One tile of 16 rows, two, groups of two, the last ones filled in part; runs over a long table and not."""
+    q = "bfloat16" if cache == "f8" else cache
+    for width in (None, 2500):
+        _Batch([150, M, 37, 0], M, 2 * share, 2, 256, 16, cache, q, width=width).check()
