@@ -124,8 +124,8 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
  * exact with fp32 sums (8-bit keys beside bf16 queries down to multiples of
  * 2^-133); the softmax's weights enter the second product as two
  * 16-bit parts (2^-16 of a weight is lost); one rounding to q_type.
- * workspace: qattn_decode_workspace bytes (0: may be NULL), 16-byte aligned,
- * used by this call only. */
+ * workspace: qattn_decode_workspace bytes (0: may be NULL; at most 33 MiB,
+ * however many sequences there are), 16-byte aligned, used by this call only. */
 size_t qattn_decode_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int cache_type, int page,
                               int64_t width);
 qg_status qattn_decode(const void *cache, int64_t pages, int page, int kv_heads, int dim, int cache_type,

@@ -78,8 +78,8 @@ __device__ __forceinline__ int scalar_int(const int32_t *p, int64_t i)
 // (its rows are written in any case).  The tiles of all sequences, one after the
 // other, are dealt out in runs of `run` to the workgroups of a key head, so each
 // has the same work whatever the lengths are; a run may end inside a sequence
-// and begin the next one.  Run w's part of sequence b is number w + b of all
-// parts (both only grow along the runs).
+// and begin the next one.  Only sequences that a run's end cuts leave parts: at most
+// one that the run before began and one that the run after goes on with.
 struct Sequence {
     int len;
     int first;          // its first token that anybody sees, down to a multiple of 16
@@ -301,9 +301,18 @@ struct AttendLaunch {
     int rows;       // M share
     int row_groups;
     bool by_sequence;   // a workgroup a sequence, nothing to find or to join
+    bool by_run;        // no more runs than sequences
     float to_score;     // scale in powers of two
     float to_cap, cap;  // scale / softcap, the cap in powers of two
 };
+
+// The number of a run's part of a sequence that begins in it or before it: two of each
+// run or, where that is fewer, run + sequence (both only grow along the runs).
+template <bool kByRun>
+__device__ __forceinline__ int part_of(int run, int b, bool begins)
+{
+    return kByRun ? 2 * run + (begins ? 1 : 0) : run + b;
+}
 
 // TQ: type of q, of the output and of 16-bit caches; kF8: an 8-bit cache; kOnce: no
 // other group of rows reads the cache.
@@ -714,7 +723,8 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
                 weight[w] = __builtin_amdgcn_exp2f(ml[w][r][0] - from);
                 total += ml[w][r][1] * weight[w];
             }
-            const int64_t part_row = ((int64_t)(run + p.b) * heads + head) * la.rows + row;
+            const int part = la.by_run ? part_of<true>(run, p.b, p.base >= run_begin) : part_of<false>(run, p.b, false);
+            const int64_t part_row = ((int64_t)part * heads + head) * la.rows + row;
             const int i = row / a.share;
             TQ *out = static_cast<TQ *>(a.out) +
                       (((int64_t)p.b * a.M + i) * heads + head) * a.share * D + (int64_t)(row % a.share) * D;
@@ -749,34 +759,40 @@ __global__ __launch_bounds__(kBlock, resident(D, kF8, kTiles)) void attend_kerne
     }
 }
 
-// Joins the parts of a row: kWavesRow waves (all four, or one where rows are
+// Joins the parts of a row of each sequence, or of each that the end of a run cuts first
+// where runs are no more than sequences (every row looks for its sequence among all
+// lengths: rows times sequences): kWavesRow waves (all four, or one where rows are
 // many: 3840 rows 9.8 us with four, 6.1 with one), 16-byte pieces of D in
 // consecutive lanes, the parts over the rest.
-template <typename TQ, int D, int kWavesRow>
+template <typename TQ, int D, int kWavesRow, bool kByRun>
 __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
 {
     constexpr int kPer = D / 4, kRows = 64 * kWavesRow / kPer, kThreads = 64 * kWavesRow;
     const AttendArgs &a = la.a;
     const int heads = a.cache.heads;
     const int number = blockIdx.x * (kBlock / kThreads) + (kWavesRow == 1 ? (int)threadIdx.x / 64 : 0);
-    if (number >= a.B * heads * la.rows)
+    if (number >= (kByRun ? la.target - 1 : a.B) * heads * la.rows)
         return;
     const int thread = threadIdx.x % kThreads;
     const int row = number % la.rows, head = (number / la.rows) % heads;
-    const int b = __builtin_amdgcn_readfirstlane(number / (la.rows * heads));
-    const Plan p = plan<false>(a, la.target, b);
+    const int unit = __builtin_amdgcn_readfirstlane(number / (la.rows * heads));
+    const Plan p = plan<kByRun>(a, la.target, kByRun ? unit + 1 : unit);   // what the run behind a cut goes on with
+    if (p.b < 0)
+        return;
+    const int b = p.b;
     const int from_run = p.base / p.run, n = (p.base + p.seq.tiles - 1) / p.run - from_run + 1;
-    if (n == 1)
+    if (n == 1 || (kByRun && from_run != unit))
         return;
     const Parts parts = parts_at(a.workspace, la.units, heads, la.rows, D);
     const int64_t stride = (int64_t)heads * la.rows;
-    const int64_t at0 = (int64_t)(from_run + b) * stride + (int64_t)head * la.rows + row;
+    const int64_t at0 = part_of<kByRun>(from_run, b, false) * stride + (int64_t)head * la.rows + row;
+    auto at_part = [&](int c) { return at0 + (kByRun ? 2 * c + (c == 0 ? 1 : 0) : c) * stride; };
     __shared__ float o[kWavesRow == 1 ? 1 : kRows][D], ml[2][kWaves];
     const int lane = thread % kPer, mine = thread / kPer;
     // the largest maximum and the sum under it: a part a thread
     float m = -__builtin_inff();
     for (int c = thread; c < n; c += kThreads)
-        m = fmaxf(m, parts.ml[2 * (at0 + c * stride)]);
+        m = fmaxf(m, parts.ml[2 * at_part(c)]);
     m = wave_max(m);
     if constexpr (kWavesRow > 1) {
         if ((threadIdx.x & 63) == 0)
@@ -787,7 +803,7 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
     const float from = m == -__builtin_inff() ? 0.0f : m;
     float total = 0.0f;
     for (int c = thread; c < n; c += kThreads) {
-        const int64_t at = at0 + c * stride;
+        const int64_t at = at_part(c);
         total += parts.ml[2 * at + 1] * __builtin_amdgcn_exp2f(parts.ml[2 * at] - from);
     }
     total = wave_sum(total);
@@ -795,7 +811,7 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
     if (mine < kRows) {
 #pragma unroll 8
         for (int c = mine; c < n; c += kRows) {
-            const int64_t at = at0 + c * stride;
+            const int64_t at = at_part(c);
             v += *reinterpret_cast<const f4_t *>(parts.o + at * D + 4 * lane) *
                  __builtin_amdgcn_exp2f(parts.ml[2 * at] - from);
         }
@@ -851,7 +867,7 @@ int tiles_of_rows(int rows) { return rows <= 16 ? 1 : 2; }
 struct Cut {
     int rows, tiles, row_groups, target;
     int64_t units;
-    bool by_sequence;
+    bool by_sequence, by_run;
 };
 
 Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page, int64_t width, int window)
@@ -865,7 +881,8 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
     const int64_t places = window ? std::min<int64_t>(width * page, (int64_t)window + M + 16) : width * page;
     const int64_t most = ceil_div(places, kTile);
     c.target = (int)std::min<int64_t>(c.target, B * most);
-    c.units = c.target + B;
+    c.by_run = c.target <= B;
+    c.units = std::min<int64_t>(2 * c.target, c.target + B);
     // A workgroup a sequence: no plan, no second launch (5 us), but the longest sequence is one workgroup's.  Measured
     // (us, runs / a sequence each; f8, D 128, 8 key heads, lengths from 0 to the table's): 1 sequence of 333 9.7 / 7.3,
     // of 1000 9.8 / 11.7 (with the host's part of a second launch 14.4 / 12.1), of 2000 10.2 / 19.0; 32 of up to 2000
@@ -894,9 +911,13 @@ hipError_t launch(const AttendLaunch &la, const Cut &c, hipStream_t stream)
                                        stream, la);
     if (e != hipSuccess || c.by_sequence)
         return e;
-    const int64_t rows = (int64_t)la.a.B * la.a.cache.heads * c.rows;
+    const int64_t rows = (int64_t)(c.by_run ? c.target - 1 : la.a.B) * la.a.cache.heads * c.rows;
+    if (rows == 0)
+        return e;
     const bool many = rows >= kManyRows;
-    void (*join)(AttendLaunch) = many ? &join_kernel<TQ, D, 1> : &join_kernel<TQ, D, kWaves>;
+    void (*join)(AttendLaunch) = many ? c.by_run ? &join_kernel<TQ, D, 1, true> : &join_kernel<TQ, D, 1, false>
+                                 : c.by_run ? &join_kernel<TQ, D, kWaves, true>
+                                            : &join_kernel<TQ, D, kWaves, false>;
     return launch_kernel(reinterpret_cast<const void *>(join),
                          dim3((unsigned)(many ? ceil_div(rows, kBlock / 64) : rows)), dim3(kBlock), 0, stream, la);
 }
@@ -927,7 +948,7 @@ hipError_t launch_attend(const AttendArgs &a, int q_type, hipStream_t stream)
                       a.window);
     if (!c.by_sequence && !a.workspace)
         return hipErrorInvalidValue;
-    const AttendLaunch la{a, c.target, (int)c.units, c.rows, c.row_groups, c.by_sequence, a.scale * kLog2e,
+    const AttendLaunch la{a, c.target, (int)c.units, c.rows, c.row_groups, c.by_sequence, c.by_run, a.scale * kLog2e,
                           a.softcap > 0.0f ? a.scale / a.softcap : 0.0f,
                           std::min(a.softcap * kLog2e, std::numeric_limits<float>::max())};
     if (a.cache.type == QG_F8)

@@ -128,3 +128,34 @@ def test_rows_of_a_key_head_around_the_tiles_at_256_dimensions(cache, M, share):
     q = "bfloat16" if cache == "f8" else cache
     for width in (None, 2500):
         _Batch([150, M, 37, 0], M, 2 * share, 2, 256, 16, cache, q, width=width).check()
+
+
+# -------------------------------------------- more sequences than portions of work
+FEW_RUNS = [  # sequences, longest, M, heads, key heads, D, cache, q
+    (50, 200, 2, 8, 8, 256, "float16", "float16"),       # 32 portions, a wave a row in the join
+    (60, 200, 1, 16, 16, 128, "f8", "bfloat16"),         # 48
+    (36, 100, 3, 64, 32, 64, "bfloat16", "bfloat16"),    # 32
+    (9, 300, 1, 96, 96, 256, "bfloat16", "bfloat16"),    # 2, four waves a row
+    (9, 300, 1, 120, 60, 192, "f8", "float16"),          # 8
+    (5, 200, 1, 300, 300, 64, "bfloat16", "bfloat16"),   # 3
+    (5, 100, 1, 600, 600, 128, "bfloat16", "bfloat16"),  # 1: nothing to join
+    (20, 130, 16, 32, 8, 128, "float16", "float16"),     # 64 rows a key head, 16
+]
+
+
+@pytest.mark.parametrize("case", FEW_RUNS)
+@pytest.mark.parametrize("window", [0, 150])
+def test_more_sequences_than_portions_of_work(case, window):
+    """Portions that hold many sequences, sequences that take several portions, cuts between two and inside one."""
+    count, longest, M, H, KV, D, cache, q = case
+    rng = np.random.default_rng([count, D, KV])
+    lens = [int(n) for n in rng.integers(0, longest, count)]
+    lens[1], lens[2], lens[3], lens[-1] = 6 * longest, 0, 128, 256
+    _Batch(lens, M, H, KV, D, 64, cache, q, width=40000 // 64).check(window=window)
+
+
+def test_sequences_by_the_thousand_under_a_wide_table():
+    b = _Batch([int(n) for n in np.random.default_rng(0).integers(0, 4, 3000)], 1, 2, 2, 64, 16, "f8", "bfloat16",
+               width=3000)
+    y = _np(b.check())
+    assert all(y[i].any() for i, n in enumerate(b.lens) if n)
