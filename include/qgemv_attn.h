@@ -120,10 +120,15 @@ qg_status qkv_norm_rope_write(const void *q, int64_t ldq, int q_heads, const voi
  *   out = sum softmax(s) v          [B][M][q_heads][dim], q_type, contiguous.
  * A query that sees no token gets zeros.  lens are held to 0 .. width * page;
  * a table entry outside 0 .. pages - 1 holds no tokens.  What lies in places
- * that a query does not see, NaN or infinity, does not reach it.  Products are
- * exact with fp32 sums (8-bit keys beside bf16 queries down to multiples of
- * 2^-133); the softmax's weights enter the second product as two
- * 16-bit parts (2^-16 of a weight is lost); one rounding to q_type.
+ * that a query does not see, NaN or infinity, does not reach it; a value that
+ * is not finite makes its element of every query that sees it not finite,
+ * infinity or NaN.  Products are exact with fp32 sums (8-bit keys beside bf16
+ * queries down to multiples of 2^-133); the softmax's weights enter the second
+ * product as two 16-bit parts (2^-16 of a weight is lost); one rounding to
+ * q_type.  Weights reach 2^4 and are divided by their sum at the end: the values
+ * that a query sees may sum up, in magnitude, to 2^123.  An 8-bit value's scale
+ * enters its weight, in multiples of 2^-133: values of 2^-100 keep 2^-23 of the
+ * largest.
  * workspace: qattn_decode_workspace bytes (0: may be NULL; at most 33 MiB,
  * however many sequences there are), 16-byte aligned, used by this call only. */
 size_t qattn_decode_workspace(int64_t B, int M, int q_heads, int kv_heads, int dim, int cache_type, int page,

@@ -159,3 +159,37 @@ def test_sequences_by_the_thousand_under_a_wide_table():
                width=3000)
     y = _np(b.check())
     assert all(y[i].any() for i, n in enumerate(b.lens) if n)
+
+
+# --------------------------------------------------- values at the ends of the range
+@pytest.mark.parametrize("cache,q", [("f8", "bfloat16"), ("bfloat16", "bfloat16")])
+@pytest.mark.parametrize("exponent", [110, 60, -60, -100])
+@pytest.mark.parametrize("M,D", [(1, 128), (3, 64), (2, 256)])
+def test_values_of_every_size(cache, q, exponent, M, D):
+    """300 values of about 2^110, at most 2^115, sum up to some 2^119 in magnitude, and 2^123 may be.  At 2^-100 an 8-bit
+    value's scale is 2^-108 or so, and its weight a multiple of 2^-133: half of that is 2^-25 of the largest at most."""
+    b = _Batch([300, 41, 0], M, 4, 2, D, 16, cache, q)
+    b.v = au.held(b.v * 2.0 ** exponent, cache)[0]
+    assert np.abs(b.v).max() < 2.0 ** (exponent + 5)
+    b.data = au.pack(b.k, b.v, 16, cache)
+    y = b.run()
+    out, bound = b.reference()
+    lost = 300 * 2.0 ** -25 * np.abs(b.v).max() if cache == "f8" and exponent == -100 else 0.0
+    au.assert_attend(_np(y), out, bound + lost, q, f"values of 2^{exponent}")
+
+
+@pytest.mark.parametrize("cache", ["bfloat16", "float16"])
+@pytest.mark.parametrize("M", [1, 3])
+def test_a_value_that_is_not_finite_reaches_who_sees_it(cache, M):
+    """At the end of a sequence and in its middle, and no other element or sequence."""
+    for place in (199, 70):
+        b = _Batch([200, 180], M, 4, 2, 128, 16, cache, cache)
+        ref, bound = b.reference()
+        page, t = divmod(int(b.table[0, place // 16] * 16 + place % 16), 16)
+        word = {"bfloat16": 0xFF80, "float16": 0xFC00}[cache]
+        b.data[page, :2 * 2 * 16 * 128 * 2].view(np.uint16).reshape(2, 2, 16, 128)[1, 1, t, 77] = word   # -infinity
+        got = _np(b.run())
+        touched = np.zeros(ref.shape, bool)
+        touched[0, M - 1 if place == 199 else slice(None), 2:, 77] = True
+        assert np.array_equal(~np.isfinite(got), touched)
+        au.assert_attend(np.where(touched, 0, got), np.where(touched, 0, ref), bound, cache, "others")
