@@ -856,13 +856,15 @@ __global__ __launch_bounds__(kBlock) void join_kernel(AttendLaunch la)
 // Tiles of 16 rows a workgroup takes: one or two, more rows in groups that read the
 // cache each.  (Four tiles, one wave a SIMD, at 128 dimensions, the cache in part in the
 // last-level one: 64 rows a key head in f8 74 us for 56, 128 rows 109 for 85; in bf16 74
-// for 55, 106 for 91.)  Two at 256 dimensions in 16 bits too, though 37 registers spill
-// there: half the groups read the cache.  One tile / two (us, bf16, rows a key head): 16
-// sequences of up to 8000, 8 key heads: 20 rows 115 / 118, 36 157 / 149, 64 191 / 157, 256
-// 590 / 384; 8 of 20000, 1 head: 37 / 41, 48 / 49, 57 / 50, 110 / 112; 4 of 30000, 8 heads:
-// 114 / 115, 157 / 139, 183 / 142, 609 / 355; 1 of 100000, 2 heads: 69 / 59, 98 / 77,
-// 127 / 78, 247 / 150; 64 of 1500, 4 heads: 91 / 84, 125 / 153, 151 / 159, 400 / 380.
-int tiles_of_rows(int rows) { return rows <= 16 ? 1 : 2; }
+// for 55, 106 for 91.)  Two spill 37 registers at 256 dimensions in 16 bits: there one up
+// to 48 rows, where two save one group's reading of the cache at most.  One tile / two (us,
+// bf16, 20, 48, 64, 96 and 256 rows a key head): 16 sequences of up to 8000, 8 key heads 111 /
+// 126, 152 / 155, 178 / 164, 265 / 204, 575 / 380; 8 of 20000, 1 head 36 / 50, 47 / 64, 54 /
+// 65, 77 / 75, 110 / 122; 4 of 30000, 8 heads 114 / 125, 159 / 149, 186 / 154, 276 / 190, 610 /
+// 364; 64 of 1500, 4 heads 66 / 92, 86 / 124, 108 / 128, 148 / 150, 324 / 292; 1 of 100000,
+// 2 heads 69 / 63, 95 / 82, 121 / 83, 120 / 110, 249 / 157.
+constexpr bool spills(int D, bool f8) { return D == 256 && !f8; }
+int tiles_of_rows(int rows, int D, bool f8) { return rows <= (spills(D, f8) ? 48 : 16) ? 1 : 2; }
 
 struct Cut {
     int rows, tiles, row_groups, target;
@@ -874,7 +876,7 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
 {
     Cut c;
     c.rows = M * (q_heads / kv_heads);
-    c.tiles = tiles_of_rows(c.rows);
+    c.tiles = tiles_of_rows(c.rows, dim, f8);
     c.row_groups = (c.rows + 16 * c.tiles - 1) / (16 * c.tiles);
     c.target = std::max(1, kRounds * kUnits * resident(dim, f8, c.tiles) / (kv_heads * c.row_groups));
     // no sequence has more tiles than this: no more runs than tiles
@@ -903,9 +905,15 @@ Cut cut(int64_t B, int M, int q_heads, int kv_heads, int dim, bool f8, int page,
 template <typename TQ, bool kF8, int D>
 hipError_t launch(const AttendLaunch &la, const Cut &c, hipStream_t stream)
 {
-    void (*fn)(AttendLaunch) = c.row_groups > 1 ? &attend_kernel<TQ, kF8, D, 2, false>
-                               : c.tiles == 1   ? &attend_kernel<TQ, kF8, D, 1, true>
-                                                : &attend_kernel<TQ, kF8, D, 2, true>;
+    void (*fn)(AttendLaunch);
+    if constexpr (spills(D, kF8))   // (two tiles are always groups there)
+        fn = c.row_groups == 1 ? &attend_kernel<TQ, kF8, D, 1, true>
+             : c.tiles == 1    ? &attend_kernel<TQ, kF8, D, 1, false>
+                               : &attend_kernel<TQ, kF8, D, 2, false>;
+    else
+        fn = c.row_groups > 1 ? &attend_kernel<TQ, kF8, D, 2, false>
+             : c.tiles == 1   ? &attend_kernel<TQ, kF8, D, 1, true>
+                              : &attend_kernel<TQ, kF8, D, 2, true>;
     const hipError_t e = launch_kernel(reinterpret_cast<const void *>(fn),
                                        dim3((unsigned)(c.target * la.a.cache.heads * c.row_groups)), dim3(kBlock), 0,
                                        stream, la);
