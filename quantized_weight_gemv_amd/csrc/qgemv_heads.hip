@@ -9,11 +9,15 @@
 // cosines and sines of a lane are the same for every head of a token: a wave
 // takes them once and walks over the heads.
 //
-// Bound by bytes from a few thousand tokens on: 16384 tokens of 32 + 8 heads of 128
-// in bf16 forward 64 us (5.2 TB/s), backward 89 (5.7) and 5 for the sums of the
-// gains; 8192 tokens of 40 + 8 + 8 heads into a 16-bit cache 49 us (4.8); 16384
-// tokens of 8 heads into an 8-bit cache 19 us (5.2), back 17 (5.8).  A few tokens
-// take 4 us: a launch, the loads' latency and the series.
+// Bound by bytes from some ten thousand tokens on: 16384 tokens of 32 + 8 heads of 128
+// in bf16 forward 66 us (5.1 TB/s), backward 89 (5.6) and 5 for the sums of the
+// gains, in fp32 124 (5.4) and 187 (5.4); 8192 tokens of 40 + 8 + 8 heads into a 16-bit
+// cache 48 us (4.9), with norms into an 8-bit one 58 (3.8: the keys in 64 bits take 127
+// registers and more, and three waves a SIMD); 16384 tokens of 8 heads into an 8-bit cache 19
+// us (5.2), back 18 (5.7).  Some thousand tokens are bound by the vector units: 2731 of 14
+// + 2 heads of 96 on three axes 12 us forward for 3.3 us of bytes, since every group of lanes
+// of a wave, and the token's other wave, computes the same cosines in 64 bits.  A few
+// tokens take 4 us: a launch, the loads' latency and the series.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
