@@ -24,8 +24,9 @@
  * position: the angle's whole turns are taken out exactly to 2^-53 of a turn
  * (up to 2^51 turns), whatever their number.
  * freq: fp32 [rot / 2]; gains: type gain_type [D].
- * Everything is computed in fp32 and rounded once.  The gradient of a row
- * needs nothing of the forward pass but its inputs.
+ * Everything is computed in fp32 and rounded once (the squares of a row sum up
+ * to less than 2^128).  The gradient of a row needs nothing of the forward pass
+ * but its inputs.
  *
  * Cache.  `pages` pages of qkv_page_bytes(page, heads, dim, type) bytes, each
  * holding `page` tokens of every key head, page 16, 32, ... 1024 (a power of

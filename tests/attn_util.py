@@ -66,8 +66,8 @@ def norm_rope_gradient(x, dy, gain, eps, cos, sin, rot, interleaved):
 
 
 # roundings of norm and rotation in fp32, relative to |a| + |b| of a pair: the sum of squares (16 additions at
-# most, halved by the root), the root (2 steps), two products, cosine and sine (2 steps of 1, and an angle of up
-# to pi turned in fp32: pi / 2 steps), a product and a sum: under 16 steps of 2^-24
+# most, halved by the root), the root (2 steps), two products, cosine and sine (a step of 1: they and their angle
+# are taken in 64 bits), a product and a sum: under 16 steps of 2^-24
 HEADS = 16 * 2.0 ** -24
 
 
